@@ -80,6 +80,20 @@ class LayerBuffers:
         eaga.backward(self.dims, self.X, self.E, self.y, self.M, self.W, self.saved, self.dXout, self.dEout,
                       self.dX, self.dE, self.dy, self.dW, self.ws_bwd, stream, variant=variant)
 
+    def optimizer(self, **kwargs):
+        """An AdamW over this layer's weights and their gradients (optim.AdamW's
+        arguments); biases do not decay unless weight_decay says so."""
+        if not self.has_backward:
+            raise ValueError("optimizer: the buffers were made without a backward")
+        return self._optimizer([(self.W[k], self.dW[k]) for k in WEIGHT_NAMES], **kwargs)
+
+    @staticmethod
+    def _optimizer(pairs, weight_decay=0.01, **kwargs):
+        from .optim import AdamW
+        if not hasattr(weight_decay, "__len__"):
+            weight_decay = [weight_decay if w.dim() > 1 else 0.0 for w, _ in pairs]
+        return AdamW([w for w, _ in pairs], [g for _, g in pairs], weight_decay=weight_decay, **kwargs)
+
     def attention_map(self, stream=None):
         B, n, H = self.shape["B"], self.shape["n"], self.shape["H"]
         A = torch.empty(B * H * n * n + 2 * B * H, dtype=torch.float32, device=self.device)
@@ -141,6 +155,13 @@ class BlockBuffers(LayerBuffers):
             self.Wb[k].copy_(host_to_storage_tensor(block_weights[k], self.dtype))
         if dyout is not None and self.has_backward:
             self.dyout.copy_(host_to_storage_tensor(dyout, self.dtype))
+
+    def optimizer(self, **kwargs):
+        """An AdamW over the layer's and the block's weights (optim.AdamW's arguments)."""
+        if not self.has_backward:
+            raise ValueError("optimizer: the buffers were made without a backward")
+        return self._optimizer([(self.W[k], self.dW[k]) for k in WEIGHT_NAMES]
+                               + [(self.Wb[k], self.dWb[k]) for k in eaga.BLOCK_WEIGHT_NAMES], **kwargs)
 
     def block_forward(self, stream=None):
         eaga.block_forward(self.dims, self.X, self.E, self.y, self.M, self.W, self.Wb, self.Xmid, self.Emid,

@@ -24,12 +24,16 @@ EXPORTED = ("eaga_workspace_size", "eaga_saved_size", "eaga_forward", "eaga_back
             "eaga_set_profile_events", "eaga_kernel_launches", "eaga_forward_noalloc", "eaga_debug_wait_probe",
             "eaga_forward_variant", "eaga_backward_variant", "eaga_forward_rows", "eaga_backward_rows",
             "eaga_block_saved_size", "eaga_block_workspace_size", "eaga_block_kernel_launches",
-            "eaga_block_forward", "eaga_block_backward")
+            "eaga_block_forward", "eaga_block_backward",
+            "eaga_residual_norm_workspace_size", "eaga_residual_norm_forward", "eaga_residual_norm_backward",
+            "eaga_adamw_step", "eaga_adamw_unpack")
 # parameters of the graph-transformer block (eaga_block_weights field order)
 BLOCK_SUB_PARAMS = ("ln1_g", "ln1_s", "W1", "b1", "W2", "b2", "ln2_g", "ln2_s")
 BLOCK_WEIGHT_NAMES = tuple(f"{s}_{k}" for s in ("x", "e", "y") for k in BLOCK_SUB_PARAMS) + ("Wyx", "Wye", "by")
 # layer variants (eaga_variant): the layer, Light Edge, the unnormalised edge update
 VARIANTS = {"layer": 0, "light_edge": 1, "unnormalised": 2}
+# norms of the residual step (eaga_norm)
+NORMS = {"none": 0, "layer": 1, "rms": 2}
 
 
 class Dims(ctypes.Structure):
@@ -42,6 +46,22 @@ class Weights(ctypes.Structure):
 
 class BlockWeights(ctypes.Structure):
     _fields_ = [(k, ctypes.c_void_p) for k in BLOCK_WEIGHT_NAMES]
+
+
+class ResidualNormDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_longlong), ("rows_per_group", ctypes.c_longlong), ("w", ctypes.c_int),
+                ("pre", ctypes.c_int), ("post", ctypes.c_int), ("eps", ctypes.c_float), ("alpha", ctypes.c_float),
+                ("dtype", ctypes.c_int)]
+
+
+class AdamwConfig(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_double) for k in ("lr", "beta1", "beta2", "eps", "grad_scale")] + \
+               [(k, ctypes.c_int) for k in ("param_dtype", "grad_dtype", "state_bits")] + [("seed", ctypes.c_uint)]
+
+
+class AdamwTensor(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in ("p", "master", "g", "m", "v", "m_scale", "v_scale")] + \
+               [("n", ctypes.c_longlong), ("counter", ctypes.c_ulonglong), ("weight_decay", ctypes.c_float)]
 
 
 class EagaError(RuntimeError):
@@ -110,6 +130,17 @@ def lib():
         L.eaga_block_backward.argtypes = [ctypes.POINTER(Dims), vp, vp, vp, vp, W_, BW_, vp, vp, vp, vp, vp, vp,
                                           vp, vp, vp, vp, W_, BW_, vp, sz, vp]
         L.eaga_block_backward.restype = i32
+        ND_ = ctypes.POINTER(ResidualNormDims)
+        L.eaga_residual_norm_workspace_size.argtypes = [ND_]
+        L.eaga_residual_norm_workspace_size.restype = sz
+        L.eaga_residual_norm_forward.argtypes = [ND_] + [vp] * 11
+        L.eaga_residual_norm_forward.restype = i32
+        L.eaga_residual_norm_backward.argtypes = [ND_] + [vp] * 17 + [sz, vp]
+        L.eaga_residual_norm_backward.restype = i32
+        L.eaga_adamw_step.argtypes = [ctypes.POINTER(AdamwConfig), ctypes.POINTER(AdamwTensor), i32, vp, vp, vp]
+        L.eaga_adamw_step.restype = i32
+        L.eaga_adamw_unpack.argtypes = [ctypes.POINTER(AdamwTensor), i32, vp]
+        L.eaga_adamw_unpack.restype = i32
         L.eaga_strerror.argtypes = [i32]
         L.eaga_strerror.restype = ctypes.c_char_p
         _lib = L
@@ -324,3 +355,98 @@ def block_backward(d: Dims, X, E, y, M, W: dict, Wb: dict, Xmid, Emid, saved, dX
         ctypes.byref(_weights(dW, _f32(), "dW")), ctypes.byref(_block_weights(dWb, _f32(), "dWb")),
         _p(workspace, "workspace"), _nbytes(workspace), _stream(stream))
     _check(rc, "eaga_block_backward")
+
+
+# ---------------------------------------------------------------- operators around the block
+
+class _Checked:
+    """Data pointers of one call's tensors: each a contiguous CUDA tensor on the
+    current device, of the dtype and the number of elements that the call's
+    dims give it (the kernels go by the dims alone)."""
+
+    def __init__(self):
+        import torch
+        self.dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+
+    def __call__(self, t, name, dtype, numel, optional=False):
+        if t is None:
+            if optional:
+                return None
+            raise ValueError(f"{name}: a tensor is required")
+        if not t.is_cuda:
+            raise ValueError(f"{name}: a CUDA tensor is required (got {t.device})")
+        if t.get_device() != self.dev:
+            raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{self.dev}")
+        if t.dtype != dtype:
+            raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+        if t.numel() != numel:
+            raise ValueError(f"{name}: {t.numel()} elements, expected {numel}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: must be contiguous")
+        return t.data_ptr()
+
+    def workspace(self, t):
+        return self(t, "workspace", _u8(), -1 if t is None else t.numel())
+
+
+def _code(name, names, what):
+    if name not in names:
+        raise ValueError(f"{what}: {name!r}, expected one of {', '.join(names)}")
+    return names[name]
+
+
+def residual_norm_dims(rows, w, pre="layer", post="none", rows_per_group=None, eps=1e-5, alpha=1.0,
+                       dtype="bf16") -> ResidualNormDims:
+    """rows_per_group: rows that share a row of the gate (None: one group)."""
+    return ResidualNormDims(rows, max(1, rows) if rows_per_group is None else rows_per_group, w,
+                            _code(pre, NORMS, "pre"), _code(post, NORMS, "post"), eps, alpha,
+                            EAGA_BF16 if dtype == "bf16" else EAGA_FP32 if dtype == "fp32" else dtype)
+
+
+def residual_norm_workspace_size(d: ResidualNormDims) -> int:
+    """Bytes of the backward's workspace (the forward needs none)."""
+    return int(lib().eaga_residual_norm_workspace_size(ctypes.byref(d)))
+
+
+def _groups(d: ResidualNormDims) -> int:
+    return d.rows // d.rows_per_group if d.rows_per_group > 0 else 0
+
+
+def residual_norm_forward(d: ResidualNormDims, x, u, M, gate, post_g, post_s, pre_g, pre_s, r, h, stream=None):
+    """eaga_residual_norm_forward: r = alpha x + gate * post(u), h = pre(r)."""
+    p, sd, n, w = _Checked(), _storage(d), d.rows * d.w, d.w
+    rc = lib().eaga_residual_norm_forward(
+        ctypes.byref(d), p(x, "x", sd, n, True), p(u, "u", sd, n), p(M, "M", _u8(), d.rows, True),
+        p(gate, "gate", sd, _groups(d) * w, True), p(post_g, "post_g", sd, w, True), p(post_s, "post_s", sd, w, True),
+        p(pre_g, "pre_g", sd, w, True), p(pre_s, "pre_s", sd, w, True), p(r, "r", sd, n, True),
+        p(h, "h", sd, n, True), _stream(stream))
+    _check(rc, "eaga_residual_norm_forward")
+
+
+def residual_norm_backward(d: ResidualNormDims, r, u, M, gate, post_g, post_s, pre_g, dr, dh, dx, du, dgate, dpost_g,
+                           dpost_s, dpre_g, dpre_s, workspace, stream=None):
+    """eaga_residual_norm_backward."""
+    p, sd, f, n, w = _Checked(), _storage(d), _f32(), d.rows * d.w, d.w
+    ng = _groups(d) * w
+    rc = lib().eaga_residual_norm_backward(
+        ctypes.byref(d), p(r, "r", sd, n, True), p(u, "u", sd, n, True), p(M, "M", _u8(), d.rows, True),
+        p(gate, "gate", sd, ng, True), p(post_g, "post_g", sd, w, True), p(post_s, "post_s", sd, w, True),
+        p(pre_g, "pre_g", sd, w, True), p(dr, "dr", sd, n, True), p(dh, "dh", sd, n, True), p(dx, "dx", sd, n, True),
+        p(du, "du", sd, n, True), p(dgate, "dgate", sd, ng, True), p(dpost_g, "dpost_g", f, w, True),
+        p(dpost_s, "dpost_s", f, w, True), p(dpre_g, "dpre_g", f, w, True), p(dpre_s, "dpre_s", f, w, True),
+        p.workspace(workspace), _nbytes(workspace), _stream(stream))
+    _check(rc, "eaga_residual_norm_backward")
+
+
+def adamw_step(config: AdamwConfig, tensors, count: int, state, lr=None, stream=None):
+    """eaga_adamw_step over a ctypes array of AdamwTensor (optim.AdamW makes and keeps one)."""
+    p = _Checked()
+    import torch
+    rc = lib().eaga_adamw_step(ctypes.byref(config), tensors, int(count), p(state, "state", torch.int64, 2),
+                               p(lr, "lr", _f32(), 1, True), _stream(stream))
+    _check(rc, "eaga_adamw_step")
+
+
+def adamw_unpack(tensors, count: int, stream=None):
+    """eaga_adamw_unpack."""
+    _check(lib().eaga_adamw_unpack(tensors, int(count), _stream(stream)), "eaga_adamw_unpack")

@@ -368,6 +368,102 @@ EAGA_API eaga_status eaga_block_backward(const eaga_dims *dims,
                                  void *dX, void *dE, void *dy, const eaga_weight_grads *dW,
                                  const eaga_block_grads *dWb, void *workspace, size_t ws_bytes, void *stream);
 
+/* ---------------------------------------------------------------------
+ * The residual step between two sub-layers, with the norm after the one and
+ * before the other, a gate and a residual scale.  Per row, with x the residual
+ * stream, u the sub-layer's output and M the row mask:
+ *
+ *   p = post(u)     r = alpha x + gate * p     h = pre(r)      (masked rows: r = h = 0)
+ *   layer norm: gain * (z - mean) / sqrt(var + eps) + shift, over the last axis, biased variance
+ *   rms norm:   gain * z / sqrt(mean(z^2) + eps) + shift
+ *
+ * gate [rows / rows_per_group, w] holds one row per group of consecutive rows
+ * (the graphs of a padded batch: rows_per_group = n for nodes, n*n for pairs, 1
+ * for global features).  Nullable: x (absent: r = gate * p), M (all rows real),
+ * gate (1), each gain (1) and shift (0), r (not written, where h is).  h is
+ * given exactly where pre is not EAGA_NORM_NONE.  A norm alone is u = its
+ * input, x = gate = r = NULL.  Masked rows are not read: they may hold
+ * anything, NaN included.  The pre-norm takes r before it is rounded to the
+ * storage dtype.
+ *
+ * Backward: r is the forward's, dr the gradient at r from elsewhere (nullable:
+ * 0), dh that at h.  Writes, where the pointer is given, dx, du [rows, w] and
+ * dgate in the storage dtype and the gains' and shifts' gradients [w] in fp32.
+ * Masked rows' dx and du are 0.  All sums in a fixed order.
+ *
+ * Limits: w <= 8192 (any w; multiples of 16 bytes are the fast ones), rows
+ * <= 2147418112 and a multiple of rows_per_group; eps > 0.  rows = 0 is a
+ * call that writes no row (and zero parameter gradients). */
+typedef enum { EAGA_NORM_NONE = 0, EAGA_NORM_LAYER = 1, EAGA_NORM_RMS = 2 } eaga_norm;
+typedef struct {
+    long long rows, rows_per_group;
+    int w;
+    int pre, post;              /* eaga_norm */
+    float eps, alpha;
+    int dtype;                  /* eaga_dtype */
+} eaga_residual_norm_dims;
+
+/* Bytes of workspace of the backward; 0 for invalid or unsupported dims.  The
+ * forward needs none. */
+EAGA_API size_t eaga_residual_norm_workspace_size(const eaga_residual_norm_dims *dims);
+EAGA_API eaga_status eaga_residual_norm_forward(const eaga_residual_norm_dims *dims,
+                                const void *x, const void *u, const uint8_t *M, const void *gate,
+                                const void *post_g, const void *post_s, const void *pre_g, const void *pre_s,
+                                void *r, void *h, void *stream);
+EAGA_API eaga_status eaga_residual_norm_backward(const eaga_residual_norm_dims *dims,
+                                const void *r, const void *u, const uint8_t *M, const void *gate,
+                                const void *post_g, const void *post_s, const void *pre_g,
+                                const void *dr, const void *dh, void *dx, void *du, void *dgate,
+                                float *dpost_g, float *dpost_s, float *dpre_g, float *dpre_s,
+                                void *workspace, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------
+ * One AdamW step over many tensors: what turns the fp32 weight gradients of
+ * the layer, the block and the products above into new weights.  With t the
+ * step being taken, per element, every operation rounded to fp32:
+ *
+ *   g  = grad_scale * grad
+ *   m' = beta1 m + (1 - beta1) g          v' = beta2 v + (1 - beta2) g^2
+ *   p' = (1 - lr wd) p - (lr / (1 - beta1^t)) m' / (sqrt(v') / sqrt(1 - beta2^t) + eps)
+ *
+ * p is the fp32 master copy where there is one (bf16 weights only, for every
+ * tensor or for none; the weight then receives p' rounded), else the weight.
+ * state_bits = 32: m, v fp32 [n].  state_bits = 8: m, v one byte an element, in
+ * blocks of 256 elements that share a scale (m_scale, v_scale: fp32, one per
+ * block, ceil(n/256)); the codes are 8-bit floats of m and of sqrt(v) over the
+ * scale, rounded at random by a hash of seed, t and counter + i (i: the
+ * element's index in its tensor; give tensors distinct ranges of counter), so a
+ * step is reproducible.  All-zero states, scales included, are the start.  A
+ * NaN or infinity in a gradient reaches the whole block's states and shows there.
+ *
+ * `state` is 16 bytes of device memory, zero before the first step (or the
+ * number of steps taken, as int64, then zero): the step counts there, so that a
+ * captured call counts its replays.  `lr` (nullable) is a device float that
+ * replaces config.lr, for schedules under replay.  Weights, masters and states
+ * are updated in place; no two written buffers may overlap, nor one with a
+ * gradient.  Calls on the same state or tensors must be ordered by the caller. */
+typedef struct {
+    double lr, beta1, beta2, eps, grad_scale;
+    int param_dtype, grad_dtype;         /* eaga_dtype */
+    int state_bits;                      /* 8 or 32 */
+    unsigned seed;
+} eaga_adamw_config;
+typedef struct {
+    void *p;                             /* weights, param_dtype */
+    float *master;                       /* nullable */
+    const void *g;                       /* gradients, grad_dtype */
+    void *m, *v;
+    float *m_scale, *v_scale;            /* state_bits = 8 only; 4-byte aligned */
+    long long n;                         /* elements; 0: skipped */
+    unsigned long long counter;
+    float weight_decay;
+} eaga_adamw_tensor;
+EAGA_API eaga_status eaga_adamw_step(const eaga_adamw_config *config, const eaga_adamw_tensor *tensors, int count,
+                                     void *state, const float *lr, void *stream);
+/* The 8-bit states of `tensors` (m, v, m_scale, v_scale, n) as fp32 values m
+ * and v, into p and master of each entry (either nullable). */
+EAGA_API eaga_status eaga_adamw_unpack(const eaga_adamw_tensor *tensors, int count, void *stream);
+
 EAGA_API const char *eaga_strerror(eaga_status s);
 
 #ifdef __cplusplus

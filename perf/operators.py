@@ -421,7 +421,7 @@ def _plan(s, op, c):
                          counters=s["at"], seed=s["seed"], step=c["step"])
         if c["bits"] == 8:
             s["m32"], s["v32"] = torch.zeros(s["p"].numel(), device=DEV), torch.zeros(s["p"].numel(), device=DEV)
-            s["m32_parts"], s["v32_parts"] = part(s["m32"]), part(s["v32"])
+            s["unpack"] = s["opt"].unpacker(part(s["m32"]), part(s["v32"]))
 
 
 def _call(s, c):
@@ -444,7 +444,7 @@ def _call(s, c):
     s["opt"].step()
     out = some("p", "master", "m", "v")
     if c["bits"] == 8:  # the states as the values that they stand for
-        s["opt"].unpack(s["m32_parts"], s["v32_parts"])
+        s["unpack"]()
         out.update(m=s["m32"], v=s["v32"])
     return out
 

@@ -1,0 +1,272 @@
+// The linear operator for up to eight rows (serving: one token, one graph's
+// global features).  Bound: the read of W, and in the backward the write of dW;
+// there is nothing for the tensor cores to do, so each weight goes from memory
+// to registers once and is multiplied by all rows there.
+//
+// Forward: a CTA takes 128 bytes of columns of W and a part of its rows; the
+// parts of one column tile are a cluster, whose first CTA adds the others'
+// sums out of their shared memory (in order) and does the epilogue: one launch,
+// no workspace.  Backward: a warp takes a row of W, the same row of dW and one
+// column of dX, with dZ (all rows) in shared memory.
+#include <algorithm>
+#include "ops_linear.h"
+#include "sm100.cuh"
+
+namespace eaga {
+namespace ops {
+
+using namespace sm100;
+
+template <typename T, int VEC>
+__device__ __forceinline__ void vec_load(const T *p, float (&v)[VEC]) {
+    if constexpr (VEC == 1) {
+        v[0] = ldf(p);
+    } else if constexpr (VEC == 4) {
+        const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    } else {
+        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p));
+        const unsigned x[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = __uint_as_float(x[j] << 16);
+            v[2 * j + 1] = __uint_as_float(x[j] & 0xffff0000u);
+        }
+    }
+}
+
+constexpr int LV_CHUNK = 512;      // rows of W whose X is in shared memory at once
+
+// R: rows (the call's, rounded up).  part: rows of W a CTA takes.
+template <typename T, int VEC, int R>
+__global__ void __launch_bounds__(256)
+k_lin_vec_fwd(const LinVec<T> p, const LinEpi<T> e, int part, int cluster) {
+    constexpr int LANES = VEC == 1 ? 32 : 8, C = LANES * VEC, KR = 256 / LANES;
+    __shared__ float xs[R][LV_CHUNK];
+    __shared__ float red[8][R][C];
+    __shared__ float sum[R][C];
+    const int tid = threadIdx.x, cl = tid % LANES, kr = tid / LANES, warp = tid >> 5, lane = tid & 31;
+    const int rank = blockIdx.x % cluster, c0 = blockIdx.x / cluster * C;
+    const int k0 = rank * part, k1 = min(p.in, k0 + part);
+    const int col = c0 + cl * VEC;
+    const bool on = col < p.out;
+    if (blockIdx.x == 0 && tid == 0) *p.status = 0;
+    float acc[R][VEC];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) acc[r][j] = 0.f;
+    for (int kb = k0; kb < k1; kb += LV_CHUNK) {
+        const int n = min(LV_CHUNK, k1 - kb);
+        __syncthreads();
+        for (int i = tid; i < R * LV_CHUNK; i += 256) {
+            const int r = i / LV_CHUNK, k = i % LV_CHUNK;
+            xs[r][k] = r < p.rows && k < n ? ldf(p.X + (size_t)r * p.in + kb + k) : 0.f;
+        }
+        __syncthreads();
+        if (on) {
+            const T *w = p.W + (size_t)kb * p.out + col;
+#pragma unroll 8
+            for (int k = kr; k < n; k += KR) {
+                float v[VEC];
+                vec_load<T, VEC>(w + (size_t)k * p.out, v);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float x = xs[r][k];
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) acc[r][j] += x * v[j];
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            float s = acc[r][j];
+            if (LANES < 32) {
+                s += __shfl_xor_sync(0xffffffffu, s, 8);
+                s += __shfl_xor_sync(0xffffffffu, s, 16);
+            }
+            if (lane < LANES) red[warp][r][cl * VEC + j] = s;
+        }
+    __syncthreads();
+    for (int i = tid; i < R * C; i += 256) {
+        float s = 0.f;
+#pragma unroll
+        for (int v = 0; v < 8; ++v) s += red[v][i / C][i % C];
+        sum[i / C][i % C] = s;
+    }
+    __syncthreads();
+    if (cluster > 1) cluster_sync_all();
+    if (rank == 0) {
+        for (int i = tid; i < p.rows * C; i += 256) {
+            const int r = i / C, c = c0 + i % C;
+            if (c >= p.out) continue;
+            float z = sum[r][i % C];
+            const uint32_t local = smem_u32(&sum[r][i % C]);
+            for (int q = 1; q < cluster; ++q) {
+                float v;
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_map(local, q)) : "memory");
+                z += v;
+            }
+            if (e.bias) z += ldf(e.bias + c);
+            const size_t at = (size_t)r * p.out + c;
+            if (e.out2) stf(e.out2 + at, z);
+            float y[1] = {z};
+            act_apply(y, e.act);
+            if (e.add) y[0] += ldf(e.add + at);
+            stf(e.out + at, y[0]);
+        }
+    }
+    __syncthreads();
+    if (cluster > 1) cluster_sync_all();       // shared memory stays until the first CTA has read it
+}
+
+template <typename T, int VEC, int R>
+__global__ void __launch_bounds__(256)
+k_lin_vec_bwd(const LinVec<T> p, const LinEpi<T> e) {
+    constexpr int CC = 8192 / R;               // columns of dZ at once
+    __shared__ __align__(16) float dz[R][CC];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int i = blockIdx.x * 8 + warp;
+    const bool on = i < p.in;
+    if (blockIdx.x == 0 && tid == 0) *p.status = 0;
+    float x[R], acc[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        x[r] = on && p.dW && r < p.rows ? ldf(p.X + (size_t)r * p.in + i) : 0.f;
+        acc[r] = 0.f;
+    }
+    for (int c0 = 0; c0 < p.out; c0 += CC) {
+        const int n = min(CC, p.out - c0);
+        __syncthreads();
+        for (int q = tid; q < R * n; q += 256) {
+            const int r = q / n, c = q % n;
+            float d[1] = {0.f};
+            if (r < p.rows) {
+                const size_t at = (size_t)r * p.out + c0 + c;
+                d[0] = ldf(p.dY + at);
+                if (p.Z) {
+                    const float z[1] = {ldf(p.Z + at)};
+                    act_slope_mul(d, z, p.act);
+                }
+            }
+            dz[r][c] = d[0];
+        }
+        __syncthreads();
+        if (p.db && blockIdx.x == 0) {
+            for (int c = tid; c < n; c += 256) {
+                float s = 0.f;
+#pragma unroll
+                for (int r = 0; r < R; ++r) s += dz[r][c];
+                p.db[c0 + c] = s;
+            }
+        }
+        if (on) {
+            const T *w = p.W + (size_t)i * p.out + c0;
+            float *o = p.dW ? p.dW + (size_t)i * p.out + c0 : nullptr;
+#pragma unroll 4
+            for (int c = lane * VEC; c < n; c += 32 * VEC) {
+                float v[VEC], s[VEC];
+                if (p.dX) {
+                    vec_load<T, VEC>(w + c, v);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) v[j] = 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) s[j] = 0.f;
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) {
+                        const float d = dz[r][c + j];
+                        acc[r] += v[j] * d;
+                        s[j] += x[r] * d;
+                    }
+                if (o) {
+                    if constexpr (VEC == 1) {
+                        o[c] = s[0];
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < VEC; j += 4)
+                            __stcs(reinterpret_cast<float4 *>(o + c + j), make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]));
+                    }
+                }
+            }
+        }
+    }
+    if (on && p.dX) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) acc[r] = warp_sum(acc[r]);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (lane == r && r < p.rows) {
+                const size_t at = (size_t)r * p.in + i;
+                float y[1] = {acc[r]};
+                if (e.zin) {
+                    const float z[1] = {ldf(e.zin + at)};
+                    act_slope_mul(y, z, e.act);
+                }
+                if (e.add) y[0] += ldf(e.add + at);
+                stf(p.dX + at, y[0]);
+            }
+    }
+}
+
+// ------------------------------------------------------------------ host side
+
+template <typename T, int VEC, int R>
+static cudaError_t vec_fwd(const LinVec<T> &p, const LinEpi<T> &e, cudaStream_t st) {
+    constexpr int C = (VEC == 1 ? 32 : 8) * VEC;
+    const int tiles = (p.out + C - 1) / C;
+    // parts of 128 rows of W or more, up to eight, until there are about four CTAs an SM
+    int cluster = 1;
+    while (cluster < 8 && tiles * cluster < 4 * sm_count() && p.in >= 256 * cluster) cluster *= 2;
+    const int part = (p.in + cluster - 1) / cluster;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)tiles * cluster);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, k_lin_vec_fwd<T, VEC, R>, p, e, part, cluster);
+}
+template <typename T, int VEC, int R>
+static cudaError_t vec_bwd(const LinVec<T> &p, const LinEpi<T> &e, cudaStream_t st) {
+    k_lin_vec_bwd<T, VEC, R><<<(p.in + 7) / 8, 256, 0, st>>>(p, e);
+    return cudaGetLastError();
+}
+
+template <typename T, typename F>
+static cudaError_t vec_pick(int rows, int out, F &&f) {
+    constexpr int W = 16 / sizeof(T);
+    auto go = [&](auto vec) {
+        if (rows <= 1) return f(vec, std::integral_constant<int, 1>{});
+        if (rows <= 2) return f(vec, std::integral_constant<int, 2>{});
+        if (rows <= 4) return f(vec, std::integral_constant<int, 4>{});
+        return f(vec, std::integral_constant<int, 8>{});
+    };
+    return out % W == 0 ? go(std::integral_constant<int, W>{}) : go(std::integral_constant<int, 1>{});
+}
+
+template <typename T>
+cudaError_t lin_vec_forward(const LinVec<T> &p, const LinEpi<T> &e, cudaStream_t st) {
+    return vec_pick<T>(p.rows, p.out, [&](auto v, auto r) { return vec_fwd<T, decltype(v)::value, decltype(r)::value>(p, e, st); });
+}
+template <typename T>
+cudaError_t lin_vec_backward(const LinVec<T> &p, const LinEpi<T> &e, cudaStream_t st) {
+    return vec_pick<T>(p.rows, p.out, [&](auto v, auto r) { return vec_bwd<T, decltype(v)::value, decltype(r)::value>(p, e, st); });
+}
+template cudaError_t lin_vec_forward<float>(const LinVec<float> &, const LinEpi<float> &, cudaStream_t);
+template cudaError_t lin_vec_forward<__nv_bfloat16>(const LinVec<__nv_bfloat16> &, const LinEpi<__nv_bfloat16> &, cudaStream_t);
+template cudaError_t lin_vec_backward<float>(const LinVec<float> &, const LinEpi<float> &, cudaStream_t);
+template cudaError_t lin_vec_backward<__nv_bfloat16>(const LinVec<__nv_bfloat16> &, const LinEpi<__nv_bfloat16> &, cudaStream_t);
+
+}  // namespace ops
+}  // namespace eaga

@@ -25,6 +25,7 @@ EXPORTED = ("eaga_workspace_size", "eaga_saved_size", "eaga_forward", "eaga_back
             "eaga_forward_variant", "eaga_backward_variant", "eaga_forward_rows", "eaga_backward_rows",
             "eaga_block_saved_size", "eaga_block_workspace_size", "eaga_block_kernel_launches",
             "eaga_block_forward", "eaga_block_backward",
+            "eaga_linear_workspace_size", "eaga_linear_forward", "eaga_linear_backward",
             "eaga_residual_norm_workspace_size", "eaga_residual_norm_forward", "eaga_residual_norm_backward",
             "eaga_adamw_step", "eaga_adamw_unpack")
 # parameters of the graph-transformer block (eaga_block_weights field order)
@@ -34,6 +35,8 @@ BLOCK_WEIGHT_NAMES = tuple(f"{s}_{k}" for s in ("x", "e", "y") for k in BLOCK_SU
 VARIANTS = {"layer": 0, "light_edge": 1, "unnormalised": 2}
 # norms of the residual step (eaga_norm)
 NORMS = {"none": 0, "layer": 1, "rms": 2}
+# activations of the linear operator (eaga_act)
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
 
 
 class Dims(ctypes.Structure):
@@ -46,6 +49,10 @@ class Weights(ctypes.Structure):
 
 class BlockWeights(ctypes.Structure):
     _fields_ = [(k, ctypes.c_void_p) for k in BLOCK_WEIGHT_NAMES]
+
+
+class LinearDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_longlong)] + [(k, ctypes.c_int) for k in ("in_", "out", "act", "dtype")]
 
 
 class ResidualNormDims(ctypes.Structure):
@@ -130,6 +137,13 @@ def lib():
         L.eaga_block_backward.argtypes = [ctypes.POINTER(Dims), vp, vp, vp, vp, W_, BW_, vp, vp, vp, vp, vp, vp,
                                           vp, vp, vp, vp, W_, BW_, vp, sz, vp]
         L.eaga_block_backward.restype = i32
+        LD_ = ctypes.POINTER(LinearDims)
+        L.eaga_linear_workspace_size.argtypes = [LD_, i32]
+        L.eaga_linear_workspace_size.restype = sz
+        L.eaga_linear_forward.argtypes = [LD_] + [vp] * 7 + [sz, vp]
+        L.eaga_linear_forward.restype = i32
+        L.eaga_linear_backward.argtypes = [LD_] + [vp] * 4 + [i32] + [vp] * 6 + [sz, vp]
+        L.eaga_linear_backward.restype = i32
         ND_ = ctypes.POINTER(ResidualNormDims)
         L.eaga_residual_norm_workspace_size.argtypes = [ND_]
         L.eaga_residual_norm_workspace_size.restype = sz
@@ -393,6 +407,36 @@ def _code(name, names, what):
     if name not in names:
         raise ValueError(f"{what}: {name!r}, expected one of {', '.join(names)}")
     return names[name]
+
+
+def linear_dims(rows, in_, out, act="none", dtype="bf16") -> LinearDims:
+    return LinearDims(rows, in_, out, _code(act, ACTS, "act"),
+                      EAGA_BF16 if dtype == "bf16" else EAGA_FP32 if dtype == "fp32" else dtype)
+
+
+def linear_workspace_size(d: LinearDims, for_backward: bool) -> int:
+    return int(lib().eaga_linear_workspace_size(ctypes.byref(d), int(bool(for_backward))))
+
+
+def linear_forward(d: LinearDims, X, W, b, R, Y, Z, workspace, stream=None):
+    """eaga_linear_forward: Z = X W + b, Y = act(Z) + R."""
+    p, sd, n = _Checked(), _storage(d), d.rows * d.out
+    rc = lib().eaga_linear_forward(
+        ctypes.byref(d), p(X, "X", sd, d.rows * d.in_), p(W, "W", sd, d.in_ * d.out), p(b, "b", sd, d.out, True),
+        p(R, "R", sd, n, True), p(Y, "Y", sd, n), p(Z, "Z", sd, n, True), p.workspace(workspace), _nbytes(workspace),
+        _stream(stream))
+    _check(rc, "eaga_linear_forward")
+
+
+def linear_backward(d: LinearDims, X, W, Z, dY, dX, dW, db, workspace, act_in="none", Zin=None, dR=None, stream=None):
+    """eaga_linear_backward: dX = act_in'(Zin) (dZ W^T) + dR, dW = X^T dZ, db = sum of dZ's rows."""
+    p, sd, f, n, m = _Checked(), _storage(d), _f32(), d.rows * d.out, d.rows * d.in_
+    rc = lib().eaga_linear_backward(
+        ctypes.byref(d), p(X, "X", sd, m, True), p(W, "W", sd, d.in_ * d.out, True), p(Z, "Z", sd, n, True),
+        p(dY, "dY", sd, n), _code(act_in, ACTS, "act_in"), p(Zin, "Zin", sd, m, True), p(dR, "dR", sd, m, True),
+        p(dX, "dX", sd, m, True), p(dW, "dW", f, d.in_ * d.out, True), p(db, "db", f, d.out, True),
+        p.workspace(workspace), _nbytes(workspace), _stream(stream))
+    _check(rc, "eaga_linear_backward")
 
 
 def residual_norm_dims(rows, w, pre="layer", post="none", rows_per_group=None, eps=1e-5, alpha=1.0,

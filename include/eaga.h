@@ -369,6 +369,47 @@ EAGA_API eaga_status eaga_block_backward(const eaga_dims *dims,
                                  const eaga_block_grads *dWb, void *workspace, size_t ws_bytes, void *stream);
 
 /* ---------------------------------------------------------------------
+ * A dense product with its epilogue, and its gradients: the projections,
+ * feed-forward products and heads around the block.  X [rows, in], W [in,
+ * out], b [out], R, Y, Z, dY [rows, out], Zin, dR, dX [rows, in] in the
+ * storage dtype; dW [in, out], db [out] in fp32:
+ *
+ *   Z  = X W + b           Y  = act(Z) + R
+ *   dZ = act'(Z) dY        dX = act_in'(Zin) (dZ W^T) + dR
+ *   dW = X^T dZ            db = sum of dZ's rows
+ *
+ * with gelu its exact (erf) form and silu z / (1 + exp(-z)).  act is applied
+ * to fp32 sums; every output is rounded once.  act_in is the activation that
+ * made X (X = act_in(Zin)) where its gradient is wanted in the same pass; dR
+ * the gradient that reaches X by another way.  With act none, dY is dZ.
+ *
+ * Nullable: b, R and, in the forward, Z (needed by the backward unless act is
+ * none); in the backward Z (exactly where act is none), Zin (exactly where
+ * act_in is none), dR, one of dX and dW, db (given only with dW).  Outputs are
+ * overwritten.  All sums run in an order that the dims fix.
+ *
+ * Limits: in, out <= 65536, rows <= 2147418112.  rows = 0 is a call that
+ * writes no row (and zero dW, db).  Any size; rows of X, W and dZ that are not
+ * a multiple of 16 bytes cost a padded copy in the workspace. */
+typedef enum { EAGA_ACT_NONE = 0, EAGA_ACT_RELU = 1, EAGA_ACT_GELU = 2, EAGA_ACT_SILU = 3 } eaga_act;
+typedef struct {
+    long long rows;
+    int in, out;
+    int act;                    /* eaga_act */
+    int dtype;                  /* eaga_dtype */
+} eaga_linear_dims;
+
+/* Bytes of workspace of the forward (for_backward = 0) or the backward (1);
+ * 0 for invalid or unsupported dims.  Starts with the status word that
+ * eaga_get_device_status reads. */
+EAGA_API size_t eaga_linear_workspace_size(const eaga_linear_dims *dims, int for_backward);
+EAGA_API eaga_status eaga_linear_forward(const eaga_linear_dims *dims, const void *X, const void *W, const void *b,
+                                const void *R, void *Y, void *Z, void *workspace, size_t ws_bytes, void *stream);
+EAGA_API eaga_status eaga_linear_backward(const eaga_linear_dims *dims, const void *X, const void *W, const void *Z,
+                                const void *dY, int act_in, const void *Zin, const void *dR, void *dX, float *dW,
+                                float *db, void *workspace, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------
  * The residual step between two sub-layers, with the norm after the one and
  * before the other, a gate and a residual scale.  Per row, with x the residual
  * stream, u the sub-layer's output and M the row mask:

@@ -115,3 +115,56 @@ def test_adamw_needs_a_gpu():
     from edge_aware_graph_b200.optim import AdamW
     with pytest.raises(ValueError):
         AdamW([torch.zeros(8)], [torch.zeros(8)])
+
+
+def linear_call(L, d, **over):
+    names = "X W b R Y Z".split()
+    p = [over.get(k, OK + ((i + 1) << 28)) for i, k in enumerate(names)]
+    return L.eaga_linear_forward(ctypes.byref(d) if d else None, *p, over.get("ws", OK + (30 << 28)),
+                                 over.get("size", eaga.linear_workspace_size(d, False) if d else 0), None)
+
+
+def linear_back(L, d, act_in=0, **over):
+    at = {k: OK + ((i + 1) << 28) for i, k in enumerate("X W Z dY Zin dR dX dW db".split())}
+    if not d.act:
+        at["Z"] = None
+    if not act_in:
+        at["Zin"] = None
+    at.update(over)
+    return L.eaga_linear_backward(ctypes.byref(d), at["X"], at["W"], at["Z"], at["dY"], act_in, at["Zin"], at["dR"], at["dX"], at["dW"],
+                                  at["db"], over.get("ws", OK + (30 << 28)),
+                                  over.get("size", eaga.linear_workspace_size(d, True)), None)
+
+
+@pytest.mark.parametrize("args,code", [
+    ((-1, 8, 8), 1), ((4, 0, 8), 1), ((4, 8, 0), 1), ((4, 65537, 8), 2), ((4, 8, 65537), 2), ((1 << 31, 8, 8), 2), ((4, 8, 8, "none", 7), 1),
+])
+def test_linear_dims(L, args, code):
+    d = eaga.linear_dims(*args)
+    assert linear_call(L, d) == code and linear_back(L, d) == code
+    assert eaga.linear_workspace_size(d, False) == 0 and eaga.linear_workspace_size(d, True) == 0
+
+
+def test_linear_pointers(L):
+    d = eaga.linear_dims(64, 40, 24, "silu", "bf16")
+    assert linear_call(L, None) == 1
+    for k in ("X", "W", "Y", "ws"):
+        assert linear_call(L, d, **{k: None}) == 1, k
+    for k in ("X", "W", "b", "R", "Y", "Z", "ws"):
+        assert linear_call(L, d, **{k: OK + (20 << 28) + 8}) == 3, k
+    assert linear_call(L, d, size=eaga.linear_workspace_size(d, False) - 1) == 4
+    assert linear_call(L, d, Y=OK + (4 << 28)) == 1 and linear_call(L, d, Z=OK + (5 << 28)) == 1      # Y over R, Z over Y
+    for k in ("X", "W", "Z", "dY", "ws"):
+        assert linear_back(L, d, **{k: None}) == 1, k
+    for k in ("X", "W", "Z", "dY", "dR", "dX", "dW", "db", "ws"):
+        assert linear_back(L, d, **{k: OK + (20 << 28) + 8}) == 3, k
+    assert linear_back(L, d, size=eaga.linear_workspace_size(d, True) - 1) == 4
+    assert linear_back(L, d, dX=None, dW=None, db=None, dR=None) == 1
+    assert linear_back(L, d, dW=None) == 1                              # db without dW
+    assert linear_back(L, d, dX=None) == 1                              # dR without dX
+    assert linear_back(L, d, act_in=9) == 1 and linear_back(L, d, act_in=2, Zin=None) == 1
+    assert linear_back(L, d, Zin=OK + (21 << 28)) == 1                  # an input activation's z without the activation
+    assert linear_back(L, eaga.linear_dims(64, 40, 24), Z=OK + (21 << 28)) == 1
+    assert linear_back(L, d, dX=OK + (6 << 28)) == 1                    # dX over dR
+    with pytest.raises(ValueError):
+        eaga.linear_dims(4, 8, 8, "tanh")

@@ -1,4 +1,5 @@
-"""Build libeaga.so (in-tree) from csrc/*.cu for sm_100a with nvcc."""
+"""Build libeaga.so (in-tree) from csrc/*.cu for sm_100a with nvcc, and the
+Python entry of the operators (_native.so, csrc/native.cpp) beside it with g++."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -11,6 +12,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libeaga.so")
+NATIVE = os.path.join(HERE, "_native.so")
 OBJ = os.path.join(HERE, "_build")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
@@ -39,6 +41,32 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _native(force: bool):
+    """_native.so against this interpreter and its torch."""
+    import sysconfig
+
+    import torch
+    src = os.path.join(CSRC, "native.cpp")
+    stamp = os.path.join(OBJ, "native.stamp")           # the torch and Python it was built for
+    want = f"{torch.__version__} {sys.version}"
+    newest = max(os.path.getmtime(p) for p in (src, os.path.join(ROOT, "include", "eaga.h")))
+    if not force and os.path.exists(NATIVE) and os.path.getmtime(NATIVE) >= newest and os.path.exists(stamp) \
+            and open(stamp).read() == want:
+        return
+    t = os.path.dirname(torch.__file__)
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(ROOT, "include"),
+           "-I", os.path.join(t, "include"), "-I", os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"),
+           src, "-o", NATIVE, "-L", HERE, "-leaga", "-Wl,-rpath,$ORIGIN", "-L", os.path.join(t, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stderr}")
+    with open(stamp, "w") as f:
+        f.write(want)
+
+
 def build(verbose: bool = False, force: bool = False) -> str:
     os.makedirs(OBJ, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
@@ -52,6 +80,7 @@ def build(verbose: bool = False, force: bool = False) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stderr}")
+    _native(force)
     return LIB
 
 

@@ -11,13 +11,15 @@ namespace fast {
 
 constexpr int DE = 64, NH = 8, DH = 32, HD = 256, NF = 16;
 constexpr int TB = 8;            // query rows per pair-kernel CTA (one row block)
-// Streaming multiprocessors of the current device.
+// Streaming multiprocessors of the current device (asked once per device).
 inline int sm_count() {
+    static std::atomic<int> known[32];
     int dev = 0, v = 0;
-    if (cudaGetDevice(&dev) == cudaSuccess && cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess &&
-        v > 0)
-        return v;
-    return 148;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+    if (dev >= 0 && dev < 32 && (v = known[dev].load(std::memory_order_relaxed)) > 0) return v;
+    if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0) return 148;
+    if (dev >= 0 && dev < 32) known[dev].store(v, std::memory_order_relaxed);
+    return v;
 }
 
 // Launch of a kernel that may start behind the previous kernel of its stream

@@ -336,14 +336,15 @@ static cudaError_t launch_part(const AdScalars &s, const AdEntry *e, int count, 
     return LAUNCH::go(t, st);
 }
 
-// Up to 32 tensors travel in a small table, more in launches of 384 (32 KB of parameters, the most a launch takes).
+// A launch copies its whole table: up to 64 tensors (a block of the framework has 39) travel in a small one,
+// more in launches of 384 (32 KB of parameters, the most a launch takes; 3 us more of the host's time).
 template <typename LAUNCH>
 static cudaError_t launch_all(const AdScalars &s, const AdEntry *e, int count, cudaStream_t st) {
     int at = 0;
     do {
         const int k = std::min(count - at, 384);
         const bool last = at + k == count;
-        const cudaError_t err = k <= 32 ? launch_part<LAUNCH, 32>(s, e + at, k, last, st)
+        const cudaError_t err = k <= 64 ? launch_part<LAUNCH, 64>(s, e + at, k, last, st)
                                         : launch_part<LAUNCH, 384>(s, e + at, k, last, st);
         if (err != cudaSuccess) return err;
         at += k;

@@ -376,8 +376,8 @@ static LtParams<TO> lt_params(const LinTc &q, long long M, int N, int bn) {
 }
 // The maps of the parts that are there.
 static bool lt_encode(CUtensorMap (&m)[3], const bf16 *const (&base)[3], long long rows, int ld, int box) {
-    for (int k = 0; k < 3; ++k)
-        if (!fast::encode_2d(&m[k], base[base[k] ? k : 0], (int)rows, ld, box)) return false;
+    for (int k = 0; k < 3 && base[k]; ++k)
+        if (!fast::encode_2d(&m[k], base[k], (int)rows, ld, box)) return false;
     return true;
 }
 

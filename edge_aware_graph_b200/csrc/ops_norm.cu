@@ -23,6 +23,7 @@
 // row per parameter and each run of a group's rows one of its gate, which
 // k_rn_finish adds in a fixed order: no atomics, the same bits every time.
 #include <algorithm>
+#include <type_traits>
 #include "common.cuh"
 #include "ops.h"
 
@@ -52,29 +53,48 @@ struct RnArgs {
 template <typename T, int VEC, int E>
 struct RowIo {
     static constexpr int NV = E / VEC;
+    // A row's elements as they lie in memory: 16-byte vectors (fewer registers than the values), or elements.
+    struct Raw {
+        typename std::conditional<VEC == 1, T, uint4>::type v[NV];
+    };
     // column of element q of this thread
     static __device__ __forceinline__ unsigned col(int q, unsigned k, unsigned team) {
         return (k + (q / VEC) * team) * VEC + q % VEC;
     }
-    static __device__ __forceinline__ void load(const T *p, unsigned k, unsigned team, unsigned w, float (&v)[E]) {
+    static __device__ __forceinline__ void fetch(const T *p, bool there, unsigned k, unsigned team, unsigned w, Raw &r) {
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
             const unsigned c = (k + n * team) * VEC;
             if constexpr (VEC == 1) {
-                v[n] = c < w ? ldf(p + c) : 0.f;
-            } else if constexpr (sizeof(T) == 4) {
-                const float4 a = c < w ? *reinterpret_cast<const float4 *>(p + c) : make_float4(0, 0, 0, 0);
-                v[4 * n] = a.x; v[4 * n + 1] = a.y; v[4 * n + 2] = a.z; v[4 * n + 3] = a.w;
+                r.v[n] = there && c < w ? p[c] : T(0.f);
             } else {
-                const uint4 a = c < w ? *reinterpret_cast<const uint4 *>(p + c) : make_uint4(0, 0, 0, 0);
-                const unsigned x[4] = {a.x, a.y, a.z, a.w};
+                r.v[n] = there && c < w ? *reinterpret_cast<const uint4 *>(p + c) : make_uint4(0, 0, 0, 0);
+            }
+        }
+    }
+    static __device__ __forceinline__ void values(const Raw &r, float (&v)[E]) {
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            if constexpr (VEC == 1) {
+                v[n] = ldf(&r.v[n]);
+            } else {
+                const unsigned x[4] = {r.v[n].x, r.v[n].y, r.v[n].z, r.v[n].w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    v[8 * n + 2 * j] = __uint_as_float(x[j] << 16);
-                    v[8 * n + 2 * j + 1] = __uint_as_float(x[j] & 0xffff0000u);
+                    if constexpr (sizeof(T) == 4) {
+                        v[4 * n + j] = __uint_as_float(x[j]);
+                    } else {
+                        v[8 * n + 2 * j] = __uint_as_float(x[j] << 16);
+                        v[8 * n + 2 * j + 1] = __uint_as_float(x[j] & 0xffff0000u);
+                    }
                 }
             }
         }
+    }
+    static __device__ __forceinline__ void load(const T *p, unsigned k, unsigned team, unsigned w, float (&v)[E]) {
+        Raw r;
+        fetch(p, true, k, team, w, r);
+        values(r, v);
     }
     static __device__ __forceinline__ void store(T *p, unsigned k, unsigned team, unsigned w, const float (&v)[E]) {
 #pragma unroll
@@ -137,46 +157,81 @@ __device__ __forceinline__ Team my_team(unsigned team) {
     return {threadIdx.x % team, blockIdx.x * per + threadIdx.x / team, gridDim.x * per};
 }
 
+// What a thread keeps beside the row it works on.  AHEAD: the next row, as it
+// lies in memory (4 registers a tensor for 8 bf16 elements, where there is room
+// for them).  KEEP: the norms' gains and shifts; teams of a CTA's size read
+// those from L1 again, and run two CTAs an SM instead.
+template <int VEC, int E, bool WIDE>
+struct RnKeep {
+    static constexpr bool AHEAD = VEC == 8 && E == 8, KEEP = AHEAD && !WIDE;
+};
+
 template <typename T, int VEC, int E, bool WIDE, int MAXT>
-__global__ void __launch_bounds__(MAXT)
+__global__ void __launch_bounds__(MAXT, E > 8 ? 1 : WIDE ? 1024 / MAXT : 3)
 k_rn_fwd(const RnArgs a) {
     using IO = RowIo<T, VEC, E>;
+    using Raw = typename IO::Raw;
+    constexpr bool AHEAD = RnKeep<VEC, E, WIDE>::AHEAD, KEEP = RnKeep<VEC, E, WIDE>::KEEP;
     __shared__ float buf[2][4][32];
     unsigned turn = 0;
     const unsigned w = a.w, team = a.team;
     const Team tm = my_team<WIDE>(team);
-    bool on[E];
+    bool on_v[IO::NV];                               // a vector is in the row, or none of it
 #pragma unroll
-    for (int q = 0; q < E; ++q) on[q] = IO::col(q, tm.k, team) < w;
+    for (int n = 0; n < IO::NV; ++n) on_v[n] = IO::col(n * VEC, tm.k, team) < w;
+    auto on = [&](int q) { return on_v[q / VEC]; };
     const T *x = static_cast<const T *>(a.x), *u = static_cast<const T *>(a.u), *gate = static_cast<const T *>(a.gate);
     T *r = static_cast<T *>(a.r), *h = static_cast<T *>(a.h);
     const unsigned last = WIDE ? a.rows : (a.rows + tm.count - 1) / tm.count * tm.count;   // warps stay whole
+    // the next row's elements are on their way while this one is normalised; the mask a row further ahead
+    Raw nu, nx, ng;
+    auto alive = [&](unsigned row) { return row < a.rows && (!a.M || a.M[row]); };
+    auto ask = [&](unsigned row, bool live) {
+        const size_t at = (size_t)(live ? row : 0) * w;
+        IO::fetch(u + at, live, tm.k, team, w, nu);
+        IO::fetch(x + at, live && x, tm.k, team, w, nx);
+        IO::fetch(gate + (size_t)((live ? row : 0) / a.group) * w, live && gate, tm.k, team, w, ng);
+    };
+    bool live = alive(tm.id), next = AHEAD && alive(tm.id + tm.count);
+    if (AHEAD) ask(tm.id, live);
+    Raw kept[4];                                     // the norms' parameters
+    const T *const param[4] = {static_cast<const T *>(a.post_g), static_cast<const T *>(a.post_s), static_cast<const T *>(a.pre_g),
+                               static_cast<const T *>(a.pre_s)};
+    if (KEEP) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n) IO::fetch(param[n], param[n], tm.k, team, w, kept[n]);
+    }
     for (unsigned row = tm.id; row < last; row += tm.count) {
         const bool in = row < a.rows;
-        const bool live = in && (!a.M || a.M[row]);
         const size_t at = (size_t)(in ? row : 0) * w;
-        float p[E], t[E];
-        if (live) {
-            IO::load(u + at, tm.k, team, w, p);
-        } else {
+        if (!AHEAD) {
+            live = alive(row);
+            ask(row, live);
+        }
+        const bool now = live;
+        float p[E];
+        IO::values(nu, p);
+        const Raw rx = nx, rg = ng;
+        if (AHEAD) {
+            ask(row + tm.count, next);
+            live = next;
+            next = alive(row + 2 * tm.count);
+        }
+        if (WIDE && !now) {                         // the whole CTA holds this row
 #pragma unroll
             for (int q = 0; q < E; ++q) p[q] = 0.f;
-        }
-        if (WIDE && !live) {                        // the whole CTA holds this row
-#pragma unroll
-            for (int q = 0; q < E; ++q) t[q] = 0.f;
-            if (r) IO::store(r + at, tm.k, team, w, t);
-            if (h) IO::store(h + at, tm.k, team, w, t);
+            if (r) IO::store(r + at, tm.k, team, w, p);
+            if (h) IO::store(h + at, tm.k, team, w, p);
             continue;
         }
-        if (x && live) {
-            IO::load(x + at, tm.k, team, w, t);
-        } else {
-#pragma unroll
-            for (int q = 0; q < E; ++q) t[q] = 0.f;
-        }
-        auto norm = [&](float (&v)[E], int kind, const void *gain, const void *shift) {
+        auto values_of = [&](auto which, float (&c)[E]) {
+            constexpr int P = decltype(which)::value;
+            if constexpr (KEEP) IO::values(kept[P], c);
+            else IO::load(param[P], tm.k, team, w, c);
+        };
+        auto norm = [&](float (&v)[E], int kind, auto first) {       // parameters `first` (gain) and the next (shift)
             if (kind == RN_NONE) return;
+            constexpr int P = decltype(first)::value;
             float s[1];
             if (kind == RN_LAYER) {
                 s[0] = 0.f;
@@ -185,47 +240,49 @@ k_rn_fwd(const RnArgs a) {
                 team_sum<WIDE, 1>(s, team, buf, turn);
                 const float mean = s[0] * a.inv_w;
 #pragma unroll
-                for (int q = 0; q < E; ++q) v[q] = on[q] ? v[q] - mean : 0.f;
+                for (int q = 0; q < E; ++q) v[q] = on(q) ? v[q] - mean : 0.f;
             }
             s[0] = 0.f;
 #pragma unroll
             for (int q = 0; q < E; ++q) s[0] += v[q] * v[q];
             team_sum<WIDE, 1>(s, team, buf, turn);
-            const float rstd = 1.f / sqrtf(s[0] * a.inv_w + a.eps);
+            const float rstd = rsqrtf(s[0] * a.inv_w + a.eps);
             float c[E];
-            if (gain) {
-                IO::load(static_cast<const T *>(gain), tm.k, team, w, c);
+            if (param[P]) {
+                values_of(first, c);
 #pragma unroll
                 for (int q = 0; q < E; ++q) v[q] *= rstd * c[q];
             } else {
 #pragma unroll
                 for (int q = 0; q < E; ++q) v[q] *= rstd;
             }
-            if (shift) {
-                IO::load(static_cast<const T *>(shift), tm.k, team, w, c);
+            if (param[P + 1]) {
+                values_of(std::integral_constant<int, P + 1>{}, c);
 #pragma unroll
                 for (int q = 0; q < E; ++q) v[q] += c[q];
             }
         };
-        norm(p, a.post, a.post_g, a.post_s);
+        norm(p, a.post, std::integral_constant<int, 0>{});
         if (gate) {
             float c[E];
-            IO::load(gate + (size_t)((in ? row : 0) / a.group) * w, tm.k, team, w, c);
+            IO::values(rg, c);
 #pragma unroll
             for (int q = 0; q < E; ++q) p[q] *= c[q];
         }
         if (x) {
+            float t[E];
+            IO::values(rx, t);
 #pragma unroll
             for (int q = 0; q < E; ++q) p[q] += a.alpha * t[q];
         }
-        if (!live) {
+        if (!now) {
 #pragma unroll
             for (int q = 0; q < E; ++q) p[q] = 0.f;
         }
         if (r && in) IO::store(r + at, tm.k, team, w, p);
         if (!h) continue;
-        norm(p, a.pre, a.pre_g, a.pre_s);
-        if (!live) {
+        norm(p, a.pre, std::integral_constant<int, 2>{});
+        if (!now) {
 #pragma unroll
             for (int q = 0; q < E; ++q) p[q] = 0.f;
         }
@@ -233,22 +290,29 @@ k_rn_fwd(const RnArgs a) {
     }
 }
 
-// A team takes runs of consecutive rows of one group (a run is the whole group or a part of it).
+// A team takes runs of consecutive rows of one group (a run is the whole group
+// or a part of it), a row a step; every team of the launch takes the same number
+// of steps.  While a row is worked on, the next one's elements are on their way
+// into registers (as they lie in memory: 4 registers a tensor), and the mask of
+// the row after that.
 template <typename T, int VEC, int E, bool WIDE, int MAXT>
-__global__ void __launch_bounds__(MAXT)
+__global__ void __launch_bounds__(MAXT, 512 / MAXT)
 k_rn_bwd(const RnArgs a) {
     using IO = RowIo<T, VEC, E>;
+    using Raw = typename IO::Raw;
+    constexpr bool AHEAD = RnKeep<VEC, E, WIDE>::AHEAD, KEEP = RnKeep<VEC, E, WIDE>::KEEP;
     __shared__ float buf[2][4][32];
     unsigned turn = 0;
     const unsigned w = a.w, team = a.team;
     const Team tm = my_team<WIDE>(team);
-    bool on[E];
+    bool on_v[IO::NV];                               // a vector is in the row, or none of it
 #pragma unroll
-    for (int q = 0; q < E; ++q) on[q] = IO::col(q, tm.k, team) < w;
+    for (int n = 0; n < IO::NV; ++n) on_v[n] = IO::col(n * VEC, tm.k, team) < w;
+    auto on = [&](int q) { return on_v[q / VEC]; };
     const T *u = static_cast<const T *>(a.u), *rin = static_cast<const T *>(a.rin), *dr = static_cast<const T *>(a.dr),
             *dh = static_cast<const T *>(a.dh), *gate = static_cast<const T *>(a.gate);
     T *dx = static_cast<T *>(a.dx), *du = static_cast<T *>(a.du);
-    const bool need_u = gate != nullptr || a.post != RN_NONE;
+    const bool need_u = gate != nullptr || a.post != RN_NONE, has_pre = a.pre != RN_NONE;
     // Sums of the gains' and shifts' gradients, post then pre: in registers, or, where a thread holds 16 columns
     // and they would not fit, in shared memory (each thread its own columns).
     constexpr bool IN_SMEM = E > 8;
@@ -264,53 +328,103 @@ k_rn_bwd(const RnArgs a) {
     auto add = [&](auto which, int q, float v) {
         constexpr int P = decltype(which)::value;
         if constexpr (IN_SMEM) {
-            if (on[q]) acc[P * w + IO::col(q, tm.k, team)] += v;
+            if (on(q)) acc[P * w + IO::col(q, tm.k, team)] += v;
         } else {
             sums[P][q] += v;
         }
     };
-    const unsigned last = WIDE ? a.runs : (a.runs + tm.count - 1) / tm.count * tm.count;
-    for (unsigned run = tm.id; run < last; run += tm.count) {
-        const bool has = run < a.runs;
-        const unsigned grp = has ? run / a.runs_per_group : 0, part = has ? run % a.runs_per_group : 0;
-        const unsigned row0 = grp * a.group + part * a.run;
-        const unsigned n = has ? min(a.run, a.group - part * a.run) : 0;
-        float gt[E], s_gate[E];
-#pragma unroll
-        for (int q = 0; q < E; ++q) s_gate[q] = 0.f;
-        if (gate) {
-            IO::load(gate + (size_t)grp * w, tm.k, team, w, gt);
+    Raw pre_g, post_g;
+    if (KEEP) {
+        IO::fetch(static_cast<const T *>(a.pre_g), a.pre_g, tm.k, team, w, pre_g);
+        IO::fetch(static_cast<const T *>(a.post_g), a.post_g, tm.k, team, w, post_g);
+    }
+    auto gain_of = [&](const void *p, const Raw &kept, float (&c)[E]) {
+        if constexpr (KEEP) IO::values(kept, c);
+        else IO::load(static_cast<const T *>(p), tm.k, team, w, c);
+    };
+
+    // A place in the team's sequence of rows.
+    struct Place {
+        unsigned run, i, row0, n;                    // the run, the row in it, the run's first row and number of rows
+        bool in;
+    };
+    auto enter = [&](Place &p) {                     // the run's rows
+        if (p.run < a.runs) {
+            const unsigned grp = p.run / a.runs_per_group, part = p.run - grp * a.runs_per_group;
+            p.row0 = grp * a.group + part * a.run;
+            p.n = min(a.run, a.group - part * a.run);
         } else {
-#pragma unroll
-            for (int q = 0; q < E; ++q) gt[q] = 1.f;
+            p.row0 = p.n = 0;
         }
-        for (unsigned i = 0; i < a.run; ++i) {      // the same number for every team: warps stay whole
-            const bool in = i < n;
-            const unsigned row = row0 + (in ? i : 0);
-            const bool live = in && (!a.M || a.M[row]);
-            const size_t at = (size_t)row * w;
-            if (WIDE && !in) break;
-            if (WIDE ? !live : !__any_sync(0xffffffffu, live)) {
-                float z[E];
+    };
+    auto forward = [&](Place &p) {
+        if (++p.i == a.run) {
+            p.i = 0;
+            p.run = a.runs - p.run > tm.count && p.run < a.runs ? p.run + tm.count : a.runs;
+            enter(p);
+        }
+        p.in = p.i < p.n;
+    };
+    auto alive = [&](const Place &p) { return p.in && (!a.M || a.M[p.row0 + p.i]); };
+    Raw n_dr, n_dh, n_r, n_u, n_gate;
+    auto ask = [&](const Place &p, bool live) {
+        const size_t at = (size_t)(live ? p.row0 + p.i : 0) * w;
+        IO::fetch(dr + at, live && dr, tm.k, team, w, n_dr);
+        IO::fetch(dh + at, live && has_pre, tm.k, team, w, n_dh);
+        IO::fetch(rin + at, live && has_pre, tm.k, team, w, n_r);
+        IO::fetch(u + at, live && need_u, tm.k, team, w, n_u);
+    };
+    auto ask_gate = [&](const Place &p) {
+        if (p.i == 0) IO::fetch(gate + (size_t)(p.run < a.runs ? p.run / a.runs_per_group : 0) * w, gate, tm.k, team, w, n_gate);
+    };
+    Place at0 = {tm.id, 0, 0, 0, false};
+    enter(at0);
+    at0.in = at0.n > 0;
+    Place at1 = at0;
+    if (AHEAD) forward(at1);
+    bool live0 = alive(at0), live1 = AHEAD && alive(at1);
+    if (AHEAD) ask(at0, live0);
+    ask_gate(at0);
+    Raw gt = n_gate;
+    float s_gate[E];
+    const unsigned steps = WIDE ? (tm.id < a.runs ? (a.runs - tm.id + tm.count - 1) / tm.count : 0)
+                                : (a.runs + tm.count - 1) / tm.count;
+    for (unsigned long long left = (unsigned long long)steps * a.run; left; --left) {
+        const Place here = at0;
+        if (!AHEAD) {
+            live0 = alive(here);
+            ask(here, live0);
+            ask_gate(here);
+        }
+        const bool in = here.in, live = live0;
+        const size_t at = (size_t)(in ? here.row0 + here.i : 0) * w;
+        if (here.i == 0) {
+            gt = n_gate;
 #pragma unroll
-                for (int q = 0; q < E; ++q) z[q] = 0.f;
-                if (in && dx) IO::store(dx + at, tm.k, team, w, z);
-                if (in && du) IO::store(du + at, tm.k, team, w, z);
-                continue;
-            }
-            float g[E], d[E], z[E], uu[E];
-            auto get = [&](const T *p, float (&v)[E]) {
-                if (p && live) {
-                    IO::load(p + at, tm.k, team, w, v);
-                } else {
+            for (int q = 0; q < E; ++q) s_gate[q] = 0.f;
+        }
+        const Raw c_dr = n_dr, c_dh = n_dh, c_r = n_r, c_u = n_u;
+        if (AHEAD) {
+            ask(at1, live1);
+            ask_gate(at1);
+            at0 = at1;
+            live0 = live1;
+            forward(at1);
+            live1 = alive(at1);
+        } else {
+            forward(at0);
+        }
+        if (WIDE ? !live : !__any_sync(0xffffffffu, live)) {
+            float z[E];
 #pragma unroll
-                    for (int q = 0; q < E; ++q) v[q] = 0.f;
-                }
-            };
-            get(dr, g);
-            get(need_u ? u : nullptr, uu);
+            for (int q = 0; q < E; ++q) z[q] = 0.f;
+            if (in && dx) IO::store(dx + at, tm.k, team, w, z);
+            if (in && du) IO::store(du + at, tm.k, team, w, z);
+        } else {
+            float g[E], d[E], z[E];
+            IO::values(c_dr, g);
             // d becomes norm'(d; z), z is centred; returns 1 / deviation
-            auto back = [&](float (&d)[E], float (&z)[E], int kind, const void *gain, auto first) {
+            auto back = [&](float (&d)[E], float (&z)[E], int kind, const void *gain, const Raw &kept, auto first) {
                 constexpr int P = decltype(first)::value;
                 if (kind == RN_LAYER) {
                     float s[1] = {0.f};
@@ -319,11 +433,11 @@ k_rn_bwd(const RnArgs a) {
                     team_sum<WIDE, 1>(s, team, buf, turn);
                     const float mean = s[0] * a.inv_w;
 #pragma unroll
-                    for (int q = 0; q < E; ++q) z[q] = on[q] ? z[q] - mean : 0.f;
+                    for (int q = 0; q < E; ++q) z[q] = on(q) ? z[q] - mean : 0.f;
                 }
                 float e[E];
                 if (gain) {
-                    IO::load(static_cast<const T *>(gain), tm.k, team, w, e);
+                    gain_of(gain, kept, e);
 #pragma unroll
                     for (int q = 0; q < E; ++q) e[q] *= d[q];
                 } else {
@@ -338,7 +452,7 @@ k_rn_bwd(const RnArgs a) {
                     s[2] += e[q];
                 }
                 team_sum<WIDE, 3>(s, team, buf, turn);
-                const float rstd = 1.f / sqrtf(s[0] * a.inv_w + a.eps);
+                const float rstd = rsqrtf(s[0] * a.inv_w + a.eps);
                 const float c1 = s[1] * a.inv_w * rstd * rstd, c2 = kind == RN_LAYER ? s[2] * a.inv_w : 0.f;
 #pragma unroll
                 for (int q = 0; q < E; ++q) {
@@ -348,48 +462,49 @@ k_rn_bwd(const RnArgs a) {
                 }
                 return rstd;
             };
-            if (a.pre != RN_NONE) {
-                get(dh, d);
-                get(rin, z);
-                back(d, z, a.pre, a.pre_g, std::integral_constant<int, 2>{});
+            if (has_pre) {
+                IO::values(c_dh, d);
+                IO::values(c_r, z);
+                back(d, z, a.pre, a.pre_g, pre_g, std::integral_constant<int, 2>{});
 #pragma unroll
-                for (int q = 0; q < E; ++q) g[q] += d[q];
+                for (int q = 0; q < E; ++q) g[q] = live ? g[q] + d[q] : 0.f;
             }
-            if (dx) {
-                float o[E];
+            if (dx && in) {
 #pragma unroll
-                for (int q = 0; q < E; ++q) o[q] = live ? a.alpha * g[q] : 0.f;
-                if (in) IO::store(dx + at, tm.k, team, w, o);
+                for (int q = 0; q < E; ++q) z[q] = a.alpha * g[q];
+                IO::store(dx + at, tm.k, team, w, z);
             }
-            if (!live) {
+            if (gate) {
+                IO::values(gt, d);
 #pragma unroll
-                for (int q = 0; q < E; ++q) g[q] = 0.f;
+                for (int q = 0; q < E; ++q) d[q] *= g[q];
+            } else {
+#pragma unroll
+                for (int q = 0; q < E; ++q) d[q] = g[q];
             }
-#pragma unroll
-            for (int q = 0; q < E; ++q) d[q] = g[q] * gt[q];
+            IO::values(c_u, z);
             if (a.post != RN_NONE) {
-                const float rstd = back(d, uu, a.post, a.post_g, std::integral_constant<int, 0>{});
-                if (gate) {                          // p = gain zh + shift; uu is centred
+                const float rstd = back(d, z, a.post, a.post_g, post_g, std::integral_constant<int, 0>{});
+                if (gate) {                          // p = gain zh + shift; z is centred
                     float c[E];
                     if (a.post_g) {
-                        IO::load(static_cast<const T *>(a.post_g), tm.k, team, w, c);
+                        gain_of(a.post_g, post_g, c);
+#pragma unroll
+                        for (int q = 0; q < E; ++q) z[q] *= rstd * c[q];
                     } else {
 #pragma unroll
-                        for (int q = 0; q < E; ++q) c[q] = 1.f;
+                        for (int q = 0; q < E; ++q) z[q] *= rstd;
                     }
-#pragma unroll
-                    for (int q = 0; q < E; ++q) uu[q] *= rstd * c[q];
                     if (a.post_s) {
                         IO::load(static_cast<const T *>(a.post_s), tm.k, team, w, c);
 #pragma unroll
-                        for (int q = 0; q < E; ++q) uu[q] += c[q];
+                        for (int q = 0; q < E; ++q) z[q] += c[q];
                     }
-#pragma unroll
-                    for (int q = 0; q < E; ++q) s_gate[q] += g[q] * uu[q];
                 }
-            } else if (gate) {
+            }
+            if (gate) {
 #pragma unroll
-                for (int q = 0; q < E; ++q) s_gate[q] += g[q] * uu[q];
+                for (int q = 0; q < E; ++q) s_gate[q] += g[q] * z[q];
             }
             if (du && in) {
                 if (!live) {
@@ -399,14 +514,14 @@ k_rn_bwd(const RnArgs a) {
                 IO::store(du + at, tm.k, team, w, d);
             }
         }
-        if (gate && a.dgate && has) {
+        if (here.i == a.run - 1 && a.dgate && here.run < a.runs) {
             if (a.runs_per_group == 1) {
-                IO::store(static_cast<T *>(a.dgate) + (size_t)grp * w, tm.k, team, w, s_gate);
+                IO::store(static_cast<T *>(a.dgate) + (size_t)here.run * w, tm.k, team, w, s_gate);
             } else {
-                float *o = a.gparts + (size_t)run * w;
+                float *o = a.gparts + (size_t)here.run * w;
 #pragma unroll
                 for (int q = 0; q < E; ++q)
-                    if (on[q]) o[IO::col(q, tm.k, team)] = s_gate[q];
+                    if (on(q)) o[IO::col(q, tm.k, team)] = s_gate[q];
             }
         }
     }
@@ -415,7 +530,7 @@ k_rn_bwd(const RnArgs a) {
     if constexpr (WIDE && !IN_SMEM) {
 #pragma unroll
         for (int q = 0; q < E; ++q)
-            if (on[q]) {
+            if (on(q)) {
 #pragma unroll
                 for (int n = 0; n < 4; ++n) out[n * w + IO::col(q, tm.k, team)] = sums[n][q];
             }
@@ -430,7 +545,7 @@ k_rn_bwd(const RnArgs a) {
             if (warp == v && lane < team) {
 #pragma unroll
                 for (int q = 0; q < E; ++q)
-                    if (on[q]) {
+                    if (on(q)) {
 #pragma unroll
                         for (int n = 0; n < 4; ++n) {
                             float &o = acc[n * w + IO::col(q, tm.k, team)];
@@ -447,8 +562,8 @@ k_rn_bwd(const RnArgs a) {
     }
 }
 
-// The partial rows' sums, in the order of the rows.  A CTA takes 32 columns of
-// one output: its 8 warps sum every eighth row each, then the eight in order.
+// The partial rows' sums, in a fixed order.  A CTA takes 32 columns of one
+// output: its 32 warps sum every 32nd row each, then the 32 in order.
 // Outputs: the four parameters' gradients (`parts` CTA rows each), then the gate's groups.
 struct FinishArgs {
     const float *parts, *gparts;
@@ -457,8 +572,8 @@ struct FinishArgs {
     unsigned w, ctas, groups, runs_per_group;
     int n_out, which[4], dtype;
 };
-__global__ void __launch_bounds__(256) k_rn_finish(const FinishArgs f) {
-    __shared__ float sum[8][32];
+__global__ void __launch_bounds__(1024) k_rn_finish(const FinishArgs f) {
+    __shared__ float sum[32][33];
     const unsigned lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     for (unsigned job = blockIdx.y; job < f.n_out + f.groups; job += gridDim.y) {
         const bool param = job < (unsigned)f.n_out;
@@ -467,14 +582,16 @@ __global__ void __launch_bounds__(256) k_rn_finish(const FinishArgs f) {
         const float *src = param ? f.parts + (size_t)f.which[job] * f.w
                                  : f.gparts + (size_t)(job - f.n_out) * f.runs_per_group * f.w;
         float s = 0.f;
-        if (c < f.w)
-            for (unsigned r = warp; r < rows; r += 8) s += src[r * stride + c];
+        if (c < f.w) {
+#pragma unroll 8
+            for (unsigned r = warp; r < rows; r += 32) s += src[r * stride + c];
+        }
         sum[warp][lane] = s;
         __syncthreads();
         if (warp == 0 && c < f.w) {
             s = 0.f;
 #pragma unroll
-            for (int v = 0; v < 8; ++v) s += sum[v][lane];
+            for (int v = 0; v < 32; ++v) s += sum[v][lane];
             if (param) f.out[job][c] = s;
             else if (f.dtype == EAGA_FP32) static_cast<float *>(f.dgate)[(size_t)(job - f.n_out) * f.w + c] = s;
             else static_cast<__nv_bfloat16 *>(f.dgate)[(size_t)(job - f.n_out) * f.w + c] = __float2bfloat16_rn(s);
@@ -507,8 +624,8 @@ static RnPlan rn_plan(const eaga_residual_norm_dims &d) {
     p.threads = p.wide ? p.team : 256;
     const long long per = p.wide ? 1 : p.threads / p.team;
     const long long rows = d.rows, sms = sm_count();
-    const long long room = sms * (512 / p.threads);        // the backward's registers: 512 threads an SM
-    p.ctas_fwd = (int)std::max(1LL, std::min((rows + per - 1) / per, p.wide ? sms * (2048 / p.threads) : sms * 8));
+    const long long room = sms * (512 / p.threads);        // the registers: 512 threads an SM, 768 or 1024 forward
+    p.ctas_fwd = (int)std::max(1LL, std::min((rows + per - 1) / per, p.wide ? sms * (p.e > 8 ? 1 : 1024 / p.threads) : sms * 3));
     p.ctas_bwd = (int)std::max(1LL, std::min((rows + per - 1) / per, room));
     // runs: at least about four for each team, of 16 rows or more where groups are that long
     const long long groups = std::max(1LL, rows / d.rows_per_group), teams = p.ctas_bwd * per;
@@ -678,7 +795,7 @@ eaga_status eaga_residual_norm_backward(const eaga_residual_norm_dims *d, const 
     f.parts = a.parts; f.gparts = a.gparts; f.dgate = dgate;
     f.w = a.w; f.ctas = p.ctas_bwd; f.runs_per_group = p.runs_per_group; f.dtype = d->dtype;
     const dim3 grid((a.w + 31) / 32, std::min(f.n_out + f.groups, 65535u));
-    k_rn_finish<<<grid, 256, 0, st>>>(f);
+    k_rn_finish<<<grid, 1024, 0, st>>>(f);
     return cudaGetLastError() == cudaSuccess ? EAGA_OK : EAGA_ERR_CUDA;
 }
 

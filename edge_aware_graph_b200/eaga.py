@@ -3,7 +3,7 @@
 Argument marshalling only: every function takes torch tensors that already
 live on the GPU (or plain ints), passes their data pointers and the current
 CUDA stream to the C entry point of the same name, and raises on a non-OK
-status.  All arithmetic runs in the library's CUDA kernels; there is no
+status.  The operators around the block are marshalled by _native (C++).  All arithmetic runs in the library's CUDA kernels; there is no
 fallback of any kind.  The library must have been built in-tree
 (edge_aware_graph_b200/build.py); loading fails loudly otherwise.
 """
@@ -372,35 +372,21 @@ def block_backward(d: Dims, X, E, y, M, W: dict, Wb: dict, Xmid, Emid, saved, dX
 
 
 # ---------------------------------------------------------------- operators around the block
+# Their calls go through _native (csrc/native.cpp): every tensor is checked there against the dims (device, dtype, number of
+# elements, contiguity; ValueError), then the C entry is called.
 
-class _Checked:
-    """Data pointers of one call's tensors: each a contiguous CUDA tensor on the
-    current device, of the dtype and the number of elements that the call's
-    dims give it (the kernels go by the dims alone)."""
+_native_module = None
 
-    def __init__(self):
-        import torch
-        self.dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
 
-    def __call__(self, t, name, dtype, numel, optional=False):
-        if t is None:
-            if optional:
-                return None
-            raise ValueError(f"{name}: a tensor is required")
-        if not t.is_cuda:
-            raise ValueError(f"{name}: a CUDA tensor is required (got {t.device})")
-        if t.get_device() != self.dev:
-            raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{self.dev}")
-        if t.dtype != dtype:
-            raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
-        if t.numel() != numel:
-            raise ValueError(f"{name}: {t.numel()} elements, expected {numel}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name}: must be contiguous")
-        return t.data_ptr()
-
-    def workspace(self, t):
-        return self(t, "workspace", _u8(), -1 if t is None else t.numel())
+def _native():
+    """The module, loaded once.  Raises if it has not been built."""
+    global _native_module
+    if _native_module is None:
+        lib()
+        import torch  # noqa: F401  (its libraries)
+        from . import _native as m
+        _native_module = m
+    return _native_module
 
 
 def _code(name, names, what):
@@ -420,23 +406,17 @@ def linear_workspace_size(d: LinearDims, for_backward: bool) -> int:
 
 def linear_forward(d: LinearDims, X, W, b, R, Y, Z, workspace, stream=None):
     """eaga_linear_forward: Z = X W + b, Y = act(Z) + R."""
-    p, sd, n = _Checked(), _storage(d), d.rows * d.out
-    rc = lib().eaga_linear_forward(
-        ctypes.byref(d), p(X, "X", sd, d.rows * d.in_), p(W, "W", sd, d.in_ * d.out), p(b, "b", sd, d.out, True),
-        p(R, "R", sd, n, True), p(Y, "Y", sd, n), p(Z, "Z", sd, n, True), p.workspace(workspace), _nbytes(workspace),
-        _stream(stream))
-    _check(rc, "eaga_linear_forward")
+    rc = (_native_module or _native()).linear_forward(d, X, W, b, R, Y, Z, workspace, stream)
+    if rc:
+        raise EagaError(rc, "eaga_linear_forward")
 
 
 def linear_backward(d: LinearDims, X, W, Z, dY, dX, dW, db, workspace, act_in="none", Zin=None, dR=None, stream=None):
     """eaga_linear_backward: dX = act_in'(Zin) (dZ W^T) + dR, dW = X^T dZ, db = sum of dZ's rows."""
-    p, sd, f, n, m = _Checked(), _storage(d), _f32(), d.rows * d.out, d.rows * d.in_
-    rc = lib().eaga_linear_backward(
-        ctypes.byref(d), p(X, "X", sd, m, True), p(W, "W", sd, d.in_ * d.out, True), p(Z, "Z", sd, n, True),
-        p(dY, "dY", sd, n), _code(act_in, ACTS, "act_in"), p(Zin, "Zin", sd, m, True), p(dR, "dR", sd, m, True),
-        p(dX, "dX", sd, m, True), p(dW, "dW", f, d.in_ * d.out, True), p(db, "db", f, d.out, True),
-        p.workspace(workspace), _nbytes(workspace), _stream(stream))
-    _check(rc, "eaga_linear_backward")
+    rc = (_native_module or _native()).linear_backward(d, X, W, Z, dY, _code(act_in, ACTS, "act_in"), Zin, dR, dX, dW, db,
+                                                       workspace, stream)
+    if rc:
+        raise EagaError(rc, "eaga_linear_backward")
 
 
 def residual_norm_dims(rows, w, pre="layer", post="none", rows_per_group=None, eps=1e-5, alpha=1.0,
@@ -452,45 +432,31 @@ def residual_norm_workspace_size(d: ResidualNormDims) -> int:
     return int(lib().eaga_residual_norm_workspace_size(ctypes.byref(d)))
 
 
-def _groups(d: ResidualNormDims) -> int:
-    return d.rows // d.rows_per_group if d.rows_per_group > 0 else 0
-
-
 def residual_norm_forward(d: ResidualNormDims, x, u, M, gate, post_g, post_s, pre_g, pre_s, r, h, stream=None):
     """eaga_residual_norm_forward: r = alpha x + gate * post(u), h = pre(r)."""
-    p, sd, n, w = _Checked(), _storage(d), d.rows * d.w, d.w
-    rc = lib().eaga_residual_norm_forward(
-        ctypes.byref(d), p(x, "x", sd, n, True), p(u, "u", sd, n), p(M, "M", _u8(), d.rows, True),
-        p(gate, "gate", sd, _groups(d) * w, True), p(post_g, "post_g", sd, w, True), p(post_s, "post_s", sd, w, True),
-        p(pre_g, "pre_g", sd, w, True), p(pre_s, "pre_s", sd, w, True), p(r, "r", sd, n, True),
-        p(h, "h", sd, n, True), _stream(stream))
-    _check(rc, "eaga_residual_norm_forward")
+    rc = (_native_module or _native()).residual_norm_forward(d, x, u, M, gate, post_g, post_s, pre_g, pre_s, r, h, stream)
+    if rc:
+        raise EagaError(rc, "eaga_residual_norm_forward")
 
 
 def residual_norm_backward(d: ResidualNormDims, r, u, M, gate, post_g, post_s, pre_g, dr, dh, dx, du, dgate, dpost_g,
                            dpost_s, dpre_g, dpre_s, workspace, stream=None):
     """eaga_residual_norm_backward."""
-    p, sd, f, n, w = _Checked(), _storage(d), _f32(), d.rows * d.w, d.w
-    ng = _groups(d) * w
-    rc = lib().eaga_residual_norm_backward(
-        ctypes.byref(d), p(r, "r", sd, n, True), p(u, "u", sd, n, True), p(M, "M", _u8(), d.rows, True),
-        p(gate, "gate", sd, ng, True), p(post_g, "post_g", sd, w, True), p(post_s, "post_s", sd, w, True),
-        p(pre_g, "pre_g", sd, w, True), p(dr, "dr", sd, n, True), p(dh, "dh", sd, n, True), p(dx, "dx", sd, n, True),
-        p(du, "du", sd, n, True), p(dgate, "dgate", sd, ng, True), p(dpost_g, "dpost_g", f, w, True),
-        p(dpost_s, "dpost_s", f, w, True), p(dpre_g, "dpre_g", f, w, True), p(dpre_s, "dpre_s", f, w, True),
-        p.workspace(workspace), _nbytes(workspace), _stream(stream))
-    _check(rc, "eaga_residual_norm_backward")
+    rc = (_native_module or _native()).residual_norm_backward(d, r, u, M, gate, post_g, post_s, pre_g, dr, dh, dx, du, dgate,
+                                                              dpost_g, dpost_s, dpre_g, dpre_s, workspace, stream)
+    if rc:
+        raise EagaError(rc, "eaga_residual_norm_backward")
 
 
 def adamw_step(config: AdamwConfig, tensors, count: int, state, lr=None, stream=None):
     """eaga_adamw_step over a ctypes array of AdamwTensor (optim.AdamW makes and keeps one)."""
-    p = _Checked()
-    import torch
-    rc = lib().eaga_adamw_step(ctypes.byref(config), tensors, int(count), p(state, "state", torch.int64, 2),
-                               p(lr, "lr", _f32(), 1, True), _stream(stream))
-    _check(rc, "eaga_adamw_step")
+    rc = (_native_module or _native()).adamw_step(config, tensors, count, state, lr, stream)
+    if rc:
+        raise EagaError(rc, "eaga_adamw_step")
 
 
 def adamw_unpack(tensors, count: int, stream=None):
     """eaga_adamw_unpack."""
-    _check(lib().eaga_adamw_unpack(tensors, int(count), _stream(stream)), "eaga_adamw_unpack")
+    rc = (_native_module or _native()).adamw_unpack(tensors, count, stream)
+    if rc:
+        raise EagaError(rc, "eaga_adamw_unpack")

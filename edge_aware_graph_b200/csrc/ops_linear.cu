@@ -127,7 +127,7 @@ static LinPlan lin_plan(const eaga_linear_dims &d, bool back) {
     LinPlan p = {};
     p.vec = d.rows <= LIN_VEC_ROWS;
     p.tc = !p.vec && d.dtype == EAGA_BF16;
-    p.split = {1, 0};
+    p.split = {1, 0, {}};
     size_t off = 256;                                // the status word
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -144,7 +144,7 @@ static LinPlan lin_plan(const eaga_linear_dims &d, bool back) {
         p.zparts = dact ? 3 : 1;
         if (back && (dact || p.ldz != d.out))
             for (int k = 0; k < p.zparts; ++k) p.dZ[k] = take(rows * p.ldz * 2);
-        if (back) p.split = lin_tc_dw_split(d.rows, d.in, d.out);
+        if (back) p.split = lin_tc_dw_split(d.rows, d.in, d.out, p.zparts);
     } else if (!p.vec && back) {
         if (dact) p.dZ32 = take(rows * out * 4);
         p.split = lin_f32_dw_split(d.rows, d.in, d.out);

@@ -105,10 +105,16 @@ struct LinEpi {
     int act;
 };
 
+// Output tiles: 256 x 256 on a pair of CTAs, or 128 x bn on one.
+struct LinTile {
+    bool pair;
+    int bn;
+};
 // Split of a weight gradient's reduction over rows into parts of `chunk` rows.
 struct LinSplit {
     int splits;
     long long chunk;
+    LinTile tile;              // tensor cores only
 };
 
 // tcgen05 products of bf16 operands whose rows are ld elements long (a multiple of 8), zero past the true
@@ -129,7 +135,7 @@ cudaError_t lin_tc_forward(const LinTc &p, const LinEpi<T> &e, cudaStream_t st);
 template <typename T>
 cudaError_t lin_tc_dx(const LinTc &p, const LinEpi<T> &e, cudaStream_t st);
 // dW (and db, where not null) or, with more than one split, the splits' partial sums [splits][in][out] (and [splits][out]).
-LinSplit lin_tc_dw_split(long long rows, int in, int out);
+LinSplit lin_tc_dw_split(long long rows, int in, int out, int nseg);
 cudaError_t lin_tc_dw(const LinTc &p, const LinSplit &s, float *dW, float *db, cudaStream_t st);
 
 // CUDA-core products of fp32 operands of any size; partial sums as above.

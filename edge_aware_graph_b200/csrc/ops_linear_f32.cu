@@ -164,7 +164,7 @@ LinSplit lin_f32_dw_split(long long rows, int in, int out) {
     long long s = std::max(1LL, 4LL * sm_count() / tiles);
     s = std::max(1LL, std::min(s, rows / 256));
     const long long chunk = std::max(1LL, ((rows + s - 1) / s + LF_BK - 1) / LF_BK) * LF_BK;
-    return {(int)std::max(1LL, (rows + chunk - 1) / chunk), chunk};
+    return {(int)std::max(1LL, (rows + chunk - 1) / chunk), chunk, {}};
 }
 cudaError_t lin_f32_dw(const LinF32 &q, const LinSplit &s, float *dW, float *db, cudaStream_t st) {
     LfParams p = {};

@@ -4,30 +4,50 @@
 //   dX        dX = f(dZ W^T)   A = dZ [rows, out] K-major    B = W  [in, out]   K-major  (the reduction is out)
 //   dW        dW = X^T dZ      A = X  [rows, in]  MN-major   B = dZ [rows, out] MN-major (the reduction is rows)
 //
-// so every operand is read as it lies in memory.  A persistent CTA takes 128 x
-// BN output tiles: a TMA warp fills a ring of 64-deep operand tiles (128-byte
-// swizzled), one thread of the next warp issues the MMAs into one of two fp32
-// accumulators in TMEM, and eight warps drain the other one, so the epilogue
-// of a tile hides behind the next tile's products.  The drain goes through a
-// small staging tile per warp, in fp32, so that bias, activation, residual and
-// the stores see rows in 16-byte pieces, and every output is rounded once.
+// so every operand is read as it lies in memory.  Persistent CTAs take output
+// tiles: a TMA warp fills a ring of 64-deep operand tiles (128-byte swizzled),
+// one thread of the next warp issues the MMAs into one of two fp32 accumulators
+// in TMEM, and eight warps drain the other one, so the epilogue of a tile hides
+// behind the next tile's products.
+//
+// Large products (CG = 2) run on pairs of CTAs: a 256 x 256 tile, of which each
+// CTA keeps 128 rows of A and 128 columns of B in its shared memory and 128 rows
+// of sums in its TMEM.  A pair loads 64 KB for 2 x 256 x 256 x 64 operations, half
+// of what two 128 x 256 tiles would: what bounds the single form is the
+// shared memory's and L2's traffic, not the tensor cores.  Small ones (CG = 1)
+// take 128 x 128 or 128 x 64 tiles.
+//
+// Epilogue: a lane holds a row; bias, activation, slope and residual work on
+// registers; residual and Zin come, and the outputs go, by TMA through one small
+// swizzled tile a warp and tensor, so global memory sees whole rows of 64 or 128
+// bytes.  Every output is rounded once.  Outputs whose rows do not begin on 16
+// bytes (VEC = false) take a plain path.
+//
+// The tensor cores add with truncation: a chain of n products of 16 is off by up
+// to n steps of fp32, all in one direction (measured 1e-6 relative after 1024
+// rows, 1.9e-5 after 16384).  fp32 results (PROMO) therefore leave the accumulator
+// every 512 steps of the reduction for a sum in registers, rounded to nearest.
 //
 // A weight gradient reduces over rows, of which there may be a million for a
 // 64 x 128 result: its tiles are split over rows, the splits' sums are added
 // in a fixed order by the caller's reduction.  The bias gradient, the column
-// sums of dZ, comes from the dZ tiles in shared memory: two more warps multiply
-// them with a matrix of ones (warp-level MMAs, joined in fp32 after every 64 rows),
-// in the CTAs of the first row of tiles, so dZ is not read again.
+// sums of dZ, comes from two more warps, for the first row of tiles: from the dZ
+// tiles in shared memory times a matrix of ones (warp-level MMAs, joined in fp32
+// after every 64 rows), or, on pairs, where the barriers are the first CTA's, from
+// dZ itself, which the tiles' loads have just brought into L2.
 //
 // An operand in fp32 comes as bf16 parts (two carry 16 bits of it, three 24):
 // the products of parts are segments of one longer reduction, the smallest first.
 #include <algorithm>
+#include <type_traits>
 #include "ops_linear.h"
 #include "sm100.cuh"
 
 namespace eaga {
 namespace fast {
 bool encode_2d(CUtensorMap *m, const void *base, int rows, int cols, int box_rows);
+bool encode_3d(CUtensorMap *m, const void *base, bool f32, long long planes, long long rows, long long cols, int box_cols,
+               int box_rows);
 }
 namespace ops {
 
@@ -38,28 +58,46 @@ typedef __nv_bfloat16 bf16;
 constexpr int LT_BM = 128, LT_BK = 64;
 constexpr int LT_EPI = 8;                              // epilogue warps: two a TMEM quadrant
 constexpr int LT_THR = 32 * (4 + LT_EPI);              // TMA, MMA, two column-sum warps, epilogue
+constexpr int LT_PROMO = 8;                            // 64-deep steps an accumulator of an fp32 result takes
 
-template <int BN>
-struct LtSmem {
-    static constexpr uint32_t A_BYTES = LT_BM * LT_BK * 2, B_BYTES = BN * LT_BK * 2, STAGE = A_BYTES + B_BYTES;
-    static constexpr int ST = BN == 256 ? 4 : BN == 128 ? 6 : 8;
-    static constexpr uint32_t EPI = ST * STAGE;                      // staging, 4 KB a warp
-    static constexpr uint32_t BAR = EPI + LT_EPI * 4096;             // full[ST], empty[ST], acc_full[2], acc_empty[2], drained
-    static constexpr uint32_t TM = BAR + (2 * ST + 5) * 8;
+// Registers of a pair's CTA with 128 sums a lane in the epilogue: 384 threads launched with 168 each; the four
+// other warps keep 88, the eight epilogue warps get 208 (128 x 88 + 256 x 208 = 384 x 168).
+constexpr int LT_REGS = 168, LT_REGS_LOW = 88, LT_REGS_EPI = 208;
+static_assert(128 * LT_REGS_LOW + 256 * LT_REGS_EPI <= LT_THR * LT_REGS, "register split");
+
+template <int KIND, int BN, int CG, typename TO, bool VEC>
+struct Lt {
+    static constexpr int BM = LT_BM * CG, PB = BN / CG;              // the tile's rows; B columns a CTA holds
+    static constexpr bool PROMO = KIND == LIN_DW || sizeof(TO) == 4;
+    static constexpr int HALF = BN / 2;                              // columns of an epilogue warp
+    static constexpr int PC = VEC ? (128 / (int)sizeof(TO) < HALF ? 128 / (int)sizeof(TO) : HALF) : 32;   // a piece's columns
+    static constexpr int PIECES = HALF / PC;
+    static constexpr uint32_t A_BYTES = LT_BM * LT_BK * 2, B_BYTES = PB * LT_BK * 2, STAGE = A_BYTES + B_BYTES;
+    static constexpr uint32_t SLOT = VEC ? 32 * PC * sizeof(TO) : 4096;
+    static constexpr int SLOTS = KIND == LIN_DW ? 2 : 3;             // two for the output in turn (in it the residual), one for Z or Zin
+    static constexpr uint32_t RING = 232448 - 1024 - 512 - LT_EPI * SLOTS * SLOT;
+    static constexpr int ST = RING / STAGE < 8 ? RING / STAGE : 8;
+    static constexpr uint32_t EPI = ST * STAGE;
+    static constexpr uint32_t BAR = EPI + LT_EPI * SLOTS * SLOT;     // full[ST], empty[ST], acc_full[2], acc_empty[2], drained, slots' [EPI][3]
+    static constexpr uint32_t TM = BAR + (2 * ST + 5 + 3 * LT_EPI) * 8;
     static constexpr uint32_t FAIL = TM + 4;
-    static constexpr uint32_t BYTES = FAIL + 12 + 1024;
-    static_assert(BYTES <= 232448, "shared memory");
+    static constexpr uint32_t SUM = FAIL + 4;
+    static constexpr uint32_t BYTES = SUM + 8 + 1024;
+    static_assert(ST >= 3 && BYTES <= 232448, "shared memory");
 };
 
-// Maps of the operands' parts.
+// Maps of the operands' parts, the outputs and the epilogue's inputs.
 struct LtMaps {
     CUtensorMap a[3], b[3];
+    CUtensorMap out, out2, add, zin;
 };
 
 template <typename TO>
 struct LtParams {
     LinEpi<TO> e;
     float *acc, *db;           // weight gradient: fp32 sums [split][M][N], [split][N]
+    const bf16 *dz[3];         // on pairs, for db: dZ's parts, their row length
+    int ldz, rows;
     int *status;
     int M, N;                  // output
     int kts;                   // forward, dX: 64-deep steps a segment; weight gradient: those of all rows
@@ -67,15 +105,16 @@ struct LtParams {
     uint32_t seg;              // four bits a segment: A's part, B's part
     int tiles_m, tiles_n, units;
     int per;                   // weight gradient: a split's steps
-    int vec, clear;
+    int clear;
 };
 
-template <int KIND, int BN, typename TO>
+template <int KIND, int BN, int CG, typename TO, bool VEC>
 __global__ void __launch_bounds__(LT_THR, 1)
-k_lin_tc(const __grid_constant__ LtMaps maps, const LtParams<TO> p) {
-    using S = LtSmem<BN>;
-    constexpr int ST = S::ST;
-    constexpr bool A_MN = KIND == LIN_DW, B_MN = KIND != LIN_DX;
+k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<TO> p) {
+    using S = Lt<KIND, BN, CG, TO, VEC>;
+    constexpr int ST = S::ST, PC = S::PC, PIECES = S::PIECES;
+    constexpr bool A_MN = KIND == LIN_DW, B_MN = KIND != LIN_DX, PAIR = CG == 2, PROMO = S::PROMO;
+    constexpr bool SMEM_SUMS = KIND == LIN_DW && !PAIR;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t *sp = smem_raw + (sbase - smem_u32(smem_raw));
@@ -87,30 +126,39 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const LtParams<TO> p) {
     auto acc_full = [&](int b) { return bar0 + 8 * (2 * ST + b); };
     auto acc_empty = [&](int b) { return bar0 + 8 * (2 * ST + 2 + b); };
     const uint32_t drained = bar0 + 8 * (2 * ST + 4);
+    const int rank = PAIR ? (int)cluster_rank() : 0;
+    const int first = blockIdx.x / CG, stride = gridDim.x / CG;
 
     if (tid == 0) {
         for (int s = 0; s < ST; ++s) {
             mbar_init(full(s), 1);
-            mbar_init(empty(s), KIND == LIN_DW ? 3 : 1);     // the MMAs; two column-sum warps
+            mbar_init(empty(s), SMEM_SUMS ? 3 : 1);          // the MMAs; two column-sum warps
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(acc_full(b), 1);
-            mbar_init(acc_empty(b), LT_EPI);
+            mbar_init(acc_empty(b), LT_EPI * CG);
         }
         mbar_init(drained, 1);
+        for (int k = 0; k < 3 * LT_EPI; ++k) mbar_init(drained + 8 + 8 * k, 1);
         fence_mbar_init();
         *fail = 0;
         if (p.clear && blockIdx.x == 0) *p.status = 0;       // a wait that gives up does so a second later
     }
     if (w == 1) {
-        tmem_alloc(sbase + S::TM, 2 * BN);
-        tmem_relinquish();
+        if constexpr (PAIR) {
+            tmem_alloc_pair(sbase + S::TM, 2 * BN);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(sbase + S::TM, 2 * BN);
+            tmem_relinquish();
+        }
     }
     tc_fence_before();
     __syncthreads();
+    if constexpr (PAIR) cluster_sync_all();                  // the other CTA's barriers are there
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sp + S::TM);
-
+    constexpr bool REGS = PAIR && PROMO;
     // unit -> output tile (columns fastest), split, its steps
     struct Unit {
         int m0, n0, split, k0, steps, tm;
@@ -119,250 +167,540 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const LtParams<TO> p) {
         Unit r;
         const int tiles = p.tiles_m * p.tiles_n;
         r.split = KIND == LIN_DW ? u / tiles : 0;
-        const int t = KIND == LIN_DW ? u % tiles : u;
+        const int t = KIND == LIN_DW ? u - r.split * tiles : u;
         r.tm = t / p.tiles_n;
-        r.m0 = r.tm * LT_BM;
-        r.n0 = (t % p.tiles_n) * BN;
+        r.m0 = r.tm * S::BM + rank * LT_BM;                  // this CTA's rows
+        r.n0 = (t - r.tm * p.tiles_n) * BN;
         r.k0 = KIND == LIN_DW ? r.split * p.per : 0;
         r.steps = KIND == LIN_DW ? min(p.per, p.kts - r.k0) : p.kts;
         return r;
     };
 
-    if (w == 0) {
-        if (lane == 0) {
-            int it = 0, issued = 0;
-            bool ok = true;
-            for (int u = blockIdx.x; ok && u < p.units; u += gridDim.x) {
-                const Unit t = unit_of(u);
-                for (int seg = 0; ok && seg < p.nseg; ++seg) {
-                    const uint32_t parts = p.seg >> (4 * seg);
-                    const CUtensorMap *am = &maps.a[parts & 3], *bm = &maps.b[(parts >> 2) & 3];
-                    for (int k = 0; k < t.steps; ++k, ++it) {
-                        const int s = it % ST, kk = (t.k0 + k) * LT_BK;
-                        if (!cta_wait(empty(s), ((it / ST) & 1) ^ 1, fail, p.status)) { ok = false; break; }
-                        const uint32_t st = sbase + s * S::STAGE;
-                        mbar_expect_tx(full(s), S::STAGE);
-                        if constexpr (A_MN) {
-                            tma_load_2d(st, am, full(s), t.m0, kk);
-                            tma_load_2d(st + 8192, am, full(s), t.m0 + 64, kk);
-                        } else {
-                            tma_load_2d(st, am, full(s), kk, t.m0);
-                        }
-                        if constexpr (B_MN) {
+    if (w < 4) {
+        if constexpr (REGS) regs_dec<LT_REGS_LOW>();
+        if (w == 0) {
+            if (lane == 0) {
+                int it = 0, issued = 0;
+                bool ok = true;
+                for (int u = first; ok && u < p.units; u += stride) {
+                    const Unit t = unit_of(u);
+                    const int nb = t.n0 + rank * S::PB;          // this CTA's columns of B
+                    for (int seg = 0; ok && seg < p.nseg; ++seg) {
+                        const uint32_t parts = p.seg >> (4 * seg);
+                        const CUtensorMap *am = &maps.a[parts & 3], *bm = &maps.b[(parts >> 2) & 3];
+                        for (int k = 0; k < t.steps; ++k, ++it) {
+                            const int s = it % ST, kk = (t.k0 + k) * LT_BK;
+                            if (!cta_wait(empty(s), ((it / ST) & 1) ^ 1, fail, p.status)) { ok = false; break; }
+                            const uint32_t st = sbase + s * S::STAGE;
+                            const uint32_t bar = PAIR ? cluster_map(full(s), 0) : full(s);
+                            if (rank == 0) mbar_expect_tx(full(s), S::STAGE * CG);
+                            auto load = [&](uint32_t dst, const CUtensorMap *m, int c0, int c1) {
+                                if constexpr (PAIR) tma_load_2d_pair(dst, m, bar, c0, c1);
+                                else tma_load_2d(dst, m, bar, c0, c1);
+                            };
+                            if constexpr (A_MN) {
+                                load(st, am, t.m0, kk);
+                                load(st + 8192, am, t.m0 + 64, kk);
+                            } else {
+                                load(st, am, kk, t.m0);
+                            }
+                            if constexpr (B_MN) {
 #pragma unroll
-                            for (int h = 0; h < BN / 64; ++h)
-                                tma_load_2d(st + S::A_BYTES + h * 8192, bm, full(s), t.n0 + 64 * h, kk);
-                        } else {
-                            tma_load_2d(st + S::A_BYTES, bm, full(s), kk, t.n0);
+                                for (int h = 0; h < S::PB / 64; ++h) load(st + S::A_BYTES + h * 8192, bm, nb + 64 * h, kk);
+                            } else {
+                                load(st + S::A_BYTES, bm, kk, nb);
+                            }
+                            issued = it + 1;
                         }
-                        issued = it + 1;
                     }
                 }
+                // After a wait that gave up: what was issued lands before the CTA's memory is released.  (Of a pair the first
+                // CTA's barriers count both CTAs' loads, and the two leave together.)
+                if (!ok && rank == 0)
+                    for (int i = max(issued - ST, 0); i < issued; ++i) mbar_wait(full(i % ST), (i / ST) & 1);
             }
-            if (!ok)                                // what was issued lands before the CTA's memory is released
-                for (int i = max(issued - ST, 0); i < issued; ++i) mbar_wait(full(i % ST), (i / ST) & 1);
-        }
-    } else if (w == 1) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = idesc_bf16_f32(LT_BM, BN) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
-            int it = 0, n = 0;
-            bool ok = true;
-            for (int u = blockIdx.x; ok && u < p.units; u += gridDim.x, ++n) {
-                const Unit t = unit_of(u);
-                const int b = n & 1, nk = t.steps * p.nseg;
-                if (!cta_wait(acc_empty(b), ((n >> 1) & 1) ^ 1, fail, p.status)) { ok = false; break; }
-                tc_fence_after();
-                const uint32_t d = tmem + b * BN;
-                const bool sums = KIND == LIN_DW && p.db != nullptr && t.tm == 0;
-                for (int k = 0; k < nk; ++k, ++it) {
-                    const int s = it % ST;
-                    if (!cta_wait(full(s), (it / ST) & 1, fail, p.status)) { ok = false; break; }
-                    tc_fence_after();
-                    const uint32_t st = sbase + s * S::STAGE;
+        } else if (w == 1) {
+            if (lane == 0 && rank == 0) {
+                constexpr uint32_t idesc = idesc_bf16_f32(S::BM, BN) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
+                int it = 0, n = 0;                               // steps; accumulators
+                bool ok = true;
+                for (int u = first; ok && u < p.units; u += stride) {
+                    const Unit t = unit_of(u);
+                    const int nk = t.steps * p.nseg;
+                    const bool sums = SMEM_SUMS && p.db != nullptr && t.tm == 0;
+                    for (int k0 = 0; ok && k0 < nk; ++n) {
+                        const int b = n & 1, k1 = PROMO ? min(k0 + LT_PROMO, nk) : nk;
+                        if (!cta_wait(acc_empty(b), ((n >> 1) & 1) ^ 1, fail, p.status)) { ok = false; break; }
+                        tc_fence_after();
+                        const uint32_t d = tmem + b * BN;
+                        for (int k = k0; k < k1; ++k, ++it) {
+                            const int s = it % ST;
+                            if (!cta_wait(full(s), (it / ST) & 1, fail, p.status)) { ok = false; break; }
+                            tc_fence_after();
+                            const uint32_t st = sbase + s * S::STAGE;
 #pragma unroll
-                    for (int kk = 0; kk < LT_BK / 16; ++kk)
-                        mma_bf16_ss(d,
-                                    A_MN ? smem_desc(st + kk * 2048, 8192, 1024, LAYOUT_SW128)
-                                         : smem_desc(st + kk * 32, 16, 1024, LAYOUT_SW128),
-                                    B_MN ? smem_desc(st + S::A_BYTES + kk * 2048, 8192, 1024, LAYOUT_SW128)
-                                         : smem_desc(st + S::A_BYTES + kk * 32, 16, 1024, LAYOUT_SW128),
-                                    idesc, (k > 0 || kk > 0) ? 1u : 0u);
-                    mma_commit(empty(s));
-                    if (KIND == LIN_DW && !sums) {  // no column sums: their two arrivals
-                        mbar_arrive(empty(s));
-                        mbar_arrive(empty(s));
+                            for (int kk = 0; kk < LT_BK / 16; ++kk) {
+                                const uint64_t ad = A_MN ? smem_desc(st + kk * 2048, 8192, 1024, LAYOUT_SW128)
+                                                         : smem_desc(st + kk * 32, 16, 1024, LAYOUT_SW128);
+                                const uint64_t bd = B_MN ? smem_desc(st + S::A_BYTES + kk * 2048, 8192, 1024, LAYOUT_SW128)
+                                                         : smem_desc(st + S::A_BYTES + kk * 32, 16, 1024, LAYOUT_SW128);
+                                const uint32_t more = k > k0 || kk > 0 ? 1u : 0u;
+                                if constexpr (PAIR) mma_bf16_ss_pair(d, ad, bd, idesc, more);
+                                else mma_bf16_ss(d, ad, bd, idesc, more);
+                            }
+                            if constexpr (PAIR) mma_commit_pair(empty(s), 3);
+                            else mma_commit(empty(s));
+                            if (SMEM_SUMS && !sums) {            // no column sums: their two arrivals
+                                mbar_arrive(empty(s));
+                                mbar_arrive(empty(s));
+                            }
+                        }
+                        if (ok) {
+                            if constexpr (PAIR) mma_commit_pair(acc_full(b), 3);
+                            else mma_commit(acc_full(b));
+                        }
+                        k0 = k1;
                     }
                 }
-                if (ok) mma_commit(acc_full(b));
-            }
-            if (!ok) {                              // the products in flight end before TMEM is freed
-                mma_commit(drained);
-                mbar_wait(drained, 0);
-            }
-        }
-    } else if (w < 4) {
-        if constexpr (KIND == LIN_DW) {
-            // column sums of the dZ tile: ones [16 x 16] times [16 rows x 8 columns] at a time
-            constexpr int COLS = BN / 2, NT = COLS / 8;        // this warp's columns
-            const uint32_t ones[4] = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
-            const int c0 = (w - 2) * COLS;
-            int it = 0;
-            bool ok = true;
-            for (int u = blockIdx.x; ok && u < p.units; u += gridDim.x) {
-                const Unit t = unit_of(u);
-                const int nk = t.steps * p.nseg;
-                if (p.db == nullptr || t.tm != 0) {
-                    it += nk;
-                    continue;
+                if (!ok) {                                       // the products in flight end before TMEM is freed
+                    if constexpr (PAIR) mma_commit_pair(drained, 1);
+                    else mma_commit(drained);
+                    mbar_wait(drained, 0);
                 }
-                float sum[NT][2];
+            }
+        } else if (w < 4) {
+            if constexpr (SMEM_SUMS) {
+                // column sums of the dZ tile: ones [16 x 16] times [16 rows x 8 columns] at a time
+                constexpr int COLS = BN / 2, NT = COLS / 8;        // this warp's columns
+                const uint32_t ones[4] = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
+                const int c0 = (w - 2) * COLS;
+                int it = 0;
+                bool ok = true;
+                for (int u = first; ok && u < p.units; u += stride) {
+                    const Unit t = unit_of(u);
+                    const int nk = t.steps * p.nseg;
+                    if (p.db == nullptr || t.tm != 0) {
+                        it += nk;
+                        continue;
+                    }
+                    float sum[NT][2];
 #pragma unroll
-                for (int j = 0; j < NT; ++j) sum[j][0] = sum[j][1] = 0.f;
-                for (int k = 0; k < nk; ++k, ++it) {
-                    const int s = it % ST;
-                    ok = __all_sync(0xffffffffu, cta_wait(full(s), (it / ST) & 1, fail, p.status));
-                    if (!ok) break;
-                    const uint32_t bt = sbase + s * S::STAGE + S::A_BYTES;
+                    for (int j = 0; j < NT; ++j) sum[j][0] = sum[j][1] = 0.f;
+                    for (int k = 0; k < nk; ++k, ++it) {
+                        const int s = it % ST;
+                        ok = __all_sync(0xffffffffu, cta_wait(full(s), (it / ST) & 1, fail, p.status));
+                        if (!ok) break;
+                        const uint32_t bt = sbase + s * S::STAGE + S::A_BYTES;
 #pragma unroll
-                    for (int j = 0; j < NT; j += 2) {
-                        float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
+                        for (int j = 0; j < NT; j += 2) {
+                            float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int kk = 0; kk < LT_BK; kk += 16) {
-                            // four 8 x 8 matrices: rows kk.., kk + 8.. of columns j, then of columns j + 1
-                            const uint32_t row = kk + (lane & 7) + 8 * ((lane >> 3) & 1), col = c0 + 8 * (j + (lane >> 4));
-                            uint32_t f[4];
-                            ldsm_x4_t(bt + (col >> 6) * 8192 + fast::sw128(row, (col >> 3) & 7), f);
-                            mma16816(d0, ones, f[0], f[1]);
-                            mma16816(d1, ones, f[2], f[3]);
+                            for (int kk = 0; kk < LT_BK; kk += 16) {
+                                // four 8 x 8 matrices: rows kk.., kk + 8.. of columns j, then of columns j + 1
+                                const uint32_t row = kk + (lane & 7) + 8 * ((lane >> 3) & 1), col = c0 + 8 * (j + (lane >> 4));
+                                uint32_t f[4];
+                                ldsm_x4_t(bt + (col >> 6) * 8192 + fast::sw128(row, (col >> 3) & 7), f);
+                                mma16816(d0, ones, f[0], f[1]);
+                                mma16816(d1, ones, f[2], f[3]);
+                            }
+                            sum[j][0] += d0[0]; sum[j][1] += d0[1];
+                            sum[j + 1][0] += d1[0]; sum[j + 1][1] += d1[1];
                         }
-                        sum[j][0] += d0[0]; sum[j][1] += d0[1];
-                        sum[j + 1][0] += d1[0]; sum[j + 1][1] += d1[1];
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(empty(s));
+                    }
+                    if (ok && lane < 4) {               // row 0 of the product: columns 2 lane, 2 lane + 1 of each 8
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) {
+                            const int c = t.n0 + c0 + 8 * j + 2 * lane;
+                            float *o = p.db + (size_t)t.split * p.N + c;
+                            if (c < p.N) o[0] = sum[j][0];
+                            if (c + 1 < p.N) o[1] = sum[j][1];
+                        }
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(empty(s));
                 }
-                if (ok && lane < 4) {               // row 0 of the product: columns 2 lane, 2 lane + 1 of each 8
+            } else if constexpr (KIND == LIN_DW) {
+                // column sums of dZ from memory: a warp 64 columns, 8 a lane, four rows at a time
+                for (int u = first; p.db != nullptr && u < p.units; u += stride) {
+                    const Unit t = unit_of(u);
+                    if (t.tm != 0) continue;
+                    const int c = t.n0 + rank * S::PB + (w - 2) * 64 + 8 * (lane & 7);
+                    const long long r0 = (long long)t.k0 * LT_BK, r1 = min((long long)p.rows, r0 + (long long)t.steps * LT_BK);
+                    float sum[8];
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        const int c = t.n0 + c0 + 8 * j + 2 * lane;
-                        float *o = p.db + (size_t)t.split * p.N + c;
-                        if (c < p.N) o[0] = sum[j][0];
-                        if (c + 1 < p.N) o[1] = sum[j][1];
+                    for (int j = 0; j < 8; ++j) sum[j] = 0.f;
+                    if (c < p.ldz) {
+                        for (int seg = 0; seg < p.nseg; ++seg) {
+                            const bf16 *z = p.dz[(p.seg >> (4 * seg + 2)) & 3] + c;
+#pragma unroll 8
+                            for (long long r = r0 + (lane >> 3); r < r1; r += 4) {
+                                float v[8];
+                                lin_ld8(z + r * p.ldz, 8, true, v);
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) sum[j] += v[j];
+                            }
+                        }
                     }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 8);
+                        sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 16);
+                    }
+                    if (lane < 8) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (c + j < p.N) p.db[(size_t)t.split * p.N + c + j] = sum[j];
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
         }
     } else {
-        const int q = w & 3, half = (w - 4) >> 2;   // TMEM quadrant: rows 32 q ..; columns: every other 32
-        const uint32_t stg = sbase + S::EPI + (w - 4) * 4096;
-        const uint8_t *stage = sp + S::EPI + (w - 4) * 4096;
+        if constexpr (REGS) regs_inc<LT_REGS_EPI>();
+        const int q = w & 3, half = (w - 4) >> 2, ew = w - 4;   // TMEM quadrant: rows 32 q ..; the tile's columns: half
+        const uint32_t slots = sbase + S::EPI + ew * S::SLOTS * S::SLOT;
+        const uint8_t *slots_p = sp + S::EPI + ew * S::SLOTS * S::SLOT;
+        const uint32_t slot_bar = drained + 8 + 24 * ew;
+        const bool has_add = VEC && KIND != LIN_DW && p.e.add != nullptr, has_zin = VEC && KIND == LIN_DX && p.e.zin != nullptr;
+        const bool has_z = VEC && KIND == LIN_FWD && p.e.out2 != nullptr;
+        const bool two = has_add && has_zin;        // Zin goes to the third slot where the residual has the output's
+        auto swz = [](uint32_t row, uint32_t ch) { return S::SLOT == 4096 ? fast::sw128(row, ch) : fast::sw64(row, ch); };
+        // the pieces with something in them, in order
+        auto some = [&](const Unit &t, int c) { return t.m0 + 32 * q < p.M && t.n0 + half * S::HALF + c * PC < p.N; };
+        struct Place {
+            int u, c;
+        };
+        auto seek = [&](Place x) {                  // the first such piece from x on
+            while (x.u < p.units) {
+                const Unit t = unit_of(x.u);
+                if (some(t, x.c)) break;
+                x = {x.u + stride, 0};
+            }
+            return x;
+        };
+        auto after = [&](Place x) { return seek(x.c + 1 < PIECES ? Place{x.u, x.c + 1} : Place{x.u + stride, 0}); };
+        // ask for the inputs of a piece, the k-th of this warp (lane 0; the slot's last store has been read)
+        auto ask = [&](Place x, int k, bool side) {
+            if (x.u >= p.units) return;
+            const Unit t = unit_of(x.u);
+            const int col = t.n0 + half * S::HALF + x.c * PC, row = t.m0 + 32 * q;
+            const int s = side ? 2 : k & 1;
+            mbar_expect_tx(slot_bar + 8 * s, S::SLOT);
+            tma_load_3d(slots + s * S::SLOT, side || !has_add ? &maps.zin : &maps.add, slot_bar + 8 * s, col, row, 0);
+        };
+        int k = 0;                                  // pieces of this warp so far
+        if constexpr (VEC && KIND != LIN_DW) {
+            if (lane == 0 && (has_add || has_zin)) {
+                const Place x = seek({first, 0});
+                ask(x, 0, false);
+                if (two) ask(x, 0, true);
+            }
+            __syncwarp();
+        }
         int n = 0;
-        for (int u = blockIdx.x; u < p.units; u += gridDim.x, ++n) {
+        bool ok = true;
+        for (int u = first; ok && u < p.units; u += stride) {
             const Unit t = unit_of(u);
-            const int b = n & 1;
-            const bool ok = __all_sync(0xffffffffu, cta_wait(acc_full(b), (n >> 1) & 1, fail, p.status));
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll 1
-            for (int c0 = 32 * half; c0 < BN; c0 += 64) {
-                __syncwarp();                       // lanes without columns are back; the last chunk's reads are done
-                float v[32];
-                const uint32_t ta = tmem + b * BN + ((uint32_t)(32 * q) << 16) + c0;
-                tmem_ld16(ta, *reinterpret_cast<float(*)[16]>(v));
-                tmem_ld16(ta + 16, *reinterpret_cast<float(*)[16]>(v + 16));
-                tmem_ld_wait();
-                if (c0 + 64 >= BN) {                // the last read: the accumulator may be written again
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(acc_empty(b));
-                }
-                const int n0 = t.n0 + c0;
-                if (n0 >= p.N || t.m0 + 32 * q >= p.M) continue;
-#pragma unroll
-                for (int ch = 0; ch < 8; ++ch) {
-                    const uint32_t a = stg + fast::sw128(lane, ch);
-                    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v[4 * ch]), "f"(v[4 * ch + 1]),
-                                 "f"(v[4 * ch + 2]), "f"(v[4 * ch + 3])
-                                 : "memory");
-                }
+            const int nk = t.steps * p.nseg, chunks = PROMO ? (nk + LT_PROMO - 1) / LT_PROMO : 1;
+            float acc[PROMO ? S::HALF : 1] = {};
+            auto released = [&](int b) {            // the accumulator may be written again
+                tc_fence_before();
                 __syncwarp();
-                // 4 lanes a row, 8 columns each; 8 rows at a time
-                const int cl = lane & 3, col = n0 + 8 * cl, have = min(8, p.N - col);
-                if (have <= 0) continue;
-                const bool vec = p.vec && (have == 8 || KIND == LIN_DW || sizeof(TO) == 4);
-                float bias[8];
-                if constexpr (KIND == LIN_FWD) {
-                    if (p.e.bias) {
-                        lin_ld8(p.e.bias + col, have, vec, bias);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) bias[j] = 0.f;
-                    }
+                if (lane == 0) {
+                    if constexpr (PAIR) mbar_arrive_cluster(cluster_map(acc_empty(b), 0));
+                    else mbar_arrive(acc_empty(b));
                 }
+            };
+            for (int ch = 0; ch < chunks; ++ch, ++n) {
+                const int b = n & 1;
+                ok = __all_sync(0xffffffffu, cta_wait(acc_full(b), (n >> 1) & 1, fail, p.status));
+                if (!ok) break;
+                tc_fence_after();
+                if constexpr (PROMO) {
+                    const uint32_t ta = tmem + b * BN + ((uint32_t)(32 * q) << 16) + half * S::HALF;
 #pragma unroll
-                for (int r8 = 0; r8 < 4; ++r8) {
-                    const int rl = 8 * r8 + (lane >> 2), row = t.m0 + 32 * q + rl;
-                    if (row >= p.M) break;
-                    const float4 x0 = *reinterpret_cast<const float4 *>(stage + fast::sw128(rl, 2 * cl));
-                    const float4 x1 = *reinterpret_cast<const float4 *>(stage + fast::sw128(rl, 2 * cl + 1));
-                    float y[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-                    const size_t at = (size_t)row * p.N + col;
-                    if constexpr (KIND == LIN_DW) {
-                        lin_st8(p.acc + (size_t)t.split * p.M * p.N + at, have, vec, y);
-                    } else {
-                        float o[8];
-                        if constexpr (KIND == LIN_FWD) {
+                    for (int c = 0; c < S::HALF; c += 32) {
+                        float v[32];
+                        tmem_ld32(ta + c, v);
+                        tmem_ld_wait();
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) y[j] += bias[j];
-                            if (p.e.out2) lin_st8(p.e.out2 + at, have, vec, y);
-                            act_apply(y, p.e.act);
-                        } else if (p.e.zin) {
-                            lin_ld8(p.e.zin + at, have, vec, o);
-                            act_slope_mul(y, o, p.e.act);
-                        }
-                        if (p.e.add) {
-                            lin_ld8(p.e.add + at, have, vec, o);
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) y[j] += o[j];
-                        }
-                        lin_st8(p.e.out + at, have, vec, y);
+                        for (int j = 0; j < 32; ++j) acc[c + j] += v[j];
                     }
+                    released(b);
                 }
             }
+            if (!ok) break;
+            const int b = (n - 1) & 1;
+            const int row0 = t.m0 + 32 * q;
+            auto piece = [&](int c, float (&v)[PC]) {
+                const int col = t.n0 + half * S::HALF + c * PC;
+                if (row0 >= p.M || col >= p.N) return;
+                if constexpr (VEC) {
+                    const int s = k & 1;
+                    if constexpr (KIND != LIN_DW) {
+                        if (has_add || has_zin) {
+                            // the next piece's inputs, into the other slot: its store (the last piece's) has been read by now
+                            if (lane == 0) {
+                                tma_store_wait_read0();
+                                ask(after({u, c}), k + 1, false);
+                            }
+                            __syncwarp();
+                            ok = __all_sync(0xffffffffu, cta_wait(slot_bar + 8 * s, (k >> 1) & 1, fail, p.status));
+                            if (two) ok = ok && __all_sync(0xffffffffu, cta_wait(slot_bar + 16, k & 1, fail, p.status));
+                            if (!ok) return;
+                        }
+                    }
+                    if (!(has_add || has_zin)) {
+                        // a slot is free when all stores but the last piece's have been read; Z's slot when that one has, too
+                        if (lane == 0) {
+                            if (has_z) tma_store_wait_read0();
+                            else tma_store_wait_read1();
+                        }
+                        __syncwarp();
+                    }
+                    const uint32_t io = slots + s * S::SLOT, side = slots + 2 * S::SLOT;
+                    const uint8_t *iop = slots_p + s * S::SLOT, *sidep = slots_p + (two ? 2 : s) * S::SLOT;
+                    constexpr int PER = 16 / sizeof(TO);        // columns of a 16-byte chunk
+                    auto put = [&](uint32_t base) {
+#pragma unroll
+                        for (int x = 0; x < PC / PER; ++x) {
+                            uint32_t o[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                if constexpr (sizeof(TO) == 2) o[j] = pack_bf16(v[x * 8 + 2 * j], v[x * 8 + 2 * j + 1]);
+                                else o[j] = __float_as_uint(v[x * 4 + j]);
+                            }
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(base + swz(lane, x)), "r"(o[0]), "r"(o[1]),
+                                         "r"(o[2]), "r"(o[3])
+                                         : "memory");
+                        }
+                    };
+                    auto get = [&](const uint8_t *base, int x, float (&f)[PER]) {
+                        const uint4 a = *reinterpret_cast<const uint4 *>(base + swz(lane, x));
+                        const uint32_t y[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if constexpr (sizeof(TO) == 2) {
+                                f[2 * j] = __uint_as_float(y[j] << 16);
+                                f[2 * j + 1] = __uint_as_float(y[j] & 0xffff0000u);
+                            } else {
+                                f[j] = __uint_as_float(y[j]);
+                            }
+                        }
+                    };
+                    if constexpr (KIND == LIN_FWD) {
+                        if (p.e.bias) {
+#pragma unroll
+                            for (int x = 0; x < PC / 8; ++x) {
+                                float f[8];
+                                const int have = min(8, p.N - col - 8 * x);        // 8, or 4 of an fp32 row, or none
+                                if (have > 0) {
+                                    lin_ld8(p.e.bias + col + 8 * x, have, true, f);
+#pragma unroll
+                                    for (int j = 0; j < 8; ++j) v[8 * x + j] += f[j];
+                                }
+                            }
+                        }
+                        if (has_z) put(side);
+                        act_apply(v, p.e.act);
+                    } else if constexpr (KIND == LIN_DX) {
+                        if (has_zin) {
+#pragma unroll
+                            for (int x = 0; x < PC / PER; ++x) {
+                                float f[PER], y[PER];
+                                get(sidep, x, f);
+#pragma unroll
+                                for (int j = 0; j < PER; ++j) y[j] = v[x * PER + j];
+                                act_slope_mul(y, f, p.e.act);
+#pragma unroll
+                                for (int j = 0; j < PER; ++j) v[x * PER + j] = y[j];
+                            }
+                        }
+                    }
+                    if (has_add) {
+#pragma unroll
+                        for (int x = 0; x < PC / PER; ++x) {
+                            float f[PER];
+                            get(iop, x, f);
+#pragma unroll
+                            for (int j = 0; j < PER; ++j) v[x * PER + j] += f[j];
+                        }
+                    }
+                    put(io);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_3d(&maps.out, io, col, row0, KIND == LIN_DW ? t.split : 0);
+                        if (has_z) tma_store_3d(&maps.out2, side, col, row0, 0);
+                        tma_store_commit();
+                        if (two) ask(after({u, c}), k + 1, true);      // Zin of the next piece: this one's has been read
+                    }
+                    __syncwarp();
+                    ++k;
+                } else {
+                    // 4 lanes a row, 8 columns each; 8 rows at a time
+                    __syncwarp();                   // lanes without columns are back; the last piece's reads are done
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(slots + fast::sw128(lane, x)), "f"(v[4 * x]),
+                                     "f"(v[4 * x + 1]), "f"(v[4 * x + 2]), "f"(v[4 * x + 3])
+                                     : "memory");
+                    __syncwarp();
+                    const int cl = lane & 3, cc = col + 8 * cl, have = min(8, p.N - cc);
+                    if (have > 0) {
+                        float bias[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) bias[j] = KIND == LIN_FWD && p.e.bias && j < have ? ldf(p.e.bias + cc + j) : 0.f;
+#pragma unroll 1
+                        for (int r8 = 0; r8 < 4; ++r8) {
+                            const int rl = 8 * r8 + (lane >> 2), row = row0 + rl;
+                            if (row >= p.M) break;
+                            const float4 x0 = *reinterpret_cast<const float4 *>(slots_p + fast::sw128(rl, 2 * cl));
+                            const float4 x1 = *reinterpret_cast<const float4 *>(slots_p + fast::sw128(rl, 2 * cl + 1));
+                            float y[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w}, o[8];
+                            const size_t at = (size_t)row * p.N + cc;
+                            if constexpr (KIND == LIN_DW) {
+                                lin_st8(p.acc + (size_t)t.split * p.M * p.N + at, have, false, y);
+                            } else {
+                                if constexpr (KIND == LIN_FWD) {
+#pragma unroll
+                                    for (int j = 0; j < 8; ++j) y[j] += bias[j];
+                                    if (p.e.out2) lin_st8(p.e.out2 + at, have, false, y);
+                                    act_apply(y, p.e.act);
+                                } else if (p.e.zin) {
+                                    lin_ld8(p.e.zin + at, have, false, o);
+                                    act_slope_mul(y, o, p.e.act);
+                                }
+                                if (p.e.add) {
+                                    lin_ld8(p.e.add + at, have, false, o);
+#pragma unroll
+                                    for (int j = 0; j < 8; ++j) y[j] += o[j];
+                                }
+                                lin_st8(p.e.out + at, have, false, y);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                }
+            };
+            if constexpr (PROMO) {
+#pragma unroll
+                for (int c = 0; c < PIECES; ++c) {
+                    float v[PC];
+#pragma unroll
+                    for (int j = 0; j < PC; ++j) v[j] = acc[c * PC + j];
+                    piece(c, v);
+                    if (!ok) break;
+                }
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < PIECES; ++c) {
+                    float v[PC];
+                    const uint32_t ta = tmem + b * BN + ((uint32_t)(32 * q) << 16) + half * S::HALF + c * PC;
+#pragma unroll
+                    for (int j = 0; j < PC; j += 32) tmem_ld32(ta + j, *reinterpret_cast<float(*)[32]>(v + j));
+                    tmem_ld_wait();
+                    if (c == PIECES - 1) released(b);
+                    piece(c, v);
+                    if (!ok) break;
+                }
+            }
+        }
+        if constexpr (VEC) {
+            if (lane == 0) {
+                tma_store_wait_all();
+                // after a wait that gave up: inputs asked for land before the CTA's memory is released
+                if (!ok && (has_add || has_zin)) {
+                    mbar_wait(slot_bar + 8 * (k & 1), (k >> 1) & 1);
+                    mbar_wait(slot_bar + 8 * ((k + 1) & 1), ((k + 1) >> 1) & 1);
+                    if (two) mbar_wait(slot_bar + 16, k & 1);
+                }
+            }
+            __syncwarp();
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (w == 1) tmem_dealloc(tmem, 2 * BN);
+    if constexpr (PAIR) cluster_sync_all();
+    if (w == 1) {
+        if constexpr (PAIR) tmem_dealloc_pair(tmem, 2 * BN);
+        else tmem_dealloc(tmem, 2 * BN);
+    }
 }
 
 // ------------------------------------------------------------------ host side
 
-template <int KIND, int BN, typename TO>
+template <int KIND, int BN, int CG, typename TO, bool VEC>
 static cudaError_t lt_launch(const LtMaps &m, const LtParams<TO> &p, cudaStream_t st) {
+    using S = Lt<KIND, BN, CG, TO, VEC>;
+    auto kernel = k_lin_tc<KIND, BN, CG, TO, VEC>;
     static std::atomic<uint32_t> attr_set{0};
-    if (cudaError_t e = ensure_smem_attr(k_lin_tc<KIND, BN, TO>, LtSmem<BN>::BYTES, attr_set); e != cudaSuccess) return e;
-    k_lin_tc<KIND, BN, TO><<<std::min(p.units, sm_count()), LT_THR, LtSmem<BN>::BYTES, st>>>(m, p);
-    return cudaGetLastError();
+    if (cudaError_t e = ensure_smem_attr(kernel, S::BYTES, attr_set); e != cudaSuccess) return e;
+    if constexpr (CG == 2 && S::PROMO) {
+        // the register split draws on what the launch has: never with less
+        static std::atomic<int> regs{0};
+        int r = regs.load(std::memory_order_relaxed);
+        if (!r) {
+            cudaFuncAttributes a;
+            if (cudaError_t e = cudaFuncGetAttributes(&a, kernel); e != cudaSuccess) return e;
+            regs.store(r = a.numRegs, std::memory_order_relaxed);
+        }
+        if (r < LT_REGS) return cudaErrorLaunchOutOfResources;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(std::min(p.units, sm_count() / CG) * CG));
+    cfg.blockDim = dim3(LT_THR);
+    cfg.dynamicSmemBytes = S::BYTES;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CG;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CG > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, m, p);
 }
-template <int KIND, typename TO>
-static cudaError_t lt_run(int bn, const LtMaps &m, const LtParams<TO> &p, cudaStream_t st) {
-    if (bn == 256) return lt_launch<KIND, 256, TO>(m, p, st);
-    if (bn == 128) return lt_launch<KIND, 128, TO>(m, p, st);
-    return lt_launch<KIND, 64, TO>(m, p, st);
+template <int KIND, typename TO, bool VEC>
+static cudaError_t lt_run(const LinTile &t, const LtMaps &m, const LtParams<TO> &p, cudaStream_t st) {
+    if (t.pair) return lt_launch<KIND, 256, 2, TO, VEC>(m, p, st);
+    if (t.bn == 128) return lt_launch<KIND, 128, 1, TO, VEC>(m, p, st);
+    return lt_launch<KIND, 64, 1, TO, VEC>(m, p, st);
 }
 
-// The widest tile that leaves no SM without one; where none does, the narrowest.
-static int lt_bn(long long tiles_m, int N) {
-    const int sms = sm_count();
-    for (int bn : {256, 128})
-        if (N > bn / 2 && tiles_m * ((N + bn - 1) / bn) >= sms) return bn;
-    return 64;
+// Tiles and, for a weight gradient, splits: the least of an estimate of each form's time.  The unit is a 64-deep
+// step of a pair's tile, 0.28 us.  A step of the single tiles takes 0.75 (128 columns) and 0.45 (64) of it for a
+// half and a quarter of a CTA's work: the shared memory's traffic bounds them (measured 1.0e15 op/s, pairs 1.4e15).  A tile
+// costs six steps more for the pipeline's start and the epilogue's end, a split the write and read of its sums.
+static double lt_cost(const LinTile &t, long long M, int N, long long steps, int splits, bool dw) {
+    const int bm = t.pair ? 256 : 128, sms = sm_count();
+    const double units = (double)((M + bm - 1) / bm) * ((N + t.bn - 1) / t.bn) * splits;
+    const double step = t.pair ? 1.0 : t.bn == 128 ? 0.75 : 0.45;
+    const double waves = std::ceil(units / (t.pair ? sms / 2 : sms));
+    const double per = (double)((steps + splits - 1) / splits);
+    double c = waves * (per * step + 3 * step) + 6;
+    if (dw && splits > 1) c += 10 + (double)splits * M * N * 8 / 6.5e6 / 0.28;       // bytes / (bytes a us) / (us a step)
+    return c;
+}
+static const LinTile LT_TILES[3] = {{true, 256}, {false, 128}, {false, 64}};
+static bool lt_fits(const LinTile &t, long long M, int N) {
+    if (t.pair) return M > 128 && N > 128;
+    return t.bn == 64 || N > 64;
+}
+static LinTile lt_tile(long long M, int N, long long steps) {
+    LinTile best = LT_TILES[2];
+    double least = 1e300;
+    for (const LinTile &t : LT_TILES)
+        if (lt_fits(t, M, N))
+            if (const double c = lt_cost(t, M, N, steps, 1, false); c < least) {
+                least = c;
+                best = t;
+            }
+    return best;
 }
 
 template <typename TO>
-static LtParams<TO> lt_params(const LinTc &q, long long M, int N, int bn) {
+static LtParams<TO> lt_params(const LinTc &q, const LinTile &t, long long M, int N) {
     LtParams<TO> p = {};
     p.status = q.status;
     p.clear = q.clear;
@@ -370,8 +708,9 @@ static LtParams<TO> lt_params(const LinTc &q, long long M, int N, int bn) {
     p.N = N;
     p.nseg = q.nseg;
     for (int s = 0; s < q.nseg; ++s) p.seg |= (uint32_t)q.seg[s] << (4 * s);
-    p.tiles_m = (p.M + LT_BM - 1) / LT_BM;
-    p.tiles_n = (N + bn - 1) / bn;
+    const int bm = t.pair ? 2 * LT_BM : LT_BM;
+    p.tiles_m = (int)((M + bm - 1) / bm);
+    p.tiles_n = (N + t.bn - 1) / t.bn;
     return p;
 }
 // The maps of the parts that are there.
@@ -380,64 +719,81 @@ static bool lt_encode(CUtensorMap (&m)[3], const bf16 *const (&base)[3], long lo
         if (!fast::encode_2d(&m[k], base[k], (int)rows, ld, box)) return false;
     return true;
 }
+// The maps of the outputs and the epilogue's inputs, a warp's piece at a time.
+template <typename TO>
+static bool lt_encode_out(LtMaps &m, const LinTile &t, const void *out, const LinEpi<TO> &e, long long planes, long long M, int N) {
+    const int pc = std::min(128 / (int)sizeof(TO), t.bn / 2);
+    auto enc = [&](CUtensorMap *x, const void *base) { return !base || fast::encode_3d(x, base, sizeof(TO) == 4, planes, M, N, pc, 32); };
+    return enc(&m.out, out) && enc(&m.out2, e.out2) && enc(&m.add, e.add) && enc(&m.zin, e.zin);
+}
 
+template <int KIND, typename T>
+static cudaError_t lt_product(const LinTc &q, const LinEpi<T> &e, long long M, int N, int K, cudaStream_t st) {
+    const int steps = (K + LT_BK - 1) / LT_BK;
+    const LinTile t = lt_tile(M, N, (long long)steps * q.nseg);
+    LtParams<T> p = lt_params<T>(q, t, M, N);
+    if ((long long)p.tiles_m * p.tiles_n > 0x7fffffffLL) return cudaErrorInvalidValue;
+    p.units = p.tiles_m * p.tiles_n;
+    p.e = e;
+    p.kts = steps;
+    LtMaps m;
+    const int bk = t.pair ? 128 : t.bn;             // B's columns a CTA loads
+    if (KIND == LIN_FWD ? !lt_encode(m.a, q.X, q.rows, q.ldx, LT_BM) || !lt_encode(m.b, q.W, q.in, q.ldw, 64)
+                        : !lt_encode(m.a, q.dZ, q.rows, q.ldz, LT_BM) || !lt_encode(m.b, q.W, q.in, q.ldw, bk))
+        return cudaErrorInvalidValue;
+    if ((long long)N * sizeof(T) % 16) return lt_run<KIND, T, false>(t, m, p, st);
+    if (!lt_encode_out<T>(m, t, e.out, e, 1, M, N)) return cudaErrorInvalidValue;
+    return lt_run<KIND, T, true>(t, m, p, st);
+}
 template <typename T>
 cudaError_t lin_tc_forward(const LinTc &q, const LinEpi<T> &e, cudaStream_t st) {
-    const int bn = lt_bn((q.rows + LT_BM - 1) / LT_BM, q.out);
-    LtParams<T> p = lt_params<T>(q, q.rows, q.out, bn);
-    if ((long long)p.tiles_m * p.tiles_n > 0x7fffffffLL) return cudaErrorInvalidValue;
-    p.units = p.tiles_m * p.tiles_n;
-    p.e = e;
-    p.kts = (q.in + LT_BK - 1) / LT_BK;
-    p.vec = (long long)q.out * sizeof(T) % 16 == 0;
-    LtMaps m;
-    if (!lt_encode(m.a, q.X, q.rows, q.ldx, LT_BM) || !lt_encode(m.b, q.W, q.in, q.ldw, 64)) return cudaErrorInvalidValue;
-    return lt_run<LIN_FWD, T>(bn, m, p, st);
+    return lt_product<LIN_FWD, T>(q, e, q.rows, q.out, q.in, st);
 }
-
 template <typename T>
 cudaError_t lin_tc_dx(const LinTc &q, const LinEpi<T> &e, cudaStream_t st) {
-    const int bn = lt_bn((q.rows + LT_BM - 1) / LT_BM, q.in);
-    LtParams<T> p = lt_params<T>(q, q.rows, q.in, bn);
-    if ((long long)p.tiles_m * p.tiles_n > 0x7fffffffLL) return cudaErrorInvalidValue;
-    p.units = p.tiles_m * p.tiles_n;
-    p.e = e;
-    p.kts = (q.out + LT_BK - 1) / LT_BK;
-    p.vec = (long long)q.in * sizeof(T) % 16 == 0;
-    LtMaps m;
-    if (!lt_encode(m.a, q.dZ, q.rows, q.ldz, LT_BM) || !lt_encode(m.b, q.W, q.in, q.ldw, bn)) return cudaErrorInvalidValue;
-    return lt_run<LIN_DX, T>(bn, m, p, st);
+    return lt_product<LIN_DX, T>(q, e, q.rows, q.in, q.out, st);
 }
-
 template cudaError_t lin_tc_forward<bf16>(const LinTc &, const LinEpi<bf16> &, cudaStream_t);
 template cudaError_t lin_tc_dx<bf16>(const LinTc &, const LinEpi<bf16> &, cudaStream_t);
 
-static int lt_dw_bn(int out) { return out > 128 ? 256 : out > 64 ? 128 : 64; }
-
-// Splits so that the units fill the SMs about twice, each with eight steps of 64 rows or more.
-LinSplit lin_tc_dw_split(long long rows, int in, int out) {
-    const int bn = lt_dw_bn(out);
-    const long long tiles = (long long)((in + LT_BM - 1) / LT_BM) * ((out + bn - 1) / bn);
+LinSplit lin_tc_dw_split(long long rows, int in, int out, int nseg) {
     const long long steps = std::max(1LL, (rows + LT_BK - 1) / LT_BK);
-    long long s = std::max(1LL, 2 * sm_count() / tiles);
-    s = std::max(1LL, std::min(s, steps / 8));
-    const long long per = (steps + s - 1) / s;
-    return {(int)((steps + per - 1) / per), per * LT_BK};
+    LinSplit best = {1, steps * LT_BK, LT_TILES[2]};
+    double least = 1e300;
+    for (const LinTile &t : LT_TILES) {
+        if (!lt_fits(t, in, out)) continue;
+        // splits of four steps or more, up to two for each SM
+        const int most = (int)std::max(1LL, std::min(steps / 4, 2LL * sm_count()));
+        for (int s = 1; s <= most; ++s) {
+            const long long per = (steps + s - 1) / s;
+            const int real = (int)((steps + per - 1) / per);
+            if (real != s) continue;
+            const double c = lt_cost(t, in, out, steps * nseg, s, true);
+            if (c < least) {
+                least = c;
+                best = {s, per * LT_BK, t};
+            }
+        }
+    }
+    return best;
 }
 
 cudaError_t lin_tc_dw(const LinTc &q, const LinSplit &s, float *dW, float *db, cudaStream_t st) {
-    const int bn = lt_dw_bn(q.out);
-    LtParams<bf16> p = lt_params<bf16>(q, q.in, q.out, bn);
+    LtParams<float> p = lt_params<float>(q, s.tile, q.in, q.out);
     const long long units = (long long)p.tiles_m * p.tiles_n * s.splits;
     if (units > 0x7fffffffLL) return cudaErrorInvalidValue;
     p.units = (int)units;
     p.acc = dW; p.db = db;
+    for (int k = 0; k < 3; ++k) p.dz[k] = q.dZ[k];
+    p.ldz = q.ldz;
+    p.rows = (int)q.rows;
     p.per = (int)(s.chunk / LT_BK);
     p.kts = (int)((q.rows + LT_BK - 1) / LT_BK);
-    p.vec = q.out % 4 == 0;
     LtMaps m;
     if (!lt_encode(m.a, q.X, q.rows, q.ldx, 64) || !lt_encode(m.b, q.dZ, q.rows, q.ldz, 64)) return cudaErrorInvalidValue;
-    return lt_run<LIN_DW, bf16>(bn, m, p, st);
+    if (q.out % 4) return lt_run<LIN_DW, float, false>(s.tile, m, p, st);
+    if (!lt_encode_out<float>(m, s.tile, dW, p.e, s.splits, q.in, q.out)) return cudaErrorInvalidValue;
+    return lt_run<LIN_DW, float, true>(s.tile, m, p, st);
 }
 
 }  // namespace ops

@@ -89,6 +89,35 @@ def test_exact_products(rows, i, o, dtype):
     assert torch.equal(dB.cpu().double(), dz.sum(0))
 
 
+@pytest.mark.parametrize("rows,i,o", [(4000, 200, 2056), (3900, 136, 2051), (4000, 2056, 200), (3900, 2051, 140), (520, 4000, 2056),
+                                      (777, 2200, 4099), (10_000, 1000, 1032)])
+def test_exact_products_of_large_tiles(rows, i, o):
+    """Results of many tiles, whole and ragged, and reductions of many steps."""
+    g = torch.Generator().manual_seed(rows + i)
+    X, W, b, R = cuda(*(whole(g, *s, dtype="bf16") for s in ((rows, i), (i, o), (o,), (rows, o))))
+    dY, dR, Zin, zo = cuda(*(whole(g, *s, dtype="bf16") for s in ((rows, o), (rows, i), (rows, i), (rows, o))))
+    z = X.double() @ W.double() + b.double()
+    for res in (R, None):
+        for save in (True, False):
+            Y, Z = forward(X, W, b, res, act="relu", save=save)
+            if save:
+                assert torch.equal(Z, z.bfloat16())
+            assert torch.equal(Y, (z.clamp(min=0) + (R.double() if res is not None else 0)).bfloat16())
+    dX, dW, dB = backward(X, W, dY)
+    assert torch.equal(dX, (dY.double() @ W.double().T).bfloat16())
+    assert torch.equal(dW.double(), X.double().T @ dY.double())
+    assert torch.equal(dB.double(), dY.double().sum(0))
+    dz = dY.double() * (zo.double() > 0)
+    dx = (dz @ W.double().T) * (Zin.double() > 0)
+    for res in (dR, None):
+        dX, dW, dB = backward(X, W, dY, Z=zo, act="relu", act_in="relu", Zin=Zin, dR=res)
+        assert torch.equal(dX.double(), (dx + (dR.double() if res is not None else 0)).bfloat16().double())
+        assert torch.equal(dW.double(), X.double().T @ dz)
+        assert torch.equal(dB.double(), dz.sum(0))
+    dX, _, _ = backward(None, W, dY, dR=dR, dw=False)
+    assert torch.equal(dX, (dY.double() @ W.double().T + dR.double()).bfloat16())
+
+
 def act64(z, act):
     if act == "relu":
         return z.clamp(min=0)

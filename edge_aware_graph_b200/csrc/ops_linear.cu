@@ -77,20 +77,21 @@ __global__ void __launch_bounds__(256) k_lin_prep(const __grid_constant__ PrepAr
 // adds its eight warps' sums.
 template <int VEC>
 __global__ void __launch_bounds__(256)
-k_lin_reduce(const float *acc, float *dW, long long n, const float *bacc, float *db, int out, int splits, unsigned wblocks) {
+k_lin_reduce(const float *acc, float *dW, long long n, int splits, const float *bacc, float *db, int out, int bparts, unsigned wblocks) {
     __shared__ float sum[8][32 * VEC];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const bool is_w = blockIdx.x < wblocks;
     const float *src = is_w ? acc : bacc;
     float *dst = is_w ? dW : db;
     const long long len = is_w ? n : out;
+    const int parts = is_w ? splits : bparts;
     const long long i = ((is_w ? blockIdx.x : blockIdx.x - wblocks) * 32LL + lane) * VEC;
     float s[VEC];
 #pragma unroll
     for (int k = 0; k < VEC; ++k) s[k] = 0.f;
     if (i < len) {
 #pragma unroll 8
-        for (int r = warp; r < splits; r += 8) {
+        for (int r = warp; r < parts; r += 8) {
             if constexpr (VEC == 4) {
                 const float4 v = *reinterpret_cast<const float4 *>(src + r * len + i);
                 s[0] += v.x; s[1] += v.y; s[2] += v.z; s[3] += v.w;
@@ -120,6 +121,7 @@ struct LinPlan {
     bool vec, tc;
     int ldx, ldw, ldz, zparts;
     LinSplit split;
+    int bparts;                // of the bias gradient
     size_t X, W, dZ[3], dZ32, acc, bacc, total;      // workspace offsets; 0: not there
 };
 
@@ -149,10 +151,9 @@ static LinPlan lin_plan(const eaga_linear_dims &d, bool back) {
         if (dact) p.dZ32 = take(rows * out * 4);
         p.split = lin_f32_dw_split(d.rows, d.in, d.out);
     }
-    if (p.split.splits > 1) {
-        p.acc = take(p.split.splits * in * out * 4);
-        p.bacc = take(p.split.splits * out * 4);
-    }
+    if (p.split.splits > 1) p.acc = take(p.split.splits * in * out * 4);
+    if (back && !p.vec) p.bparts = lin_db_parts(p.split, d.in);
+    if (p.bparts > 1) p.bacc = take(p.bparts * out * 4);
     p.total = off;
     return p;
 }
@@ -179,13 +180,15 @@ static cudaError_t lin_prep(const PrepJob *jobs, int n, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-static cudaError_t lin_reduce(const LinSplit &s, long long n, int out, const float *acc, float *dW, const float *bacc,
-                              float *db, cudaStream_t st) {
+// Whichever of the two sums is in more than one part.
+static cudaError_t lin_reduce(long long n, int splits, const float *acc, float *dW, int out, int bparts, const float *bacc, float *db,
+                              cudaStream_t st) {
     const bool v4 = n % 4 == 0 && out % 4 == 0;
     const long long per = v4 ? 128 : 32;
-    const unsigned wb = (unsigned)((n + per - 1) / per), bb = db ? (unsigned)((out + per - 1) / per) : 0;
-    if (v4) k_lin_reduce<4><<<wb + bb, 256, 0, st>>>(acc, dW, n, bacc, db, out, s.splits, wb);
-    else k_lin_reduce<1><<<wb + bb, 256, 0, st>>>(acc, dW, n, bacc, db, out, s.splits, wb);
+    const unsigned wb = splits > 1 ? (unsigned)((n + per - 1) / per) : 0, bb = db && bparts > 1 ? (unsigned)((out + per - 1) / per) : 0;
+    if (!(wb + bb)) return cudaSuccess;
+    if (v4) k_lin_reduce<4><<<wb + bb, 256, 0, st>>>(acc, dW, n, splits, bacc, db, out, bparts, wb);
+    else k_lin_reduce<1><<<wb + bb, 256, 0, st>>>(acc, dW, n, splits, bacc, db, out, bparts, wb);
     return cudaGetLastError();
 }
 
@@ -242,11 +245,10 @@ static cudaError_t backward_tc(const eaga_linear_dims &d, const LinPlan &p, cons
     if (b.dW) {
         q.nseg = zparts;
         for (int k = 0; k < q.nseg; ++k) q.seg[k] = (uint8_t)((q.nseg - 1 - k) << 2);       // B = dZ, X in one part
-        const bool split = p.split.splits > 1;
-        float *acc = split ? reinterpret_cast<float *>(b.ws + p.acc) : b.dW;
-        float *bacc = !b.db ? nullptr : split ? reinterpret_cast<float *>(b.ws + p.bacc) : b.db;
+        float *acc = p.split.splits > 1 ? reinterpret_cast<float *>(b.ws + p.acc) : b.dW;
+        float *bacc = !b.db ? nullptr : p.bparts > 1 ? reinterpret_cast<float *>(b.ws + p.bacc) : b.db;
         if (cudaError_t err = lin_tc_dw(q, p.split, acc, bacc, st); err != cudaSuccess) return err;
-        if (split) return lin_reduce(p.split, (long long)d.in * d.out, d.out, acc, b.dW, bacc, b.db, st);
+        return lin_reduce((long long)d.in * d.out, p.split.splits, acc, b.dW, d.out, p.bparts, bacc, b.db, st);
     }
     return cudaSuccess;
 }
@@ -265,11 +267,10 @@ static cudaError_t backward_f32(const eaga_linear_dims &d, const LinPlan &p, con
         if (cudaError_t err = lin_f32_dx(q, e, st); err != cudaSuccess) return err;
     }
     if (b.dW) {
-        const bool split = p.split.splits > 1;
-        float *acc = split ? reinterpret_cast<float *>(b.ws + p.acc) : b.dW;
-        float *bacc = !b.db ? nullptr : split ? reinterpret_cast<float *>(b.ws + p.bacc) : b.db;
+        float *acc = p.split.splits > 1 ? reinterpret_cast<float *>(b.ws + p.acc) : b.dW;
+        float *bacc = !b.db ? nullptr : p.bparts > 1 ? reinterpret_cast<float *>(b.ws + p.bacc) : b.db;
         if (cudaError_t err = lin_f32_dw(q, p.split, acc, bacc, st); err != cudaSuccess) return err;
-        if (split) return lin_reduce(p.split, (long long)d.in * d.out, d.out, acc, b.dW, bacc, b.db, st);
+        return lin_reduce((long long)d.in * d.out, p.split.splits, acc, b.dW, d.out, p.bparts, bacc, b.db, st);
     }
     return cudaSuccess;
 }

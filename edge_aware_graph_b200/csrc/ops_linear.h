@@ -134,8 +134,10 @@ template <typename T>
 cudaError_t lin_tc_forward(const LinTc &p, const LinEpi<T> &e, cudaStream_t st);
 template <typename T>
 cudaError_t lin_tc_dx(const LinTc &p, const LinEpi<T> &e, cudaStream_t st);
-// dW (and db, where not null) or, with more than one split, the splits' partial sums [splits][in][out] (and [splits][out]).
+// dW or, with more than one split, the splits' sums [splits][in][out]; and where db is not null the column sums in
+// lin_db_parts() parts [parts][out].
 LinSplit lin_tc_dw_split(long long rows, int in, int out, int nseg);
+inline int lin_db_parts(const LinSplit &s, int in) { return s.splits * (s.tile.pair ? (in + 255) / 256 : 1); }
 cudaError_t lin_tc_dw(const LinTc &p, const LinSplit &s, float *dW, float *db, cudaStream_t st);
 
 // CUDA-core products of fp32 operands of any size; partial sums as above.

@@ -31,10 +31,11 @@
 // A weight gradient reduces over rows, of which there may be a million for a
 // 64 x 128 result: its tiles are split over rows, the splits' sums are added
 // in a fixed order by the caller's reduction.  The bias gradient, the column
-// sums of dZ, comes from two more warps, for the first row of tiles: from the dZ
-// tiles in shared memory times a matrix of ones (warp-level MMAs, joined in fp32
-// after every 64 rows), or, on pairs, where the barriers are the first CTA's, from
-// dZ itself, which the tiles' loads have just brought into L2.
+// sums of dZ, comes from two more warps: on single tiles in those of the first
+// row, from the dZ tiles in shared memory times a matrix of ones (warp-level MMAs,
+// joined in fp32 after every 64 rows); on pairs, where the barriers are the first
+// CTA's, from dZ itself, which the tiles' loads have brought into L2, a share of
+// the rows in every row of tiles.
 //
 // An operand in fp32 comes as bf16 parts (two carry 16 bits of it, three 24):
 // the products of parts are segments of one longer reduction, the smallest first.
@@ -52,7 +53,6 @@ bool encode_3d(CUtensorMap *m, const void *base, bool f32, long long planes, lon
 namespace ops {
 
 using namespace sm100;
-using fast::dev::cta_wait;
 typedef __nv_bfloat16 bf16;
 
 constexpr int LT_BM = 128, LT_BK = 64;
@@ -70,11 +70,15 @@ struct Lt {
     static constexpr int BM = LT_BM * CG, PB = BN / CG;              // the tile's rows; B columns a CTA holds
     static constexpr bool PROMO = KIND == LIN_DW || sizeof(TO) == 4;
     static constexpr int HALF = BN / 2;                              // columns of an epilogue warp
-    static constexpr int PC = VEC ? (128 / (int)sizeof(TO) < HALF ? 128 / (int)sizeof(TO) : HALF) : 32;   // a piece's columns
+    // A piece's columns: rows of 128 bytes, or 64 where the tile is narrow or, on pairs, the ring needs the room.
+    static constexpr int ROW = CG == 2 ? 64 : 128;
+    static constexpr int PC = VEC ? (ROW / (int)sizeof(TO) < HALF ? ROW / (int)sizeof(TO) : HALF) : 32;
     static constexpr int PIECES = HALF / PC;
     static constexpr uint32_t A_BYTES = LT_BM * LT_BK * 2, B_BYTES = PB * LT_BK * 2, STAGE = A_BYTES + B_BYTES;
     static constexpr uint32_t SLOT = VEC ? 32 * PC * sizeof(TO) : 4096;
-    static constexpr int SLOTS = KIND == LIN_DW ? 2 : 3;             // two for the output in turn (in it the residual), one for Z or Zin
+    // Slots of a warp: the output's (in it the residual), two in turn where the epilogue is not hidden behind long
+    // products anyway; one for Z or Zin.
+    static constexpr int NIO = CG == 2 && KIND != LIN_DW ? 1 : 2, SLOTS = KIND == LIN_DW ? NIO : NIO + 1;
     static constexpr uint32_t RING = 232448 - 1024 - 512 - LT_EPI * SLOTS * SLOT;
     static constexpr int ST = RING / STAGE < 8 ? RING / STAGE : 8;
     static constexpr uint32_t EPI = ST * STAGE;
@@ -86,6 +90,12 @@ struct Lt {
     static_assert(ST >= 3 && BYTES <= 232448, "shared memory");
 };
 
+// A bounded wait that looks at the CTA's failure flag only where the barrier is not there yet.
+__device__ __forceinline__ bool lt_wait(uint32_t bar, uint32_t parity, volatile int *fail, int *status) {
+    if (mbar_try_wait(bar, parity)) return true;
+    return fast::dev::cta_wait(bar, parity, fail, status);
+}
+
 // Maps of the operands' parts, the outputs and the epilogue's inputs.
 struct LtMaps {
     CUtensorMap a[3], b[3];
@@ -95,7 +105,7 @@ struct LtMaps {
 template <typename TO>
 struct LtParams {
     LinEpi<TO> e;
-    float *acc, *db;           // weight gradient: fp32 sums [split][M][N], [split][N]
+    float *acc, *db;           // weight gradient: fp32 sums [split][M][N]; [split][N], on pairs [split][row of tiles][N]
     const bf16 *dz[3];         // on pairs, for db: dZ's parts, their row length
     int ldz, rows;
     int *status;
@@ -180,17 +190,18 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
         if constexpr (REGS) regs_dec<LT_REGS_LOW>();
         if (w == 0) {
             if (lane == 0) {
-                int it = 0, issued = 0;
+                int s = 0, issued = 0;                       // the stage; stages filled
+                uint32_t ph = 1;
                 bool ok = true;
                 for (int u = first; ok && u < p.units; u += stride) {
                     const Unit t = unit_of(u);
-                    const int nb = t.n0 + rank * S::PB;          // this CTA's columns of B
+                    const int nb = t.n0 + rank * S::PB;      // this CTA's columns of B
                     for (int seg = 0; ok && seg < p.nseg; ++seg) {
                         const uint32_t parts = p.seg >> (4 * seg);
                         const CUtensorMap *am = &maps.a[parts & 3], *bm = &maps.b[(parts >> 2) & 3];
-                        for (int k = 0; k < t.steps; ++k, ++it) {
-                            const int s = it % ST, kk = (t.k0 + k) * LT_BK;
-                            if (!cta_wait(empty(s), ((it / ST) & 1) ^ 1, fail, p.status)) { ok = false; break; }
+                        int kk = t.k0 * LT_BK;
+                        for (int k = t.steps; k > 0; --k, kk += LT_BK) {
+                            if (!lt_wait(empty(s), ph, fail, p.status)) { ok = false; break; }
                             const uint32_t st = sbase + s * S::STAGE;
                             const uint32_t bar = PAIR ? cluster_map(full(s), 0) : full(s);
                             if (rank == 0) mbar_expect_tx(full(s), S::STAGE * CG);
@@ -210,11 +221,15 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
                             } else {
                                 load(st + S::A_BYTES, bm, kk, nb);
                             }
-                            issued = it + 1;
+                            ++issued;
+                            if (++s == ST) {
+                                s = 0;
+                                ph ^= 1;
+                            }
                         }
                     }
                 }
-                // After a wait that gave up: what was issued lands before the CTA's memory is released.  (Of a pair the first
+            // After a wait that gave up: what was issued lands before the CTA's memory is released.  (Of a pair the first
                 // CTA's barriers count both CTAs' loads, and the two leave together.)
                 if (!ok && rank == 0)
                     for (int i = max(issued - ST, 0); i < issued; ++i) mbar_wait(full(i % ST), (i / ST) & 1);
@@ -222,7 +237,14 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
         } else if (w == 1) {
             if (lane == 0 && rank == 0) {
                 constexpr uint32_t idesc = idesc_bf16_f32(S::BM, BN) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
-                int it = 0, n = 0;                               // steps; accumulators
+                // One thread feeds the tensor cores: between two stages it has 512 clocks (a pair's, 256 or 128 a single
+                // tile's), so descriptors are one addition away, and a wait looks at the failure flag only when it has to.
+                const uint64_t ad0 = A_MN ? smem_desc(sbase, 8192, 1024, LAYOUT_SW128) : smem_desc(sbase, 16, 1024, LAYOUT_SW128);
+                const uint64_t bd0 = B_MN ? smem_desc(sbase + S::A_BYTES, 8192, 1024, LAYOUT_SW128)
+                                          : smem_desc(sbase + S::A_BYTES, 16, 1024, LAYOUT_SW128);
+                constexpr uint32_t AK = (A_MN ? 2048 : 32) >> 4, BK = (B_MN ? 2048 : 32) >> 4;     // 16 steps on
+                int s = 0, n = 0;                                // the stage; accumulators
+                uint32_t ph = 0;
                 bool ok = true;
                 for (int u = first; ok && u < p.units; u += stride) {
                     const Unit t = unit_of(u);
@@ -230,29 +252,28 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
                     const bool sums = SMEM_SUMS && p.db != nullptr && t.tm == 0;
                     for (int k0 = 0; ok && k0 < nk; ++n) {
                         const int b = n & 1, k1 = PROMO ? min(k0 + LT_PROMO, nk) : nk;
-                        if (!cta_wait(acc_empty(b), ((n >> 1) & 1) ^ 1, fail, p.status)) { ok = false; break; }
+                        if (!lt_wait(acc_empty(b), ((n >> 1) & 1) ^ 1, fail, p.status)) { ok = false; break; }
                         tc_fence_after();
                         const uint32_t d = tmem + b * BN;
-                        for (int k = k0; k < k1; ++k, ++it) {
-                            const int s = it % ST;
-                            if (!cta_wait(full(s), (it / ST) & 1, fail, p.status)) { ok = false; break; }
+                        for (int k = k0; k < k1; ++k) {
+                            if (!lt_wait(full(s), ph, fail, p.status)) { ok = false; break; }
                             tc_fence_after();
-                            const uint32_t st = sbase + s * S::STAGE;
+                            const uint64_t ad = ad0 + (uint32_t)(s * (S::STAGE >> 4)), bd = bd0 + (uint32_t)(s * (S::STAGE >> 4));
 #pragma unroll
                             for (int kk = 0; kk < LT_BK / 16; ++kk) {
-                                const uint64_t ad = A_MN ? smem_desc(st + kk * 2048, 8192, 1024, LAYOUT_SW128)
-                                                         : smem_desc(st + kk * 32, 16, 1024, LAYOUT_SW128);
-                                const uint64_t bd = B_MN ? smem_desc(st + S::A_BYTES + kk * 2048, 8192, 1024, LAYOUT_SW128)
-                                                         : smem_desc(st + S::A_BYTES + kk * 32, 16, 1024, LAYOUT_SW128);
                                 const uint32_t more = k > k0 || kk > 0 ? 1u : 0u;
-                                if constexpr (PAIR) mma_bf16_ss_pair(d, ad, bd, idesc, more);
-                                else mma_bf16_ss(d, ad, bd, idesc, more);
+                                if constexpr (PAIR) mma_bf16_ss_pair(d, ad + kk * AK, bd + kk * BK, idesc, more);
+                                else mma_bf16_ss(d, ad + kk * AK, bd + kk * BK, idesc, more);
                             }
                             if constexpr (PAIR) mma_commit_pair(empty(s), 3);
                             else mma_commit(empty(s));
                             if (SMEM_SUMS && !sums) {            // no column sums: their two arrivals
                                 mbar_arrive(empty(s));
                                 mbar_arrive(empty(s));
+                            }
+                            if (++s == ST) {
+                                s = 0;
+                                ph ^= 1;
                             }
                         }
                         if (ok) {
@@ -288,7 +309,7 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
                     for (int j = 0; j < NT; ++j) sum[j][0] = sum[j][1] = 0.f;
                     for (int k = 0; k < nk; ++k, ++it) {
                         const int s = it % ST;
-                        ok = __all_sync(0xffffffffu, cta_wait(full(s), (it / ST) & 1, fail, p.status));
+                        ok = __all_sync(0xffffffffu, lt_wait(full(s), (it / ST) & 1, fail, p.status));
                         if (!ok) break;
                         const uint32_t bt = sbase + s * S::STAGE + S::A_BYTES;
 #pragma unroll
@@ -321,12 +342,14 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
                     __syncwarp();
                 }
             } else if constexpr (KIND == LIN_DW) {
-                // column sums of dZ from memory: a warp 64 columns, 8 a lane, four rows at a time
+                // column sums of dZ from memory, each row of tiles its share of the unit's rows: a warp 64 columns, 8 a
+                // lane, four rows at a time
                 for (int u = first; p.db != nullptr && u < p.units; u += stride) {
                     const Unit t = unit_of(u);
-                    if (t.tm != 0) continue;
                     const int c = t.n0 + rank * S::PB + (w - 2) * 64 + 8 * (lane & 7);
-                    const long long r0 = (long long)t.k0 * LT_BK, r1 = min((long long)p.rows, r0 + (long long)t.steps * LT_BK);
+                    const long long all = min((long long)p.rows - (long long)t.k0 * LT_BK, (long long)t.steps * LT_BK);
+                    const long long part = (all + p.tiles_m - 1) / p.tiles_m, base = (long long)t.k0 * LT_BK;
+                    const long long r0 = base + min(all, part * t.tm), r1 = base + min(all, part * (t.tm + 1));
                     float sum[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) sum[j] = 0.f;
@@ -350,7 +373,7 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
                     if (lane < 8) {
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            if (c + j < p.N) p.db[(size_t)t.split * p.N + c + j] = sum[j];
+                            if (c + j < p.N) p.db[((size_t)t.split * p.tiles_m + t.tm) * p.N + c + j] = sum[j];
                     }
                     __syncwarp();
                 }
@@ -385,7 +408,7 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
             if (x.u >= p.units) return;
             const Unit t = unit_of(x.u);
             const int col = t.n0 + half * S::HALF + x.c * PC, row = t.m0 + 32 * q;
-            const int s = side ? 2 : k & 1;
+            const int s = side ? S::NIO : k % S::NIO;
             mbar_expect_tx(slot_bar + 8 * s, S::SLOT);
             tma_load_3d(slots + s * S::SLOT, side || !has_add ? &maps.zin : &maps.add, slot_bar + 8 * s, col, row, 0);
         };
@@ -414,7 +437,7 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
             };
             for (int ch = 0; ch < chunks; ++ch, ++n) {
                 const int b = n & 1;
-                ok = __all_sync(0xffffffffu, cta_wait(acc_full(b), (n >> 1) & 1, fail, p.status));
+                ok = __all_sync(0xffffffffu, lt_wait(acc_full(b), (n >> 1) & 1, fail, p.status));
                 if (!ok) break;
                 tc_fence_after();
                 if constexpr (PROMO) {
@@ -437,30 +460,30 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
                 const int col = t.n0 + half * S::HALF + c * PC;
                 if (row0 >= p.M || col >= p.N) return;
                 if constexpr (VEC) {
-                    const int s = k & 1;
+                    const int s = k % S::NIO;
                     if constexpr (KIND != LIN_DW) {
                         if (has_add || has_zin) {
                             // the next piece's inputs, into the other slot: its store (the last piece's) has been read by now
                             if (lane == 0) {
                                 tma_store_wait_read0();
-                                ask(after({u, c}), k + 1, false);
+                                if (S::NIO == 2) ask(after({u, c}), k + 1, false);
                             }
                             __syncwarp();
-                            ok = __all_sync(0xffffffffu, cta_wait(slot_bar + 8 * s, (k >> 1) & 1, fail, p.status));
-                            if (two) ok = ok && __all_sync(0xffffffffu, cta_wait(slot_bar + 16, k & 1, fail, p.status));
+                            ok = __all_sync(0xffffffffu, lt_wait(slot_bar + 8 * s, (k / S::NIO) & 1, fail, p.status));
+                            if (two) ok = ok && __all_sync(0xffffffffu, lt_wait(slot_bar + 8 * S::NIO, k & 1, fail, p.status));
                             if (!ok) return;
                         }
                     }
                     if (!(has_add || has_zin)) {
                         // a slot is free when all stores but the last piece's have been read; Z's slot when that one has, too
                         if (lane == 0) {
-                            if (has_z) tma_store_wait_read0();
+                            if (has_z || S::NIO == 1) tma_store_wait_read0();
                             else tma_store_wait_read1();
                         }
                         __syncwarp();
                     }
-                    const uint32_t io = slots + s * S::SLOT, side = slots + 2 * S::SLOT;
-                    const uint8_t *iop = slots_p + s * S::SLOT, *sidep = slots_p + (two ? 2 : s) * S::SLOT;
+                    const uint32_t io = slots + s * S::SLOT, side = slots + S::NIO * S::SLOT;
+                    const uint8_t *iop = slots_p + s * S::SLOT, *sidep = slots_p + (two ? S::NIO : s) * S::SLOT;
                     constexpr int PER = 16 / sizeof(TO);        // columns of a 16-byte chunk
                     auto put = [&](uint32_t base) {
 #pragma unroll
@@ -534,6 +557,10 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
                         tma_store_3d(&maps.out, io, col, row0, KIND == LIN_DW ? t.split : 0);
                         if (has_z) tma_store_3d(&maps.out2, side, col, row0, 0);
                         tma_store_commit();
+                        if (S::NIO == 1 && (has_add || has_zin)) {
+                            tma_store_wait_read0();
+                            ask(after({u, c}), k + 1, false);
+                        }
                         if (two) ask(after({u, c}), k + 1, true);      // Zin of the next piece: this one's has been read
                     }
                     __syncwarp();
@@ -612,9 +639,8 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
                 tma_store_wait_all();
                 // after a wait that gave up: inputs asked for land before the CTA's memory is released
                 if (!ok && (has_add || has_zin)) {
-                    mbar_wait(slot_bar + 8 * (k & 1), (k >> 1) & 1);
-                    mbar_wait(slot_bar + 8 * ((k + 1) & 1), ((k + 1) >> 1) & 1);
-                    if (two) mbar_wait(slot_bar + 16, k & 1);
+                    for (int x = k; x < k + S::NIO; ++x) mbar_wait(slot_bar + 8 * (x % S::NIO), (x / S::NIO) & 1);
+                    if (two) mbar_wait(slot_bar + 8 * S::NIO, k & 1);
                 }
             }
             __syncwarp();
@@ -722,7 +748,7 @@ static bool lt_encode(CUtensorMap (&m)[3], const bf16 *const (&base)[3], long lo
 // The maps of the outputs and the epilogue's inputs, a warp's piece at a time.
 template <typename TO>
 static bool lt_encode_out(LtMaps &m, const LinTile &t, const void *out, const LinEpi<TO> &e, long long planes, long long M, int N) {
-    const int pc = std::min(128 / (int)sizeof(TO), t.bn / 2);
+    const int pc = std::min((t.pair ? 64 : 128) / (int)sizeof(TO), t.bn / 2);
     auto enc = [&](CUtensorMap *x, const void *base) { return !base || fast::encode_3d(x, base, sizeof(TO) == 4, planes, M, N, pc, 32); };
     return enc(&m.out, out) && enc(&m.out2, e.out2) && enc(&m.add, e.add) && enc(&m.zin, e.zin);
 }

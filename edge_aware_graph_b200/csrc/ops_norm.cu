@@ -42,8 +42,39 @@ struct RnArgs {
     float *parts, *gparts;     // [CTA][4][w] sums of the gains' and shifts' gradients, [run][w] of the gate's
     float alpha, eps, inv_w;
     unsigned rows, w, group, run, runs_per_group, runs;
-    int pre, post, team;       // threads that hold a row
+    int pre, post, team, crew; // threads that hold a row; threads that share a run (backward)
 };
+
+// ------------------------------------------------------------------ two fp32 values at once
+// The kernels are bound by the instructions they issue as much as by memory;
+// sm_100a adds, multiplies and fuses two fp32 values (rounded like one) in one.
+struct f2 {
+    unsigned long long b;
+};
+__device__ __forceinline__ f2 pair(float x, float y) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.b) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ f2 both(float x) { return pair(x, x); }
+__device__ __forceinline__ float lo(f2 a) { return __uint_as_float((unsigned)a.b); }
+__device__ __forceinline__ float hi(f2 a) { return __uint_as_float((unsigned)(a.b >> 32)); }
+__device__ __forceinline__ f2 operator+(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.b) : "l"(a.b), "l"(b.b));
+    return r;
+}
+__device__ __forceinline__ f2 operator*(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.b) : "l"(a.b), "l"(b.b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.b) : "l"(a.b), "l"(b.b), "l"(c.b));
+    return r;
+}
+__device__ __forceinline__ float across(f2 a) { return lo(a) + hi(a); }
 
 // ------------------------------------------------------------------ a row in registers
 // E elements a thread.  VEC > 1: 16-byte vectors, thread k of a team holds
@@ -72,45 +103,68 @@ struct RowIo {
             }
         }
     }
-    static __device__ __forceinline__ void values(const Raw &r, float (&v)[E]) {
+    static __device__ __forceinline__ void values(const Raw &r, f2 (&v)[E / 2]) {
+        if constexpr (VEC == 1) {
 #pragma unroll
-        for (int n = 0; n < NV; ++n) {
-            if constexpr (VEC == 1) {
-                v[n] = ldf(&r.v[n]);
-            } else {
+            for (int n = 0; n < E / 2; ++n) v[n] = pair(ldf(&r.v[2 * n]), ldf(&r.v[2 * n + 1]));
+        } else {
+#pragma unroll
+            for (int n = 0; n < NV; ++n) {
                 const unsigned x[4] = {r.v[n].x, r.v[n].y, r.v[n].z, r.v[n].w};
+                if constexpr (sizeof(T) == 4) {
+                    v[2 * n] = pair(__uint_as_float(x[0]), __uint_as_float(x[1]));
+                    v[2 * n + 1] = pair(__uint_as_float(x[2]), __uint_as_float(x[3]));
+                } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if constexpr (sizeof(T) == 4) {
-                        v[4 * n + j] = __uint_as_float(x[j]);
-                    } else {
-                        v[8 * n + 2 * j] = __uint_as_float(x[j] << 16);
-                        v[8 * n + 2 * j + 1] = __uint_as_float(x[j] & 0xffff0000u);
-                    }
+                    for (int j = 0; j < 4; ++j) v[4 * n + j] = pair(__uint_as_float(x[j] << 16), __uint_as_float(x[j] & 0xffff0000u));
                 }
             }
         }
     }
-    static __device__ __forceinline__ void load(const T *p, unsigned k, unsigned team, unsigned w, float (&v)[E]) {
+    static __device__ __forceinline__ void load(const T *p, unsigned k, unsigned team, unsigned w, f2 (&v)[E / 2]) {
         Raw r;
         fetch(p, true, k, team, w, r);
         values(r, v);
     }
-    static __device__ __forceinline__ void store(T *p, unsigned k, unsigned team, unsigned w, const float (&v)[E]) {
+    static __device__ __forceinline__ void store(T *p, unsigned k, unsigned team, unsigned w, const f2 (&v)[E / 2]) {
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
             const unsigned c = (k + n * team) * VEC;
             if (c >= w) continue;
             if constexpr (VEC == 1) {
-                stf(p + c, v[n]);
+                stf(p + c, n & 1 ? hi(v[n / 2]) : lo(v[n / 2]));
             } else if constexpr (sizeof(T) == 4) {
-                *reinterpret_cast<float4 *>(p + c) = make_float4(v[4 * n], v[4 * n + 1], v[4 * n + 2], v[4 * n + 3]);
+                *reinterpret_cast<float4 *>(p + c) = make_float4(lo(v[2 * n]), hi(v[2 * n]), lo(v[2 * n + 1]), hi(v[2 * n + 1]));
             } else {
                 uint4 o;
                 __nv_bfloat162 *q = reinterpret_cast<__nv_bfloat162 *>(&o);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) q[j] = __floats2bfloat162_rn(v[8 * n + 2 * j], v[8 * n + 2 * j + 1]);
+                for (int j = 0; j < 4; ++j) q[j] = __floats2bfloat162_rn(lo(v[4 * n + j]), hi(v[4 * n + j]));
                 *reinterpret_cast<uint4 *>(p + c) = o;
+            }
+        }
+    }
+    static __device__ __forceinline__ void store_zeros(T *p, unsigned k, unsigned team, unsigned w) {
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const unsigned c = (k + n * team) * VEC;
+            if (c >= w) continue;
+            if constexpr (VEC == 1) stf(p + c, 0.f);
+            else *reinterpret_cast<uint4 *>(p + c) = make_uint4(0, 0, 0, 0);
+        }
+    }
+    // v - m, nothing where the row has no element
+    static __device__ __forceinline__ void centre(f2 (&v)[E / 2], float m, unsigned k, unsigned team, unsigned w) {
+        if constexpr (VEC == 1) {
+#pragma unroll
+            for (int n = 0; n < E / 2; ++n)
+                v[n] = v[n] + pair(col(2 * n, k, team) < w ? -m : 0.f, col(2 * n + 1, k, team) < w ? -m : 0.f);
+        } else {
+#pragma unroll
+            for (int n = 0; n < NV; ++n) {
+                const f2 t = both(col(n * VEC, k, team) < w ? -m : 0.f);
+#pragma unroll
+                for (int j = 0; j < VEC / 2; ++j) v[n * (VEC / 2) + j] = v[n * (VEC / 2) + j] + t;
             }
         }
     }
@@ -123,10 +177,12 @@ struct RowIo {
 // sum's barrier, which every thread reaches after it has read).
 template <bool WIDE, int N>
 __device__ __forceinline__ void team_sum(float (&a)[N], unsigned team, float (*buf)[4][32], unsigned &turn) {
-    const unsigned span = WIDE ? 32u : team;
-    for (unsigned o = span >> 1; o; o >>= 1)
 #pragma unroll
-        for (int n = 0; n < N; ++n) a[n] += __shfl_xor_sync(0xffffffffu, a[n], o);
+    for (unsigned o = 16; o; o >>= 1)
+        if (WIDE || o < team) {
+#pragma unroll
+            for (int n = 0; n < N; ++n) a[n] += __shfl_xor_sync(0xffffffffu, a[n], o);
+        }
     if constexpr (WIDE) {
         float (*b)[32] = buf[turn & 1];
         ++turn;
@@ -139,9 +195,8 @@ __device__ __forceinline__ void team_sum(float (&a)[N], unsigned team, float (*b
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             float s = lane < nw ? b[n][lane] : 0.f;
-#pragma unroll
-            for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            a[n] = s;
+            for (unsigned o = nw >> 1; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            a[n] = __shfl_sync(0xffffffffu, s, 0);
         }
     }
 }
@@ -157,7 +212,9 @@ __device__ __forceinline__ Team my_team(unsigned team) {
     return {threadIdx.x % team, blockIdx.x * per + threadIdx.x / team, gridDim.x * per};
 }
 
-// What a thread keeps beside the row it works on.  AHEAD: the next row, as it
+constexpr int RN_DEPTH = 4;        // steps of the backward in shared memory, the one that is worked on among them
+
+// What a thread of the forward keeps beside the row it works on.  AHEAD: the next row, as it
 // lies in memory (4 registers a tensor for 8 bf16 elements, where there is room
 // for them).  KEEP: the norms' gains and shifts; teams of a CTA's size read
 // those from L1 again, and run two CTAs an SM instead.
@@ -171,15 +228,12 @@ __global__ void __launch_bounds__(MAXT, E > 8 ? 1 : WIDE ? 1024 / MAXT : 3)
 k_rn_fwd(const RnArgs a) {
     using IO = RowIo<T, VEC, E>;
     using Raw = typename IO::Raw;
+    constexpr int H = E / 2;
     constexpr bool AHEAD = RnKeep<VEC, E, WIDE>::AHEAD, KEEP = RnKeep<VEC, E, WIDE>::KEEP;
     __shared__ float buf[2][4][32];
     unsigned turn = 0;
     const unsigned w = a.w, team = a.team;
     const Team tm = my_team<WIDE>(team);
-    bool on_v[IO::NV];                               // a vector is in the row, or none of it
-#pragma unroll
-    for (int n = 0; n < IO::NV; ++n) on_v[n] = IO::col(n * VEC, tm.k, team) < w;
-    auto on = [&](int q) { return on_v[q / VEC]; };
     const T *x = static_cast<const T *>(a.x), *u = static_cast<const T *>(a.u), *gate = static_cast<const T *>(a.gate);
     T *r = static_cast<T *>(a.r), *h = static_cast<T *>(a.h);
     const unsigned last = WIDE ? a.rows : (a.rows + tm.count - 1) / tm.count * tm.count;   // warps stay whole
@@ -190,7 +244,7 @@ k_rn_fwd(const RnArgs a) {
         const size_t at = (size_t)(live ? row : 0) * w;
         IO::fetch(u + at, live, tm.k, team, w, nu);
         IO::fetch(x + at, live && x, tm.k, team, w, nx);
-        IO::fetch(gate + (size_t)((live ? row : 0) / a.group) * w, live && gate, tm.k, team, w, ng);
+        if (gate) IO::fetch(gate + (size_t)((live ? row : 0) / a.group) * w, live, tm.k, team, w, ng);
     };
     bool live = alive(tm.id), next = AHEAD && alive(tm.id + tm.count);
     if (AHEAD) ask(tm.id, live);
@@ -209,7 +263,7 @@ k_rn_fwd(const RnArgs a) {
             ask(row, live);
         }
         const bool now = live;
-        float p[E];
+        f2 p[H];
         IO::values(nu, p);
         const Raw rx = nx, rg = ng;
         if (AHEAD) {
@@ -218,97 +272,107 @@ k_rn_fwd(const RnArgs a) {
             next = alive(row + 2 * tm.count);
         }
         if (WIDE && !now) {                         // the whole CTA holds this row
-#pragma unroll
-            for (int q = 0; q < E; ++q) p[q] = 0.f;
-            if (r) IO::store(r + at, tm.k, team, w, p);
-            if (h) IO::store(h + at, tm.k, team, w, p);
+            if (r) IO::store_zeros(r + at, tm.k, team, w);
+            if (h) IO::store_zeros(h + at, tm.k, team, w);
             continue;
         }
-        auto values_of = [&](auto which, float (&c)[E]) {
+        auto values_of = [&](auto which, f2 (&c)[E / 2]) {
             constexpr int P = decltype(which)::value;
             if constexpr (KEEP) IO::values(kept[P], c);
             else IO::load(param[P], tm.k, team, w, c);
         };
-        auto norm = [&](float (&v)[E], int kind, auto first) {       // parameters `first` (gain) and the next (shift)
+        auto norm = [&](f2 (&v)[E / 2], int kind, auto first) {          // parameters `first` (gain) and the next (shift)
             if (kind == RN_NONE) return;
             constexpr int P = decltype(first)::value;
             float s[1];
             if (kind == RN_LAYER) {
-                s[0] = 0.f;
+                f2 t = v[0];
 #pragma unroll
-                for (int q = 0; q < E; ++q) s[0] += v[q];
+                for (int q = 1; q < H; ++q) t = t + v[q];
+                s[0] = across(t);
                 team_sum<WIDE, 1>(s, team, buf, turn);
-                const float mean = s[0] * a.inv_w;
-#pragma unroll
-                for (int q = 0; q < E; ++q) v[q] = on(q) ? v[q] - mean : 0.f;
+                IO::centre(v, s[0] * a.inv_w, tm.k, team, w);
             }
-            s[0] = 0.f;
+            f2 t = v[0] * v[0];
 #pragma unroll
-            for (int q = 0; q < E; ++q) s[0] += v[q] * v[q];
+            for (int q = 1; q < H; ++q) t = fma2(v[q], v[q], t);
+            s[0] = across(t);
             team_sum<WIDE, 1>(s, team, buf, turn);
-            const float rstd = rsqrtf(s[0] * a.inv_w + a.eps);
-            float c[E];
+            const f2 rstd = both(rsqrtf(s[0] * a.inv_w + a.eps));
+            f2 c[H];
             if (param[P]) {
                 values_of(first, c);
 #pragma unroll
-                for (int q = 0; q < E; ++q) v[q] *= rstd * c[q];
+                for (int q = 0; q < H; ++q) v[q] = v[q] * (rstd * c[q]);
             } else {
 #pragma unroll
-                for (int q = 0; q < E; ++q) v[q] *= rstd;
+                for (int q = 0; q < H; ++q) v[q] = v[q] * rstd;
             }
             if (param[P + 1]) {
                 values_of(std::integral_constant<int, P + 1>{}, c);
 #pragma unroll
-                for (int q = 0; q < E; ++q) v[q] += c[q];
+                for (int q = 0; q < H; ++q) v[q] = v[q] + c[q];
             }
         };
         norm(p, a.post, std::integral_constant<int, 0>{});
         if (gate) {
-            float c[E];
+            f2 c[H];
             IO::values(rg, c);
 #pragma unroll
-            for (int q = 0; q < E; ++q) p[q] *= c[q];
+            for (int q = 0; q < H; ++q) p[q] = p[q] * c[q];
         }
         if (x) {
-            float t[E];
+            f2 t[H];
             IO::values(rx, t);
+            const f2 al = both(a.alpha);
 #pragma unroll
-            for (int q = 0; q < E; ++q) p[q] += a.alpha * t[q];
+            for (int q = 0; q < H; ++q) p[q] = fma2(al, t[q], p[q]);
         }
-        if (!now) {
-#pragma unroll
-            for (int q = 0; q < E; ++q) p[q] = 0.f;
+        if (r && in) {
+            if (now) IO::store(r + at, tm.k, team, w, p);
+            else IO::store_zeros(r + at, tm.k, team, w);
         }
-        if (r && in) IO::store(r + at, tm.k, team, w, p);
         if (!h) continue;
         norm(p, a.pre, std::integral_constant<int, 2>{});
-        if (!now) {
-#pragma unroll
-            for (int q = 0; q < E; ++q) p[q] = 0.f;
+        if (in) {
+            if (now) IO::store(h + at, tm.k, team, w, p);
+            else IO::store_zeros(h + at, tm.k, team, w);
         }
-        if (in) IO::store(h + at, tm.k, team, w, p);
     }
 }
 
-// A team takes runs of consecutive rows of one group (a run is the whole group
-// or a part of it), a row a step; every team of the launch takes the same number
-// of steps.  While a row is worked on, the next one's elements are on their way
-// into registers (as they lie in memory: 4 registers a tensor), and the mask of
-// the row after that.
+// 16 bytes of global memory into shared memory, zeros where `there` is not set (the address is not read then).
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+
+// A crew takes runs of consecutive rows of one group (a run is the whole group
+// or a part of it).  A crew is a team, or a warp whose teams take a row each,
+// where groups are long enough: one sum of the gate's gradient a run then, and
+// 512 consecutive bytes a load.  Runs go to the crews of a CTA from far apart,
+// since masked rows, which cost little, come in stretches.
+//
+// With 8 bf16 elements a thread (AHEAD) the rows of the next steps are on their
+// way into shared memory, where each thread reads back what it copied itself.
+//
+// In a run the gate's row is the same, so the row sums that its gradient and
+// those of the post norm's gain and shift need are two, A = sum of g zh and
+// B = sum of g:  dgain += gate A, dshift += gate B, dgate = gain A + shift B.
 template <typename T, int VEC, int E, bool WIDE, int MAXT>
 __global__ void __launch_bounds__(MAXT, 512 / MAXT)
 k_rn_bwd(const RnArgs a) {
     using IO = RowIo<T, VEC, E>;
     using Raw = typename IO::Raw;
-    constexpr bool AHEAD = RnKeep<VEC, E, WIDE>::AHEAD, KEEP = RnKeep<VEC, E, WIDE>::KEEP;
+    constexpr int H = E / 2;
+    constexpr bool AHEAD = VEC == 8 && E == 8;
     __shared__ float buf[2][4][32];
     unsigned turn = 0;
-    const unsigned w = a.w, team = a.team;
-    const Team tm = my_team<WIDE>(team);
-    bool on_v[IO::NV];                               // a vector is in the row, or none of it
-#pragma unroll
-    for (int n = 0; n < IO::NV; ++n) on_v[n] = IO::col(n * VEC, tm.k, team) < w;
-    auto on = [&](int q) { return on_v[q / VEC]; };
+    const unsigned w = a.w, team = a.team, lane = threadIdx.x & 31;
+    const unsigned k = WIDE ? threadIdx.x : threadIdx.x % team;
+    // rows a crew takes a step, this thread's among them; the crew's number among the grid's
+    const unsigned abreast = WIDE ? 1 : a.crew / team, sub = WIDE ? 0 : threadIdx.x % a.crew / team;
+    const unsigned count = WIDE ? gridDim.x : blockDim.x / a.crew * gridDim.x;
+    const unsigned id = WIDE ? blockIdx.x : threadIdx.x / a.crew * gridDim.x + blockIdx.x;
     const T *u = static_cast<const T *>(a.u), *rin = static_cast<const T *>(a.rin), *dr = static_cast<const T *>(a.dr),
             *dh = static_cast<const T *>(a.dh), *gate = static_cast<const T *>(a.gate);
     T *dx = static_cast<T *>(a.dx), *du = static_cast<T *>(a.du);
@@ -316,240 +380,300 @@ k_rn_bwd(const RnArgs a) {
     // Sums of the gains' and shifts' gradients, post then pre: in registers, or, where a thread holds 16 columns
     // and they would not fit, in shared memory (each thread its own columns).
     constexpr bool IN_SMEM = E > 8;
-    extern __shared__ float acc[];                   // [4][w]
-    float sums[4][IN_SMEM ? 1 : E];
+    extern __shared__ __align__(16) float acc[];     // [4][w]; before the end of the AHEAD form, the rows to come
+    f2 sums[4][IN_SMEM ? 1 : H];
     if constexpr (IN_SMEM) {
         for (unsigned c = threadIdx.x; c < 4 * w; c += blockDim.x) acc[c] = 0.f;
         __syncthreads();
     } else {
 #pragma unroll
-        for (int q = 0; q < E; ++q) sums[0][q] = sums[1][q] = sums[2][q] = sums[3][q] = 0.f;
+        for (int q = 0; q < H; ++q) sums[0][q] = sums[1][q] = sums[2][q] = sums[3][q] = both(0.f);
     }
-    auto add = [&](auto which, int q, float v) {
+    // sums[P] += v * m
+    auto add = [&](auto which, int q, f2 v, f2 m) {
         constexpr int P = decltype(which)::value;
         if constexpr (IN_SMEM) {
-            if (on(q)) acc[P * w + IO::col(q, tm.k, team)] += v;
+            const f2 t = v * m;
+            if (IO::col(2 * q, k, team) < w) acc[P * w + IO::col(2 * q, k, team)] += lo(t);
+            if (IO::col(2 * q + 1, k, team) < w) acc[P * w + IO::col(2 * q + 1, k, team)] += hi(t);
         } else {
-            sums[P][q] += v;
+            sums[P][q] = fma2(v, m, sums[P][q]);
         }
     };
     Raw pre_g, post_g;
-    if (KEEP) {
-        IO::fetch(static_cast<const T *>(a.pre_g), a.pre_g, tm.k, team, w, pre_g);
-        IO::fetch(static_cast<const T *>(a.post_g), a.post_g, tm.k, team, w, post_g);
+    if (AHEAD) {
+        IO::fetch(static_cast<const T *>(a.pre_g), a.pre_g, k, team, w, pre_g);
+        IO::fetch(static_cast<const T *>(a.post_g), a.post_g, k, team, w, post_g);
     }
-    auto gain_of = [&](const void *p, const Raw &kept, float (&c)[E]) {
-        if constexpr (KEEP) IO::values(kept, c);
-        else IO::load(static_cast<const T *>(p), tm.k, team, w, c);
+    auto gain_of = [&](const void *p, const Raw &kept, f2 (&c)[E / 2]) {
+        if constexpr (AHEAD) IO::values(kept, c);
+        else IO::load(static_cast<const T *>(p), k, team, w, c);
     };
 
-    // A place in the team's sequence of rows.
+    // A place in the crew's sequence of rows.
     struct Place {
-        unsigned run, i, row0, n;                    // the run, the row in it, the run's first row and number of rows
-        bool in;
+        unsigned run, i, row0, n;                    // the run, the row in it (its crew's first), the run's first row and number of rows
     };
     auto enter = [&](Place &p) {                     // the run's rows
+        p.row0 = p.n = 0;
         if (p.run < a.runs) {
             const unsigned grp = p.run / a.runs_per_group, part = p.run - grp * a.runs_per_group;
             p.row0 = grp * a.group + part * a.run;
             p.n = min(a.run, a.group - part * a.run);
+        }
+    };
+    auto forward = [&](Place &p) {                   // true: into another run
+        p.i += abreast;
+        if (p.i < a.run) return false;
+        p.i = 0;
+        p.run = p.run < a.runs && a.runs - p.run > count ? p.run + count : a.runs;
+        enter(p);
+        return true;
+    };
+    auto inside = [&](const Place &p) { return p.i + sub < p.n; };
+    auto alive = [&](const Place &p) { return inside(p) && (!a.M || a.M[p.row0 + p.i + sub]); };
+    // the masks of a run's rows at once (up to 64), where all of the warp's lanes are in it
+    const bool one_run = WIDE || a.crew == 32;
+    auto masks = [&](const Place &p) {
+        const bool m0 = lane < p.n && (!a.M || a.M[p.row0 + lane]), m1 = lane + 32 < p.n && (!a.M || a.M[p.row0 + lane + 32]);
+        return (unsigned long long)__ballot_sync(0xffffffffu, m0) | (unsigned long long)__ballot_sync(0xffffffffu, m1) << 32;
+    };
+    // the crews of a warp take the same number of steps
+    const unsigned rounds = one_run ? (id < a.runs ? (a.runs - id + count - 1) / count : 0) : (a.runs + count - 1) / count;
+    const unsigned long long steps = (unsigned long long)rounds * ((a.run + abreast - 1) / abreast);
+
+    Place cons = {id, 0, 0, 0};
+    enter(cons);
+    Place prod = cons;
+    unsigned long long alive_run = AHEAD && one_run ? masks(prod) : 0;
+    unsigned lives = 0;                              // of the steps asked for, the latest in bit 0
+    const uint32_t slots = (uint32_t)__cvta_generic_to_shared(acc) + threadIdx.x * 16, slot = blockDim.x * 16, stage = 5 * slot;
+    const uint4 *slots_p = reinterpret_cast<const uint4 *>(acc) + threadIdx.x;
+    unsigned long long asked = 0;
+    const bool in_row = k * VEC < w;
+    auto ask = [&] {                                 // the next step's rows into its stage
+        if (asked < steps) {
+            const bool live = one_run ? (alive_run >> (prod.i + sub)) & 1 : alive(prod);
+            const uint32_t to = slots + (unsigned)(asked % RN_DEPTH) * stage;
+            const size_t at = (size_t)(prod.row0 + prod.i + sub) * w + k * VEC;
+            const bool there = live && in_row;
+            if (dr) copy16(to, dr + (there ? at : 0), there);
+            if (has_pre) {
+                copy16(to + slot, dh + (there ? at : 0), there);
+                copy16(to + 2 * slot, rin + (there ? at : 0), there);
+            }
+            if (need_u) copy16(to + 3 * slot, u + (there ? at : 0), there);
+            if (gate && prod.i == 0) {
+                const bool has = prod.run < a.runs && in_row;
+                copy16(to + 4 * slot, gate + (has ? (size_t)(prod.run / a.runs_per_group) * w + k * VEC : 0), has);
+            }
+            lives = lives << 1 | (live ? 1u : 0u);
+            if (forward(prod) && one_run) alive_run = masks(prod);
+        }
+        ++asked;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if constexpr (AHEAD) {
+        for (int d = 0; d < RN_DEPTH - 1; ++d) ask();
+    }
+    Raw c_dr, c_dh, c_r, c_u, gt;
+    auto fetch_all = [&](bool live) {
+        const size_t at = (size_t)(live ? cons.row0 + cons.i + sub : 0) * w;
+        IO::fetch(dr + at, live && dr, k, team, w, c_dr);
+        IO::fetch(dh + at, live && has_pre, k, team, w, c_dh);
+        IO::fetch(rin + at, live && has_pre, k, team, w, c_r);
+        IO::fetch(u + at, live && need_u, k, team, w, c_u);
+        if (cons.i == 0 && gate) IO::fetch(gate + (size_t)(cons.run < a.runs ? cons.run / a.runs_per_group : 0) * w, true, k, team, w, gt);
+    };
+    f2 sa[H], sb[H];                                 // the run's A and B
+    for (unsigned long long step = 0; step < steps; ++step) {
+        bool live;
+        if constexpr (AHEAD) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(RN_DEPTH - 2) : "memory");
+            const unsigned ahead = (unsigned)min((unsigned long long)(RN_DEPTH - 1), steps - step);
+            live = (lives >> (ahead - 1)) & 1;
+            const uint4 *from = slots_p + (unsigned)(step % RN_DEPTH) * 5 * blockDim.x;
+            c_dr.v[0] = dr ? from[0] : make_uint4(0, 0, 0, 0);
+            c_dh.v[0] = from[blockDim.x];
+            c_r.v[0] = from[2 * blockDim.x];
+            c_u.v[0] = from[3 * blockDim.x];
+            if (cons.i == 0) gt.v[0] = from[4 * blockDim.x];
+            ask();                                   // into the stage that the last step read
         } else {
-            p.row0 = p.n = 0;
+            live = alive(cons);
+            fetch_all(live);
         }
-    };
-    auto forward = [&](Place &p) {
-        if (++p.i == a.run) {
-            p.i = 0;
-            p.run = a.runs - p.run > tm.count && p.run < a.runs ? p.run + tm.count : a.runs;
-            enter(p);
-        }
-        p.in = p.i < p.n;
-    };
-    auto alive = [&](const Place &p) { return p.in && (!a.M || a.M[p.row0 + p.i]); };
-    Raw n_dr, n_dh, n_r, n_u, n_gate;
-    auto ask = [&](const Place &p, bool live) {
-        const size_t at = (size_t)(live ? p.row0 + p.i : 0) * w;
-        IO::fetch(dr + at, live && dr, tm.k, team, w, n_dr);
-        IO::fetch(dh + at, live && has_pre, tm.k, team, w, n_dh);
-        IO::fetch(rin + at, live && has_pre, tm.k, team, w, n_r);
-        IO::fetch(u + at, live && need_u, tm.k, team, w, n_u);
-    };
-    auto ask_gate = [&](const Place &p) {
-        if (p.i == 0) IO::fetch(gate + (size_t)(p.run < a.runs ? p.run / a.runs_per_group : 0) * w, gate, tm.k, team, w, n_gate);
-    };
-    Place at0 = {tm.id, 0, 0, 0, false};
-    enter(at0);
-    at0.in = at0.n > 0;
-    Place at1 = at0;
-    if (AHEAD) forward(at1);
-    bool live0 = alive(at0), live1 = AHEAD && alive(at1);
-    if (AHEAD) ask(at0, live0);
-    ask_gate(at0);
-    Raw gt = n_gate;
-    float s_gate[E];
-    const unsigned steps = WIDE ? (tm.id < a.runs ? (a.runs - tm.id + tm.count - 1) / tm.count : 0)
-                                : (a.runs + tm.count - 1) / tm.count;
-    for (unsigned long long left = (unsigned long long)steps * a.run; left; --left) {
-        const Place here = at0;
-        if (!AHEAD) {
-            live0 = alive(here);
-            ask(here, live0);
-            ask_gate(here);
-        }
-        const bool in = here.in, live = live0;
-        const size_t at = (size_t)(in ? here.row0 + here.i : 0) * w;
-        if (here.i == 0) {
-            gt = n_gate;
+        const bool in = inside(cons);
+        const size_t at = (size_t)(in ? cons.row0 + cons.i + sub : 0) * w;
+        if (cons.i == 0) {
 #pragma unroll
-            for (int q = 0; q < E; ++q) s_gate[q] = 0.f;
-        }
-        const Raw c_dr = n_dr, c_dh = n_dh, c_r = n_r, c_u = n_u;
-        if (AHEAD) {
-            ask(at1, live1);
-            ask_gate(at1);
-            at0 = at1;
-            live0 = live1;
-            forward(at1);
-            live1 = alive(at1);
-        } else {
-            forward(at0);
+            for (int q = 0; q < H; ++q) sa[q] = sb[q] = both(0.f);
         }
         if (WIDE ? !live : !__any_sync(0xffffffffu, live)) {
-            float z[E];
-#pragma unroll
-            for (int q = 0; q < E; ++q) z[q] = 0.f;
-            if (in && dx) IO::store(dx + at, tm.k, team, w, z);
-            if (in && du) IO::store(du + at, tm.k, team, w, z);
+            if (in && dx) IO::store_zeros(dx + at, k, team, w);
+            if (in && du) IO::store_zeros(du + at, k, team, w);
         } else {
-            float g[E], d[E], z[E];
+            // rows that are not live hold zeros, and add zeros to every sum
+            f2 g[H], d[H], z[H];
             IO::values(c_dr, g);
-            // d becomes norm'(d; z), z is centred; returns 1 / deviation
-            auto back = [&](float (&d)[E], float (&z)[E], int kind, const void *gain, const Raw &kept, auto first) {
-                constexpr int P = decltype(first)::value;
+            // d becomes norm'(d; z), z normalised; sum(q, d, zh) adds to the parameters' sums
+            auto back = [&](f2 (&d)[E / 2], f2 (&z)[E / 2], int kind, const void *gain, const Raw &kept, auto &&sum) {
                 if (kind == RN_LAYER) {
-                    float s[1] = {0.f};
+                    f2 t = z[0];
 #pragma unroll
-                    for (int q = 0; q < E; ++q) s[0] += z[q];
+                    for (int q = 1; q < H; ++q) t = t + z[q];
+                    float s[1] = {across(t)};
                     team_sum<WIDE, 1>(s, team, buf, turn);
-                    const float mean = s[0] * a.inv_w;
-#pragma unroll
-                    for (int q = 0; q < E; ++q) z[q] = on(q) ? z[q] - mean : 0.f;
+                    IO::centre(z, s[0] * a.inv_w, k, team, w);
                 }
-                float e[E];
+                f2 e[H];
                 if (gain) {
                     gain_of(gain, kept, e);
 #pragma unroll
-                    for (int q = 0; q < E; ++q) e[q] *= d[q];
+                    for (int q = 0; q < H; ++q) e[q] = e[q] * d[q];
                 } else {
 #pragma unroll
-                    for (int q = 0; q < E; ++q) e[q] = d[q];
+                    for (int q = 0; q < H; ++q) e[q] = d[q];
                 }
-                float s[3] = {0.f, 0.f, 0.f};
+                f2 zz = z[0] * z[0], ez = e[0] * z[0], es = e[0];
 #pragma unroll
-                for (int q = 0; q < E; ++q) {
-                    s[0] += z[q] * z[q];
-                    s[1] += e[q] * z[q];
-                    s[2] += e[q];
+                for (int q = 1; q < H; ++q) {
+                    zz = fma2(z[q], z[q], zz);
+                    ez = fma2(e[q], z[q], ez);
+                    es = es + e[q];
                 }
+                float s[3] = {across(zz), across(ez), across(es)};
                 team_sum<WIDE, 3>(s, team, buf, turn);
                 const float rstd = rsqrtf(s[0] * a.inv_w + a.eps);
-                const float c1 = s[1] * a.inv_w * rstd * rstd, c2 = kind == RN_LAYER ? s[2] * a.inv_w : 0.f;
+                const f2 rs = both(rstd), c1 = both(-(s[1] * a.inv_w * rstd));
+                const f2 c2 = both(kind == RN_LAYER ? -(s[2] * a.inv_w) : 0.f);
 #pragma unroll
-                for (int q = 0; q < E; ++q) {
-                    add(std::integral_constant<int, P>{}, q, d[q] * (z[q] * rstd));
-                    add(std::integral_constant<int, P + 1>{}, q, d[q]);
-                    d[q] = (e[q] - c2 - z[q] * c1) * rstd;
+                for (int q = 0; q < H; ++q) {
+                    z[q] = z[q] * rs;
+                    sum(q, d[q], z[q]);
+                    d[q] = (fma2(z[q], c1, e[q]) + c2) * rs;
                 }
-                return rstd;
             };
             if (has_pre) {
                 IO::values(c_dh, d);
                 IO::values(c_r, z);
-                back(d, z, a.pre, a.pre_g, pre_g, std::integral_constant<int, 2>{});
+                back(d, z, a.pre, a.pre_g, pre_g, [&](int q, f2 dq, f2 zh) {
+                    add(std::integral_constant<int, 2>{}, q, dq, zh);
+                    add(std::integral_constant<int, 3>{}, q, dq, both(1.f));
+                });
 #pragma unroll
-                for (int q = 0; q < E; ++q) g[q] = live ? g[q] + d[q] : 0.f;
+                for (int q = 0; q < H; ++q) g[q] = g[q] + d[q];
             }
             if (dx && in) {
+                const f2 al = both(a.alpha);
 #pragma unroll
-                for (int q = 0; q < E; ++q) z[q] = a.alpha * g[q];
-                IO::store(dx + at, tm.k, team, w, z);
+                for (int q = 0; q < H; ++q) z[q] = al * g[q];
+                if (live) IO::store(dx + at, k, team, w, z);
+                else IO::store_zeros(dx + at, k, team, w);
             }
             if (gate) {
                 IO::values(gt, d);
 #pragma unroll
-                for (int q = 0; q < E; ++q) d[q] *= g[q];
+                for (int q = 0; q < H; ++q) d[q] = d[q] * g[q];
             } else {
 #pragma unroll
-                for (int q = 0; q < E; ++q) d[q] = g[q];
+                for (int q = 0; q < H; ++q) d[q] = g[q];
             }
             IO::values(c_u, z);
             if (a.post != RN_NONE) {
-                const float rstd = back(d, z, a.post, a.post_g, post_g, std::integral_constant<int, 0>{});
-                if (gate) {                          // p = gain zh + shift; z is centred
-                    float c[E];
+                back(d, z, a.post, a.post_g, post_g, [&](int q, f2, f2 zh) {
+                    sa[q] = fma2(g[q], zh, sa[q]);
+                    sb[q] = sb[q] + g[q];
+                });
+            } else if (gate) {
+#pragma unroll
+                for (int q = 0; q < H; ++q) sa[q] = fma2(g[q], z[q], sa[q]);
+            }
+            if (du && in) {
+                if (live) IO::store(du + at, k, team, w, d);
+                else IO::store_zeros(du + at, k, team, w);
+            }
+        }
+        if (cons.i + abreast >= a.run) {             // the run's last step
+            f2 c[H];
+            if (gate) {
+                IO::values(gt, c);
+            } else {
+#pragma unroll
+                for (int q = 0; q < H; ++q) c[q] = both(1.f);
+            }
+            if (a.post != RN_NONE && (!gate || cons.run < a.runs)) {
+#pragma unroll
+                for (int q = 0; q < H; ++q) {
+                    add(std::integral_constant<int, 0>{}, q, sa[q], c[q]);
+                    add(std::integral_constant<int, 1>{}, q, sb[q], c[q]);
+                }
+            }
+            if (a.dgate) {
+                if (a.post != RN_NONE) {
                     if (a.post_g) {
                         gain_of(a.post_g, post_g, c);
 #pragma unroll
-                        for (int q = 0; q < E; ++q) z[q] *= rstd * c[q];
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < E; ++q) z[q] *= rstd;
+                        for (int q = 0; q < H; ++q) sa[q] = sa[q] * c[q];
                     }
                     if (a.post_s) {
-                        IO::load(static_cast<const T *>(a.post_s), tm.k, team, w, c);
+                        IO::load(static_cast<const T *>(a.post_s), k, team, w, c);
 #pragma unroll
-                        for (int q = 0; q < E; ++q) z[q] += c[q];
+                        for (int q = 0; q < H; ++q) sa[q] = fma2(sb[q], c[q], sa[q]);
+                    }
+                }
+                if (!WIDE && abreast > 1) {          // the crew's teams, in pairs
+                    for (unsigned o = team; o < 32; o <<= 1)
+#pragma unroll
+                        for (int q = 0; q < H; ++q)
+                            sa[q] = sa[q] + pair(__shfl_xor_sync(0xffffffffu, lo(sa[q]), o), __shfl_xor_sync(0xffffffffu, hi(sa[q]), o));
+                }
+                if (cons.run < a.runs && sub == 0) {
+                    if (a.runs_per_group == 1) {
+                        IO::store(static_cast<T *>(a.dgate) + (size_t)cons.run * w, k, team, w, sa);
+                    } else {
+                        float *o = a.gparts + (size_t)cons.run * w;
+#pragma unroll
+                        for (int q = 0; q < H; ++q) {
+                            if (IO::col(2 * q, k, team) < w) o[IO::col(2 * q, k, team)] = lo(sa[q]);
+                            if (IO::col(2 * q + 1, k, team) < w) o[IO::col(2 * q + 1, k, team)] = hi(sa[q]);
+                        }
                     }
                 }
             }
-            if (gate) {
-#pragma unroll
-                for (int q = 0; q < E; ++q) s_gate[q] += g[q] * z[q];
-            }
-            if (du && in) {
-                if (!live) {
-#pragma unroll
-                    for (int q = 0; q < E; ++q) d[q] = 0.f;
-                }
-                IO::store(du + at, tm.k, team, w, d);
-            }
         }
-        if (here.i == a.run - 1 && a.dgate && here.run < a.runs) {
-            if (a.runs_per_group == 1) {
-                IO::store(static_cast<T *>(a.dgate) + (size_t)here.run * w, tm.k, team, w, s_gate);
-            } else {
-                float *o = a.gparts + (size_t)here.run * w;
-#pragma unroll
-                for (int q = 0; q < E; ++q)
-                    if (on(q)) o[IO::col(q, tm.k, team)] = s_gate[q];
-            }
-        }
+        forward(cons);
+    }
+    if constexpr (AHEAD) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();                             // the sums take the rows' place
     }
     // The CTA's sums: its warps' teams by shuffles (same columns), the warps one after another.
     float *out = a.parts + (size_t)blockIdx.x * 4 * w;
     if constexpr (WIDE && !IN_SMEM) {
 #pragma unroll
         for (int q = 0; q < E; ++q)
-            if (on(q)) {
+            if (IO::col(q, k, team) < w) {
 #pragma unroll
-                for (int n = 0; n < 4; ++n) out[n * w + IO::col(q, tm.k, team)] = sums[n][q];
+                for (int n = 0; n < 4; ++n) out[n * w + IO::col(q, k, team)] = q & 1 ? hi(sums[n][q / 2]) : lo(sums[n][q / 2]);
             }
     } else if constexpr (!IN_SMEM) {
-        const unsigned lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+        const unsigned warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
 #pragma unroll
-        for (int q = 0; q < E; ++q)
+        for (int q = 0; q < H; ++q)
 #pragma unroll
             for (int n = 0; n < 4; ++n)
-                for (unsigned o = team; o < 32; o <<= 1) sums[n][q] += __shfl_xor_sync(0xffffffffu, sums[n][q], o);
+                for (unsigned o = team; o < 32; o <<= 1)
+                    sums[n][q] = sums[n][q] + pair(__shfl_xor_sync(0xffffffffu, lo(sums[n][q]), o), __shfl_xor_sync(0xffffffffu, hi(sums[n][q]), o));
         for (unsigned v = 0; v < nw; ++v) {
             if (warp == v && lane < team) {
 #pragma unroll
                 for (int q = 0; q < E; ++q)
-                    if (on(q)) {
+                    if (IO::col(q, k, team) < w) {
 #pragma unroll
                         for (int n = 0; n < 4; ++n) {
-                            float &o = acc[n * w + IO::col(q, tm.k, team)];
-                            o = (v ? o : 0.f) + sums[n][q];
+                            float &o = acc[n * w + IO::col(q, k, team)];
+                            o = (v ? o : 0.f) + (q & 1 ? hi(sums[n][q / 2]) : lo(sums[n][q / 2]));
                         }
                     }
             }
@@ -604,7 +728,7 @@ __global__ void __launch_bounds__(1024) k_rn_finish(const FinishArgs f) {
 
 struct RnPlan {
     bool vec, wide;
-    int e, team, threads, ctas_fwd, ctas_bwd;
+    int e, team, crew, threads, ctas_fwd, ctas_bwd;
     unsigned run, runs_per_group, runs;
     size_t parts, gparts, total;      // workspace offsets
 };
@@ -624,16 +748,21 @@ static RnPlan rn_plan(const eaga_residual_norm_dims &d) {
     p.threads = p.wide ? p.team : 256;
     const long long per = p.wide ? 1 : p.threads / p.team;
     const long long rows = d.rows, sms = sm_count();
-    const long long room = sms * (512 / p.threads);        // the registers: 512 threads an SM, 768 or 1024 forward
+    // the registers: 512 threads an SM backward, 768 or 1024 forward
     p.ctas_fwd = (int)std::max(1LL, std::min((rows + per - 1) / per, p.wide ? sms * (p.e > 8 ? 1 : 1024 / p.threads) : sms * 3));
-    p.ctas_bwd = (int)std::max(1LL, std::min((rows + per - 1) / per, room));
-    // runs: at least about four for each team, of 16 rows or more where groups are that long
-    const long long groups = std::max(1LL, rows / d.rows_per_group), teams = p.ctas_bwd * per;
-    long long per_group = std::max(1LL, (4 * teams + groups - 1) / groups);
-    per_group = std::max(1LL, std::min(per_group, (d.rows_per_group + 15) / 16));
-    p.run = (unsigned)((d.rows_per_group + per_group - 1) / per_group);
+    // Backward.  A run costs a partial row of the gate's gradient, a CTA one of each parameter's: runs of four rows a team
+    // or more (up to 64 rows, whose masks a warp holds), long inputs eight or more a crew.
+    p.crew = p.wide ? p.team : d.rows_per_group >= 2 * 32 / p.team ? 32 : p.team;
+    const long long abreast = p.crew / p.team, crews = p.threads / p.crew, room = sms * (512 / p.threads);
+    long long want = std::max(4 * abreast, (rows + room * crews - 1) / (room * crews));
+    const long long most = p.wide ? 64 : std::max(abreast, std::min(64LL, 16 * abreast) / abreast * abreast);
+    if (want > 4 * abreast) want = std::max(std::min(most, 4 * abreast), std::min(most, (rows + 8 * room * crews - 1) / (8 * room * crews)));
+    want = std::min(want, most);
+    const long long parts = std::max(1LL, (d.rows_per_group + want - 1) / want);
+    p.run = (unsigned)(((d.rows_per_group + parts - 1) / parts + abreast - 1) / abreast * abreast);
     p.runs_per_group = (unsigned)((d.rows_per_group + p.run - 1) / p.run);
     p.runs = (unsigned)(rows / d.rows_per_group * p.runs_per_group);
+    p.ctas_bwd = (int)std::max(1LL, std::min((p.runs + crews - 1) / crews, room));
     p.parts = 0;
     p.gparts = align256((size_t)p.ctas_bwd * 4 * d.w * 4);
     p.total = p.gparts + (p.runs_per_group > 1 ? align256((size_t)p.runs * d.w * 4) : 0);
@@ -676,7 +805,7 @@ static RnArgs rn_args(const eaga_residual_norm_dims &d, const RnPlan &p) {
     a.alpha = d.alpha; a.eps = d.eps; a.inv_w = 1.f / (float)d.w;
     a.rows = (unsigned)d.rows; a.w = (unsigned)d.w; a.group = (unsigned)d.rows_per_group;
     a.run = p.run; a.runs_per_group = p.runs_per_group; a.runs = p.runs;
-    a.pre = d.pre; a.post = d.post; a.team = p.team;
+    a.pre = d.pre; a.post = d.post; a.team = p.team; a.crew = p.crew;
     return a;
 }
 
@@ -773,11 +902,14 @@ eaga_status eaga_residual_norm_backward(const eaga_residual_norm_dims *d, const 
     a.gparts = reinterpret_cast<float *>(ws + p.gparts);
     cudaError_t e = rn_dispatch(*d, p, [&](auto t, auto vec, auto el, auto wide, auto maxt) {
         constexpr int E = decltype(el)::value;
-        const size_t smem = decltype(wide)::value && E == 8 ? 0 : (size_t)4 * d->w * 4;
+        constexpr bool AHEAD = decltype(vec)::value == 8 && E == 8;
+        const size_t sums = decltype(wide)::value && E == 8 ? 0 : (size_t)4 * d->w * 4;
+        const size_t smem = std::max(sums, AHEAD ? (size_t)RN_DEPTH * 5 * 16 * p.threads : 0);
         auto kernel = k_rn_bwd<decltype(t), decltype(vec)::value, E, decltype(wide)::value, decltype(maxt)::value>;
-        if (E > 8) {
+        if (E > 8 || AHEAD) {
             static std::atomic<uint32_t> attr_set{0};
-            if (cudaError_t err = ensure_smem_attr(kernel, 4 * 8192 * 4, attr_set); err != cudaSuccess) return err;
+            const int most = E > 8 ? 4 * 8192 * 4 : RN_DEPTH * 5 * 16 * decltype(maxt)::value;
+            if (cudaError_t err = ensure_smem_attr(kernel, most, attr_set); err != cudaSuccess) return err;
         }
         kernel<<<p.ctas_bwd, p.threads, smem, st>>>(a);
         return cudaGetLastError();

@@ -167,6 +167,7 @@ __device__ __forceinline__ unsigned scaled_bits(float a, float scale, bool zero)
 template <typename PT, typename GT, int BITS, bool MASTER, int CAP>
 __global__ void __launch_bounds__(AD_THR)
 k_adamw(const __grid_constant__ AdTable<CAP> tab) {
+    after_previous();
     const AdScalars &s = tab.s;
     __shared__ float sh_size, sh_inv;
     __shared__ double sh_lr;
@@ -255,6 +256,7 @@ k_adamw(const __grid_constant__ AdTable<CAP> tab) {
             }
         }
     }
+    before_next();
     // The last CTA of the call's last launch to have read the step advances it.
     if (s.advance && threadIdx.x == 0) {
         unsigned *done = reinterpret_cast<unsigned *>(s.state + 1);
@@ -267,6 +269,7 @@ k_adamw(const __grid_constant__ AdTable<CAP> tab) {
 template <int CAP>
 __global__ void __launch_bounds__(AD_THR)
 k_adamw_unpack(const __grid_constant__ AdTable<CAP> tab) {
+    after_previous();
     const AdScalars &s = tab.s;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (unsigned tile = blockIdx.x; tile < s.tiles; tile += gridDim.x) {
@@ -307,15 +310,13 @@ template <typename PT, typename GT, int BITS, bool MASTER>
 struct StepLaunch {
     template <int CAP>
     static cudaError_t go(const AdTable<CAP> &t, cudaStream_t st) {
-        k_adamw<PT, GT, BITS, MASTER, CAP><<<ad_grid(t.s.tiles), AD_THR, 0, st>>>(t);
-        return cudaGetLastError();
+        return launch_pdl(k_adamw<PT, GT, BITS, MASTER, CAP>, dim3(ad_grid(t.s.tiles)), dim3(AD_THR), 0, st, 1, t);
     }
 };
 struct UnpackLaunch {
     template <int CAP>
     static cudaError_t go(const AdTable<CAP> &t, cudaStream_t st) {
-        k_adamw_unpack<CAP><<<ad_grid(t.s.tiles), AD_THR, 0, st>>>(t);
-        return cudaGetLastError();
+        return launch_pdl(k_adamw_unpack<CAP>, dim3(ad_grid(t.s.tiles)), dim3(AD_THR), 0, st, 1, t);
     }
 };
 

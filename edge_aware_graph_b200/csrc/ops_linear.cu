@@ -42,6 +42,7 @@ __device__ __forceinline__ float take_part(float &v) {
 
 template <typename T>
 __global__ void __launch_bounds__(256) k_lin_prep(const __grid_constant__ PrepArgs a) {
+    after_previous();
     const PrepJob &j = a.job[blockIdx.y];
     const int per = j.ld / 8;
     const bool vec = (long long)j.n * sizeof(T) % 16 == 0;
@@ -78,6 +79,7 @@ __global__ void __launch_bounds__(256) k_lin_prep(const __grid_constant__ PrepAr
 template <int VEC>
 __global__ void __launch_bounds__(256)
 k_lin_reduce(const float *acc, float *dW, long long n, int splits, const float *bacc, float *db, int out, int bparts, unsigned wblocks) {
+    after_previous();
     __shared__ float sum[8][32 * VEC];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const bool is_w = blockIdx.x < wblocks;
@@ -176,8 +178,7 @@ static cudaError_t lin_prep(const PrepJob *jobs, int n, cudaStream_t st) {
         most = std::max(most, (jobs[k].rows * (jobs[k].ld / 8) + 255) / 256);
     }
     const unsigned grid = (unsigned)std::max(1LL, std::min(most, 16LL * sm_count()));
-    k_lin_prep<T><<<dim3(grid, n), 256, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_pdl(k_lin_prep<T>, dim3(grid, n), dim3(256), 0, st, 1, a);
 }
 
 // Whichever of the two sums is in more than one part.
@@ -187,9 +188,7 @@ static cudaError_t lin_reduce(long long n, int splits, const float *acc, float *
     const long long per = v4 ? 128 : 32;
     const unsigned wb = splits > 1 ? (unsigned)((n + per - 1) / per) : 0, bb = db && bparts > 1 ? (unsigned)((out + per - 1) / per) : 0;
     if (!(wb + bb)) return cudaSuccess;
-    if (v4) k_lin_reduce<4><<<wb + bb, 256, 0, st>>>(acc, dW, n, splits, bacc, db, out, bparts, wb);
-    else k_lin_reduce<1><<<wb + bb, 256, 0, st>>>(acc, dW, n, splits, bacc, db, out, bparts, wb);
-    return cudaGetLastError();
+    return launch_pdl(v4 ? k_lin_reduce<4> : k_lin_reduce<1>, dim3(wb + bb), dim3(256), 0, st, 1, acc, dW, n, splits, bacc, db, out, bparts, wb);
 }
 
 static Span span(const void *q, size_t b) { return Span{q, q ? b : 0}; }

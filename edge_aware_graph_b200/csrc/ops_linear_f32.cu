@@ -28,6 +28,7 @@ struct LfParams {
 template <int KIND, int BT>
 __global__ void __launch_bounds__(256)
 k_lin_f32(const LfParams p) {
+    after_previous();
     constexpr int TM = BT / 16, PER = BT * LF_BK / 256;
     __shared__ float sa[2][LF_BK][BT + 4], sb[2][LF_BK][BT + 4];
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
@@ -92,6 +93,7 @@ k_lin_f32(const LfParams p) {
         if (more) keep(b ^ 1);
         __syncthreads();
     }
+    before_next();
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
         const int m = m0 + ty * TM + i;
@@ -137,9 +139,7 @@ static cudaError_t lf_launch(const LfParams &p, int splits, cudaStream_t st) {
     const int bt = tiles(64) * splits >= sm_count() ? 64 : 32;
     if (tiles(bt) > 0x7fffffffLL) return cudaErrorInvalidValue;
     const dim3 grid((unsigned)tiles(bt), splits);
-    if (bt == 64) k_lin_f32<KIND, 64><<<grid, 256, 0, st>>>(p);
-    else k_lin_f32<KIND, 32><<<grid, 256, 0, st>>>(p);
-    return cudaGetLastError();
+    return launch_pdl(bt == 64 ? k_lin_f32<KIND, 64> : k_lin_f32<KIND, 32>, grid, dim3(256), 0, st, 1, p);
 }
 
 cudaError_t lin_f32_forward(const LinF32 &q, const LinEpi<float> &e, cudaStream_t st) {

@@ -152,7 +152,6 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
         for (int k = 0; k < 3 * LT_EPI; ++k) mbar_init(drained + 8 + 8 * k, 1);
         fence_mbar_init();
         *fail = 0;
-        if (p.clear && blockIdx.x == 0) *p.status = 0;       // a wait that gives up does so a second later
     }
     if (w == 1) {
         if constexpr (PAIR) {
@@ -163,6 +162,8 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
             tmem_relinquish();
         }
     }
+    after_previous();
+    if (p.clear && blockIdx.x == 0 && tid == 0) *p.status = 0;     // a wait that gives up does so a second later
     tc_fence_before();
     __syncthreads();
     if constexpr (PAIR) cluster_sync_all();                  // the other CTA's barriers are there
@@ -646,6 +647,7 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
             __syncwarp();
         }
     }
+    before_next();
     tc_fence_before();
     __syncthreads();
     if constexpr (PAIR) cluster_sync_all();
@@ -674,18 +676,7 @@ static cudaError_t lt_launch(const LtMaps &m, const LtParams<TO> &p, cudaStream_
         }
         if (r < LT_REGS) return cudaErrorLaunchOutOfResources;
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(std::min(p.units, sm_count() / CG) * CG));
-    cfg.blockDim = dim3(LT_THR);
-    cfg.dynamicSmemBytes = S::BYTES;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CG;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = CG > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, m, p);
+    return launch_pdl(kernel, dim3((unsigned)(std::min(p.units, sm_count() / CG) * CG)), dim3(LT_THR), S::BYTES, st, CG, m, p);
 }
 template <int KIND, typename TO, bool VEC>
 static cudaError_t lt_run(const LinTile &t, const LtMaps &m, const LtParams<TO> &p, cudaStream_t st) {

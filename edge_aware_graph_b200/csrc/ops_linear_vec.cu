@@ -9,6 +9,7 @@
 // no workspace.  Backward: a warp takes a row of W, the same row of dW and one
 // column of dX, with dZ (all rows) in shared memory.
 #include <algorithm>
+#include <type_traits>
 #include "ops_linear.h"
 #include "sm100.cuh"
 
@@ -17,30 +18,37 @@ namespace ops {
 
 using namespace sm100;
 
+// VEC consecutive weights as they lie in memory, and their values.
 template <typename T, int VEC>
-__device__ __forceinline__ void vec_load(const T *p, float (&v)[VEC]) {
-    if constexpr (VEC == 1) {
-        v[0] = ldf(p);
-    } else if constexpr (VEC == 4) {
-        const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    } else {
-        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p));
-        const unsigned x[4] = {a.x, a.y, a.z, a.w};
+struct VecIo {
+    typedef typename std::conditional<VEC == 1, T, uint4>::type Raw;
+    static __device__ __forceinline__ Raw fetch(const T *p) { return __ldg(reinterpret_cast<const Raw *>(p)); }
+    static __device__ __forceinline__ void values(const Raw &a, float (&v)[VEC]) {
+        if constexpr (VEC == 1) {
+            v[0] = ldf(&a);
+        } else {
+            const unsigned x[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[2 * j] = __uint_as_float(x[j] << 16);
-            v[2 * j + 1] = __uint_as_float(x[j] & 0xffff0000u);
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (VEC == 4) {
+                    v[j] = __uint_as_float(x[j]);
+                } else {
+                    v[2 * j] = __uint_as_float(x[j] << 16);
+                    v[2 * j + 1] = __uint_as_float(x[j] & 0xffff0000u);
+                }
+            }
         }
     }
-}
+};
 
 constexpr int LV_CHUNK = 512;      // rows of W whose X is in shared memory at once
+constexpr int LV_BATCH = 8;        // loads a thread has in flight
 
 // R: rows (the call's, rounded up).  part: rows of W a CTA takes.
 template <typename T, int VEC, int R>
 __global__ void __launch_bounds__(256)
 k_lin_vec_fwd(const LinVec<T> p, const LinEpi<T> e, int part, int cluster) {
+    after_previous();
     constexpr int LANES = VEC == 1 ? 32 : 8, C = LANES * VEC, KR = 256 / LANES;
     __shared__ float xs[R][LV_CHUNK];
     __shared__ float red[8][R][C];
@@ -56,23 +64,33 @@ k_lin_vec_fwd(const LinVec<T> p, const LinEpi<T> e, int part, int cluster) {
     for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int j = 0; j < VEC; ++j) acc[r][j] = 0.f;
+    typedef VecIo<T, VEC> IO;
     for (int kb = k0; kb < k1; kb += LV_CHUNK) {
         const int n = min(LV_CHUNK, k1 - kb);
+        const T *w = p.W + (size_t)kb * p.out + col;
+        typename IO::Raw raw[LV_BATCH];
+        auto fetch = [&](int k) {                    // rows k, k + KR, ..
+#pragma unroll
+            for (int i = 0; i < LV_BATCH; ++i)
+                if (on && k + i * KR < n) raw[i] = IO::fetch(w + (size_t)(k + i * KR) * p.out);
+        };
+        fetch(kr);                                   // on their way before X is there
         __syncthreads();
         for (int i = tid; i < R * LV_CHUNK; i += 256) {
             const int r = i / LV_CHUNK, k = i % LV_CHUNK;
             xs[r][k] = r < p.rows && k < n ? ldf(p.X + (size_t)r * p.in + kb + k) : 0.f;
         }
         __syncthreads();
-        if (on) {
-            const T *w = p.W + (size_t)kb * p.out + col;
-#pragma unroll 8
-            for (int k = kr; k < n; k += KR) {
+        for (int k = kr; k < n; k += LV_BATCH * KR) {
+            if (k != kr) fetch(k);
+#pragma unroll
+            for (int i = 0; i < LV_BATCH; ++i) {
+                if (!on || k + i * KR >= n) break;
                 float v[VEC];
-                vec_load<T, VEC>(w + (size_t)k * p.out, v);
+                IO::values(raw[i], v);
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    const float x = xs[r][k];
+                    const float x = xs[r][k + i * KR];
 #pragma unroll
                     for (int j = 0; j < VEC; ++j) acc[r][j] += x * v[j];
                 }
@@ -90,6 +108,7 @@ k_lin_vec_fwd(const LinVec<T> p, const LinEpi<T> e, int part, int cluster) {
             }
             if (lane < LANES) red[warp][r][cl * VEC + j] = s;
         }
+    before_next();
     __syncthreads();
     for (int i = tid; i < R * C; i += 256) {
         float s = 0.f;
@@ -126,6 +145,7 @@ k_lin_vec_fwd(const LinVec<T> p, const LinEpi<T> e, int part, int cluster) {
 template <typename T, int VEC, int R>
 __global__ void __launch_bounds__(256)
 k_lin_vec_bwd(const LinVec<T> p, const LinEpi<T> e) {
+    after_previous();
     constexpr int CC = 8192 / R;               // columns of dZ at once
     __shared__ __align__(16) float dz[R][CC];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -170,7 +190,7 @@ k_lin_vec_bwd(const LinVec<T> p, const LinEpi<T> e) {
             for (int c = lane * VEC; c < n; c += 32 * VEC) {
                 float v[VEC], s[VEC];
                 if (p.dX) {
-                    vec_load<T, VEC>(w + c, v);
+                    VecIo<T, VEC>::values(VecIo<T, VEC>::fetch(w + c), v);
                 } else {
 #pragma unroll
                     for (int j = 0; j < VEC; ++j) v[j] = 0.f;
@@ -197,6 +217,7 @@ k_lin_vec_bwd(const LinVec<T> p, const LinEpi<T> e) {
             }
         }
     }
+    before_next();
     if (on && p.dX) {
 #pragma unroll
         for (int r = 0; r < R; ++r) acc[r] = warp_sum(acc[r]);
@@ -225,22 +246,11 @@ static cudaError_t vec_fwd(const LinVec<T> &p, const LinEpi<T> &e, cudaStream_t 
     int cluster = 1;
     while (cluster < 8 && tiles * cluster < 4 * sm_count() && p.in >= 256 * cluster) cluster *= 2;
     const int part = (p.in + cluster - 1) / cluster;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)tiles * cluster);
-    cfg.blockDim = dim3(256);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = cluster;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, k_lin_vec_fwd<T, VEC, R>, p, e, part, cluster);
+    return launch_pdl(k_lin_vec_fwd<T, VEC, R>, dim3((unsigned)tiles * cluster), dim3(256), 0, st, cluster, p, e, part, cluster);
 }
 template <typename T, int VEC, int R>
 static cudaError_t vec_bwd(const LinVec<T> &p, const LinEpi<T> &e, cudaStream_t st) {
-    k_lin_vec_bwd<T, VEC, R><<<(p.in + 7) / 8, 256, 0, st>>>(p, e);
-    return cudaGetLastError();
+    return launch_pdl(k_lin_vec_bwd<T, VEC, R>, dim3((p.in + 7) / 8), dim3(256), 0, st, 1, p, e);
 }
 
 template <typename T, typename F>

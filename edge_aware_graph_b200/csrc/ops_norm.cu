@@ -212,6 +212,7 @@ __device__ __forceinline__ Team my_team(unsigned team) {
     return {threadIdx.x % team, blockIdx.x * per + threadIdx.x / team, gridDim.x * per};
 }
 
+constexpr int RN_ROUNDS = 16;     // runs a crew of the backward takes of a long input
 constexpr int RN_DEPTH = 4;        // steps of the backward in shared memory, the one that is worked on among them
 
 // What a thread of the forward keeps beside the row it works on.  AHEAD: the next row, as it
@@ -226,6 +227,7 @@ struct RnKeep {
 template <typename T, int VEC, int E, bool WIDE, int MAXT>
 __global__ void __launch_bounds__(MAXT, E > 8 ? 1 : WIDE ? 1024 / MAXT : 3)
 k_rn_fwd(const RnArgs a) {
+    after_previous();
     using IO = RowIo<T, VEC, E>;
     using Raw = typename IO::Raw;
     constexpr int H = E / 2;
@@ -339,6 +341,7 @@ k_rn_fwd(const RnArgs a) {
             else IO::store_zeros(h + at, tm.k, team, w);
         }
     }
+    before_next();
 }
 
 // 16 bytes of global memory into shared memory, zeros where `there` is not set (the address is not read then).
@@ -361,6 +364,7 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there
 template <typename T, int VEC, int E, bool WIDE, int MAXT>
 __global__ void __launch_bounds__(MAXT, 512 / MAXT)
 k_rn_bwd(const RnArgs a) {
+    after_previous();
     using IO = RowIo<T, VEC, E>;
     using Raw = typename IO::Raw;
     constexpr int H = E / 2;
@@ -644,6 +648,7 @@ k_rn_bwd(const RnArgs a) {
         }
         forward(cons);
     }
+    before_next();
     if constexpr (AHEAD) {
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();                             // the sums take the rows' place
@@ -697,6 +702,7 @@ struct FinishArgs {
     int n_out, which[4], dtype;
 };
 __global__ void __launch_bounds__(1024) k_rn_finish(const FinishArgs f) {
+    after_previous();
     __shared__ float sum[32][33];
     const unsigned lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     for (unsigned job = blockIdx.y; job < f.n_out + f.groups; job += gridDim.y) {
@@ -751,12 +757,12 @@ static RnPlan rn_plan(const eaga_residual_norm_dims &d) {
     // the registers: 512 threads an SM backward, 768 or 1024 forward
     p.ctas_fwd = (int)std::max(1LL, std::min((rows + per - 1) / per, p.wide ? sms * (p.e > 8 ? 1 : 1024 / p.threads) : sms * 3));
     // Backward.  A run costs a partial row of the gate's gradient, a CTA one of each parameter's: runs of four rows a team
-    // or more (up to 64 rows, whose masks a warp holds), long inputs eight or more a crew.
+    // or more (up to 64 rows, whose masks a warp holds), long inputs RN_ROUNDS or more a crew.
     p.crew = p.wide ? p.team : d.rows_per_group >= 2 * 32 / p.team ? 32 : p.team;
     const long long abreast = p.crew / p.team, crews = p.threads / p.crew, room = sms * (512 / p.threads);
     long long want = std::max(4 * abreast, (rows + room * crews - 1) / (room * crews));
     const long long most = p.wide ? 64 : std::max(abreast, std::min(64LL, 16 * abreast) / abreast * abreast);
-    if (want > 4 * abreast) want = std::max(std::min(most, 4 * abreast), std::min(most, (rows + 8 * room * crews - 1) / (8 * room * crews)));
+    if (want > 4 * abreast) want = std::max(std::min(most, 4 * abreast), std::min(most, (rows + RN_ROUNDS * room * crews - 1) / (RN_ROUNDS * room * crews)));
     want = std::min(want, most);
     const long long parts = std::max(1LL, (d.rows_per_group + want - 1) / want);
     p.run = (unsigned)(((d.rows_per_group + parts - 1) / parts + abreast - 1) / abreast * abreast);
@@ -854,9 +860,8 @@ eaga_status eaga_residual_norm_forward(const eaga_residual_norm_dims *d, const v
     a.r = r; a.h = h;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = rn_dispatch(*d, p, [&](auto t, auto vec, auto el, auto wide, auto maxt) {
-        k_rn_fwd<decltype(t), decltype(vec)::value, decltype(el)::value, decltype(wide)::value, decltype(maxt)::value>
-            <<<p.ctas_fwd, p.threads, 0, st>>>(a);
-        return cudaGetLastError();
+        return launch_pdl(k_rn_fwd<decltype(t), decltype(vec)::value, decltype(el)::value, decltype(wide)::value, decltype(maxt)::value>,
+                          dim3(p.ctas_fwd), dim3(p.threads), 0, st, 1, a);
     });
     return e == cudaSuccess ? EAGA_OK : EAGA_ERR_CUDA;
 }
@@ -911,8 +916,7 @@ eaga_status eaga_residual_norm_backward(const eaga_residual_norm_dims *d, const 
             const int most = E > 8 ? 4 * 8192 * 4 : RN_DEPTH * 5 * 16 * decltype(maxt)::value;
             if (cudaError_t err = ensure_smem_attr(kernel, most, attr_set); err != cudaSuccess) return err;
         }
-        kernel<<<p.ctas_bwd, p.threads, smem, st>>>(a);
-        return cudaGetLastError();
+        return launch_pdl(kernel, dim3(p.ctas_bwd), dim3(p.threads), smem, st, 1, a);
     });
     if (e != cudaSuccess) return EAGA_ERR_CUDA;
     FinishArgs f = {};
@@ -927,8 +931,7 @@ eaga_status eaga_residual_norm_backward(const eaga_residual_norm_dims *d, const 
     f.parts = a.parts; f.gparts = a.gparts; f.dgate = dgate;
     f.w = a.w; f.ctas = p.ctas_bwd; f.runs_per_group = p.runs_per_group; f.dtype = d->dtype;
     const dim3 grid((a.w + 31) / 32, std::min(f.n_out + f.groups, 65535u));
-    k_rn_finish<<<grid, 1024, 0, st>>>(f);
-    return cudaGetLastError() == cudaSuccess ? EAGA_OK : EAGA_ERR_CUDA;
+    return launch_pdl(k_rn_finish, grid, dim3(1024), 0, st, 1, f) == cudaSuccess ? EAGA_OK : EAGA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -20,6 +20,38 @@ __device__ __forceinline__ void after_previous() {
 }
 __device__ __forceinline__ void before_next() { sm100::griddep_launch_dependents(); }
 
+// ------------------------------------------------------------------ two fp32 values at once
+// The elementwise kernels are bound by the instructions they issue as much as by
+// memory; sm_100a adds, multiplies and fuses two fp32 values (each rounded as
+// alone) in one instruction.
+struct f2 {
+    unsigned long long b;
+};
+__device__ __forceinline__ f2 pair(float x, float y) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.b) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ f2 both(float x) { return pair(x, x); }
+__device__ __forceinline__ float lo(f2 a) { return __uint_as_float((unsigned)a.b); }
+__device__ __forceinline__ float hi(f2 a) { return __uint_as_float((unsigned)(a.b >> 32)); }
+__device__ __forceinline__ f2 operator+(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.b) : "l"(a.b), "l"(b.b));
+    return r;
+}
+__device__ __forceinline__ f2 operator*(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.b) : "l"(a.b), "l"(b.b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.b) : "l"(a.b), "l"(b.b), "l"(c.b));
+    return r;
+}
+__device__ __forceinline__ float across(f2 a) { return lo(a) + hi(a); }
+
 inline bool bad_align16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 
 }  // namespace ops

@@ -20,7 +20,7 @@
 // it where it is.  A positive r is never rounded to 0, where m / (0 + eps)
 // would be a jump.  m' and v' enter the weight before they are rounded.
 //
-// Bound: HBM.  A bf16 weight with its fp32 master, an fp32 gradient and fp32
+// Bound: HBM with 32-bit states, the instructions it issues with 8-bit ones.  A bf16 weight with its fp32 master, an fp32 gradient and fp32
 // states moves 30 bytes an element, with 8-bit states 18; the arithmetic (two
 // divisions, a root, for 8 bits two hashes) hides behind it.  A warp takes
 // 256 consecutive elements, 8 a lane: 16-byte accesses throughout, and the
@@ -51,7 +51,7 @@ struct AdEntry {
 };
 struct AdScalars {
     double lr, beta1, beta2;
-    float b1, omb1, b2, omb2, eps, gscale;
+    float b1, omb1, b2, omb2, eps, gscale, one;
     const float *lr_dev;
     long long *state;    // [0] the step, [1] the CTAs done with it
     unsigned seed, tiles;
@@ -146,22 +146,67 @@ __device__ __forceinline__ unsigned code_at(uint2 c, int u) { return ((u < 4 ? c
 constexpr float CODE_UP = 0x1p112f, CODE_DOWN = 0x1p-112f;   // between a code's bits and its value over the scale
 constexpr float M_TOP = 1.875f, R_TOP = 1.9375f;             // the largest codes' values
 
-__device__ __forceinline__ float decode_m(unsigned c, float scale) {
-    const float a = __fmul_rn(__fmul_rn(__uint_as_float((c & 127u) << 20), CODE_UP), scale);
-    return c & 128u ? -a : a;
+// Codes' values, 8 at a time: the code's bits as a float, up, times the scale.
+__device__ __forceinline__ void decode(uint2 c, float scale, int shift, unsigned mask, f2 (&v)[4]) {
+    const f2 up = both(CODE_UP), sc = both(scale);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        v[j] = pair(__uint_as_float((code_at(c, 2 * j) & mask) << shift), __uint_as_float((code_at(c, 2 * j + 1) & mask) << shift)) * up * sc;
 }
-__device__ __forceinline__ float decode_r(unsigned c, float scale) {
-    return __fmul_rn(__fmul_rn(__uint_as_float(c << 19), CODE_UP), scale);
+__device__ __forceinline__ void decode_m(uint2 c, float scale, f2 (&v)[4]) {
+    decode(c, scale, 20, 127u, v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)                      // the sign, bit 7 of the code
+        v[j].b ^= ((unsigned long long)(code_at(c, 2 * j + 1) & 128u) << 56) | ((code_at(c, 2 * j) & 128u) << 24);
 }
-// The warp's largest magnitude; a NaN is larger than everything and stays.
-__device__ __forceinline__ float warp_abs_max(const float (&v)[8]) {
+__device__ __forceinline__ void decode_v(uint2 c, float scale, f2 (&v)[4]) {
+    decode(c, scale, 19, 255u, v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = v[j] * v[j];
+}
+// The warp's largest of values without a sign; a NaN is larger than everything and stays.
+__device__ __forceinline__ float warp_max(const f2 (&v)[4]) {
     unsigned a = 0;
 #pragma unroll
-    for (int u = 0; u < 8; ++u) a = max(a, __float_as_uint(v[u]) & 0x7fffffffu);
+    for (int j = 0; j < 4; ++j) a = max(a, max(__float_as_uint(lo(v[j])) & 0x7fffffffu, __float_as_uint(hi(v[j])) & 0x7fffffffu));
     return __uint_as_float(__reduce_max_sync(0xffffffffu, a));
 }
-__device__ __forceinline__ unsigned scaled_bits(float a, float scale, bool zero) {
-    return zero ? 0u : __float_as_uint(__fmul_rn(__fdiv_rn(a, scale), CODE_DOWN));
+// The quotients a / scale, rounded to nearest, times 2^-112: their bits.  A block has one divisor, so the division is a
+// multiplication by its rounded reciprocal y and two corrections with the exact remainder, q + (a - scale q) y: the first makes q
+// one of the two floats around the quotient, the second (Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990) the nearest.  The remainder is exact for a scale within 2^+-60 and an `a` above 2^-102, and a smaller `a` has
+// code 0 for such a scale; other scales, NaN among them, are divided by in full.
+__device__ __forceinline__ void scaled_bits(const f2 (&a)[4], float scale, float y, bool zero, unsigned (&bits)[8]) {
+    const f2 down = both(CODE_DOWN);
+    if (scale > 0x1p-60f && scale < 0x1p60f) {
+        const f2 yy = both(y), ms = both(-scale);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f2 q = a[j] * yy;
+            q = fma2(fma2(ms, q, a[j]), yy, q);
+            q = fma2(fma2(ms, q, a[j]), yy, q) * down;
+            bits[2 * j] = __float_as_uint(lo(q));
+            bits[2 * j + 1] = __float_as_uint(hi(q));
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            bits[2 * j] = zero ? 0u : __float_as_uint(__fmul_rn(__fdiv_rn(lo(a[j]), scale), CODE_DOWN));
+            bits[2 * j + 1] = zero ? 0u : __float_as_uint(__fmul_rn(__fdiv_rn(hi(a[j]), scale), CODE_DOWN));
+        }
+    }
+}
+__device__ __forceinline__ f2 abs2(f2 a) { return f2{a.b & 0x7fffffff7fffffffull}; }
+__device__ __forceinline__ void pairs(const float (&v)[8], f2 (&o)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = pair(v[2 * j], v[2 * j + 1]);
+}
+__device__ __forceinline__ void singles(const f2 (&v)[4], float (&o)[8]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        o[2 * j] = lo(v[j]);
+        o[2 * j + 1] = hi(v[j]);
+    }
 }
 
 template <typename PT, typename GT, int BITS, bool MASTER, int CAP>
@@ -184,67 +229,88 @@ k_adamw(const __grid_constant__ AdTable<CAP> tab) {
     const float size = sh_size, inv = sh_inv;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (unsigned tile = blockIdx.x; tile < s.tiles; tile += gridDim.x) {
-        int lo = 0, hi = s.count;                    // the last entry whose first tile is at most `tile`
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (tab.e[mid].first <= tile) lo = mid;
-            else hi = mid;
+        int at = 0, past = s.count;                    // the last entry whose first tile is at most `tile`
+        while (past - at > 1) {
+            const int mid = (at + past) >> 1;
+            if (tab.e[mid].first <= tile) at = mid;
+            else past = mid;
         }
-        const AdEntry &e = tab.e[lo];
+        const AdEntry &e = tab.e[at];
         const long long w0 = (long long)(tile - e.first) * AD_TILE + warp * AD_WARP, i0 = w0 + 8 * lane;
         if (w0 >= e.n) continue;                      // whole warps only
         const int k = (int)max(0LL, min(8LL, e.n - i0));
-        float g[8], p[8], m[8], v[8];
-        load8(static_cast<const GT *>(e.g) + i0, k, g);
-        if constexpr (MASTER) load8(e.master + i0, k, p);
-        else load8(static_cast<const PT *>(e.p) + i0, k, p);
+        float x[8];
+        f2 g[4], p[4], m[4], v[4];
+        load8(static_cast<const GT *>(e.g) + i0, k, x);
+        pairs(x, g);
+        if constexpr (MASTER) load8(e.master + i0, k, x);
+        else load8(static_cast<const PT *>(e.p) + i0, k, x);
+        pairs(x, p);
         const long long blk = w0 / AD_BLOCK;
         if constexpr (BITS == 32) {
-            load8(static_cast<const float *>(e.m) + i0, k, m);
-            load8(static_cast<const float *>(e.v) + i0, k, v);
+            load8(static_cast<const float *>(e.m) + i0, k, x);
+            pairs(x, m);
+            load8(static_cast<const float *>(e.v) + i0, k, x);
+            pairs(x, v);
         } else {
             const uint2 cm = load_codes(static_cast<const uint8_t *>(e.m) + i0, k);
             const uint2 cv = load_codes(static_cast<const uint8_t *>(e.v) + i0, k);
-            const float sm = e.ms[blk], sv = e.vs[blk];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                m[u] = decode_m(code_at(cm, u), sm);
-                const float r = decode_r(code_at(cv, u), sv);
-                v[u] = __fmul_rn(r, r);
-            }
+            decode_m(cm, e.ms[blk], m);
+            decode_v(cv, e.vs[blk], v);
         }
-        const float keep = (float)__dsub_rn(1.0, __dmul_rn(sh_lr, (double)e.wd));
-        float r[8];
+        const f2 keep = both((float)__dsub_rn(1.0, __dmul_rn(sh_lr, (double)e.wd)));
+        const f2 b1 = both(s.b1), omb1 = both(s.omb1), b2 = both(s.b2), omb2 = both(s.omb2), gs = both(s.gscale);
+        // a sum behind a product: by a one that the compiler does not know, or it makes a fused one of the two
+        const f2 one = both(s.one);
+        const f2 iv = both(inv), ep = both(s.eps), msize = both(-size);
+        f2 r[4];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const float gu = __fmul_rn(g[u], s.gscale);
-            m[u] = __fadd_rn(__fmul_rn(m[u], s.b1), __fmul_rn(gu, s.omb1));
-            v[u] = __fadd_rn(__fmul_rn(v[u], s.b2), __fmul_rn(__fmul_rn(gu, gu), s.omb2));
-            r[u] = __fsqrt_rn(v[u]);
-            const float d = __fadd_rn(__fmul_rn(r[u], inv), s.eps);
-            p[u] = __fsub_rn(__fmul_rn(p[u], keep), __fmul_rn(__fdiv_rn(m[u], d), size));
+        for (int j = 0; j < 4; ++j) {
+            const f2 gu = g[j] * gs;
+            m[j] = fma2(m[j] * b1, one, gu * omb1);
+            v[j] = fma2(v[j] * b2, one, (gu * gu) * omb2);
+            r[j] = pair(__fsqrt_rn(lo(v[j])), __fsqrt_rn(hi(v[j])));
+            const f2 d = fma2(r[j] * iv, one, ep);
+            p[j] = fma2(p[j] * keep, one, pair(__fdiv_rn(lo(m[j]), lo(d)), __fdiv_rn(hi(m[j]), hi(d))) * msize);
         }
-        if constexpr (MASTER) store8(e.master + i0, k, p);
-        store8(static_cast<PT *>(e.p) + i0, k, p);
+        singles(p, x);
+        if constexpr (MASTER) store8(e.master + i0, k, x);
+        store8(static_cast<PT *>(e.p) + i0, k, x);
         if constexpr (BITS == 32) {
-            store8(static_cast<float *>(e.m) + i0, k, m);
-            store8(static_cast<float *>(e.v) + i0, k, v);
+            singles(m, x);
+            store8(static_cast<float *>(e.m) + i0, k, x);
+            singles(v, x);
+            store8(static_cast<float *>(e.v) + i0, k, x);
         } else {
+            if (k < 8) {                              // past the tensor's end: nothing
+                float y[8];
+                singles(m, x);
+                singles(r, y);
 #pragma unroll
-            for (int u = 0; u < 8; ++u)               // past the tensor's end: nothing
-                if (u >= k) m[u] = r[u] = 0.f;
-            const float am = warp_abs_max(m), ar = warp_abs_max(r);
-            const float sm = __fdiv_rn(am, M_TOP), sr = __fdiv_rn(ar, R_TOP);
+                for (int u = 0; u < 8; ++u)
+                    if (u >= k) x[u] = y[u] = 0.f;
+                pairs(x, m);
+                pairs(y, r);
+            }
+            f2 am[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) am[j] = abs2(m[j]);
+            const float tm = warp_max(am), tr = warp_max(r);
+            const float sm = __fdiv_rn(tm, M_TOP), sr = __fdiv_rn(tr, R_TOP);
+            unsigned bm[8], br[8];
+            scaled_bits(am, sm, __frcp_rn(sm), tm == 0.f, bm);
+            scaled_bits(r, sr, __frcp_rn(sr), tr == 0.f, br);
+            singles(m, x);
             uint2 cm = make_uint2(0, 0), cr = make_uint2(0, 0);
-            const unsigned long long c0 = e.counter + (unsigned long long)i0;
+            const unsigned c0 = (unsigned)(e.counter + (unsigned long long)i0) + sh_key;
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-                const unsigned h = mix32((unsigned)(c0 + u) + sh_key);
+                const unsigned h = mix32(c0 + u);
                 const unsigned h2 = h * 0x3C6EF35Fu;
-                unsigned a = min(127u, (scaled_bits(fabsf(m[u]), sm, am == 0.f) + (h >> 12)) >> 20);
-                if (m[u] < 0.f) a |= 128u;
-                unsigned b = min(255u, (scaled_bits(r[u], sr, ar == 0.f) + (h2 >> 13)) >> 19);
-                if (r[u] > 0.f) b = max(b, 1u);
+                unsigned a = min(127u, (bm[u] + (h >> 12)) >> 20);
+                if (x[u] < 0.f) a |= 128u;
+                unsigned b = min(255u, (br[u] + (h2 >> 13)) >> 19);
+                if ((u & 1 ? hi(r[u / 2]) : lo(r[u / 2])) > 0.f) b = max(b, 1u);
                 (u < 4 ? cm.x : cm.y) |= a << (8 * (u & 3));
                 (u < 4 ? cr.x : cr.y) |= b << (8 * (u & 3));
             }
@@ -273,28 +339,30 @@ k_adamw_unpack(const __grid_constant__ AdTable<CAP> tab) {
     const AdScalars &s = tab.s;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (unsigned tile = blockIdx.x; tile < s.tiles; tile += gridDim.x) {
-        int lo = 0, hi = s.count;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (tab.e[mid].first <= tile) lo = mid;
-            else hi = mid;
+        int at = 0, past = s.count;
+        while (past - at > 1) {
+            const int mid = (at + past) >> 1;
+            if (tab.e[mid].first <= tile) at = mid;
+            else past = mid;
         }
-        const AdEntry &e = tab.e[lo];
+        const AdEntry &e = tab.e[at];
         const long long w0 = (long long)(tile - e.first) * AD_TILE + warp * AD_WARP, i0 = w0 + 8 * lane;
         if (w0 >= e.n) continue;
         const int k = (int)max(0LL, min(8LL, e.n - i0));
         const uint2 cm = load_codes(static_cast<const uint8_t *>(e.m) + i0, k);
         const uint2 cv = load_codes(static_cast<const uint8_t *>(e.v) + i0, k);
-        const float sm = e.ms[w0 / AD_BLOCK], sv = e.vs[w0 / AD_BLOCK];
-        float m[8], v[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            m[u] = decode_m(code_at(cm, u), sm);
-            const float r = decode_r(code_at(cv, u), sv);
-            v[u] = __fmul_rn(r, r);
+        f2 v[4];
+        float x[8];
+        if (e.p) {
+            decode_m(cm, e.ms[w0 / AD_BLOCK], v);
+            singles(v, x);
+            store8(static_cast<float *>(e.p) + i0, k, x);
         }
-        if (e.p) store8(static_cast<float *>(e.p) + i0, k, m);
-        if (e.master) store8(e.master + i0, k, v);
+        if (e.master) {
+            decode_v(cv, e.vs[w0 / AD_BLOCK], v);
+            singles(v, x);
+            store8(e.master + i0, k, x);
+        }
     }
 }
 
@@ -496,6 +564,7 @@ eaga_status eaga_adamw_step(const eaga_adamw_config *c, const eaga_adamw_tensor 
     a.lr = c->lr; a.beta1 = c->beta1; a.beta2 = c->beta2;
     a.b1 = (float)c->beta1; a.omb1 = (float)(1.0 - c->beta1);
     a.b2 = (float)c->beta2; a.omb2 = (float)(1.0 - c->beta2);
+    a.one = 1.f;
     a.eps = (float)c->eps; a.gscale = (float)c->grad_scale;
     a.lr_dev = lr;
     a.state = static_cast<long long *>(state);

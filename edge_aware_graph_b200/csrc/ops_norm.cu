@@ -45,37 +45,6 @@ struct RnArgs {
     int pre, post, team, crew; // threads that hold a row; threads that share a run (backward)
 };
 
-// ------------------------------------------------------------------ two fp32 values at once
-// The kernels are bound by the instructions they issue as much as by memory;
-// sm_100a adds, multiplies and fuses two fp32 values (rounded like one) in one.
-struct f2 {
-    unsigned long long b;
-};
-__device__ __forceinline__ f2 pair(float x, float y) {
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.b) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ f2 both(float x) { return pair(x, x); }
-__device__ __forceinline__ float lo(f2 a) { return __uint_as_float((unsigned)a.b); }
-__device__ __forceinline__ float hi(f2 a) { return __uint_as_float((unsigned)(a.b >> 32)); }
-__device__ __forceinline__ f2 operator+(f2 a, f2 b) {
-    f2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.b) : "l"(a.b), "l"(b.b));
-    return r;
-}
-__device__ __forceinline__ f2 operator*(f2 a, f2 b) {
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.b) : "l"(a.b), "l"(b.b));
-    return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.b) : "l"(a.b), "l"(b.b), "l"(c.b));
-    return r;
-}
-__device__ __forceinline__ float across(f2 a) { return lo(a) + hi(a); }
-
 // ------------------------------------------------------------------ a row in registers
 // E elements a thread.  VEC > 1: 16-byte vectors, thread k of a team holds
 // vectors k, k + team, ..; VEC == 1: single elements, for rows whose length or

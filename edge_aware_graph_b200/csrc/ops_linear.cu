@@ -3,17 +3,14 @@
 //   Z = X W + b        Y = act(Z) + R
 //   dZ = act'(Z) dY    dX = act_in'(Zin) (dZ W^T) + dR    dW = X^T dZ    db = sum of dZ's rows
 //
-// Which kernels run is a rule on rows, type and alignment:
-//   up to 8 rows        ops_linear_vec.cu, bound by the read of W
-//   bf16                ops_linear_tc.cu (tcgen05)
-//   fp32                ops_linear_f32.cu (CUDA cores)
-//
-// The tensor-core kernels read their operands by TMA, whose rows begin on 16
-// bytes: an operand with rows of another length is copied once into padded
-// rows in the workspace.  dZ where act is not none is an fp32 value: it goes
-// into the workspace as three bf16 parts that carry its 24 bits between them.
-// dW, an fp32 result, takes all three; dX, rounded to bf16, the upper two (16
-// bits: the rest is 2^-9 of the result's own rounding).
+// Up to 8 rows run in ops_linear_vec.cu, bound by the read of W; more on the
+// tensor cores (ops_linear_tc.cu).  Those read bf16 operands by TMA, whose rows
+// begin on 16 bytes.  What is not so is prepared once in the workspace, by one
+// kernel for all operands: rows of another length are copied into padded ones;
+// fp32 values (operands in fp32, and dZ where act is not none) become three bf16
+// parts that carry their 24 bits between them.  An fp32 result takes the products
+// of all parts that count (six of nine), dX in bf16 the upper two parts of dZ (16
+// bits: the rest is 2^-8 of the result's own rounding).
 #include <algorithm>
 #include "ops_linear.h"
 
@@ -21,11 +18,10 @@ namespace eaga {
 namespace ops {
 
 // One operand to prepare: src [rows][n], times act'(z) where z is given, as `parts` bf16 parts [rows][ld]
-// (zero past n), or (f32) as fp32 [rows][n].
+// (zero past n).
 struct PrepJob {
     const void *src, *z;
     void *dst[3];
-    float *f32;
     long long rows;
     int n, ld, act, parts;
 };
@@ -33,37 +29,68 @@ struct PrepArgs {
     PrepJob job[3];
 };
 
-// A value's bf16 part and what it leaves.  Of an infinity or a NaN nothing is left: the first part says it all.
+// A value's bf16 part and what it leaves.  Of an infinity or a NaN nothing is left: the first part says it all.  A finite
+// value above bf16's largest gives that.
 __device__ __forceinline__ float take_part(float &v) {
-    const float hi = __bfloat162float(__float2bfloat16_rn(v));
+    float hi = __bfloat162float(__float2bfloat16_rn(v));
+    if (isinf(hi)) hi = __uint_as_float(__float_as_uint(v) & 0xffff0000u);
     v = isfinite(hi) ? v - hi : 0.f;
     return hi;
+}
+
+// The 8 values from `at` on of a flat array of `total`, whatever their alignment: the two aligned 16 bytes (bf16; fp32 three)
+// that hold them, shifted into place.  Near the array's end single loads.
+template <typename T>
+__device__ __forceinline__ void flat_ld8(const T *p, long long at, long long total, int have, float (&v)[8]) {
+    constexpr int PER = 16 / sizeof(T), N = 8 / PER + 1;
+    const int s = (int)(at % PER);
+    const long long first = at / PER;
+    const int need = s ? N : N - 1;
+    if ((first + need) * PER > total) {
+        lin_ld8(p + at, have, false, v);
+        return;
+    }
+    unsigned w[4 * N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const uint4 a = n < need ? reinterpret_cast<const uint4 *>(p)[first + n] : make_uint4(0, 0, 0, 0);
+        w[4 * n] = a.x; w[4 * n + 1] = a.y; w[4 * n + 2] = a.z; w[4 * n + 3] = a.w;
+    }
+    const int words = s * (int)sizeof(T) / 4;        // 0 .. 3
+#pragma unroll
+    for (int k = 0; k < 4 * N; ++k)
+        if (words & 2) w[k] = k + 2 < 4 * N ? w[k + 2] : 0u;
+#pragma unroll
+    for (int k = 0; k < 4 * N; ++k)
+        if (words & 1) w[k] = k + 1 < 4 * N ? w[k + 1] : 0u;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = k < have ? __uint_as_float(w[k]) : 0.f;
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const unsigned x = s & 1 ? __funnelshift_r(w[k], w[k + 1], 16) : w[k];
+            v[2 * k] = 2 * k < have ? __uint_as_float(x << 16) : 0.f;
+            v[2 * k + 1] = 2 * k + 1 < have ? __uint_as_float(x & 0xffff0000u) : 0.f;
+        }
+    }
 }
 
 template <typename T>
 __global__ void __launch_bounds__(256) k_lin_prep(const __grid_constant__ PrepArgs a) {
     after_previous();
     const PrepJob &j = a.job[blockIdx.y];
-    const int per = j.ld / 8;
-    const bool vec = (long long)j.n * sizeof(T) % 16 == 0;
+    const unsigned per = j.ld / 8;
     const T *src = static_cast<const T *>(j.src), *zs = static_cast<const T *>(j.z);
-    const long long total = j.rows * per, step = (long long)gridDim.x * 256;
+    const long long total = j.rows * per, step = (long long)gridDim.x * 256, all = j.rows * j.n;
     for (long long i = blockIdx.x * 256LL + threadIdx.x; i < total; i += step) {
-        const long long row = i / per;
-        const int c = (int)(i % per) * 8, have = min(8, j.n - c);
-        const size_t at = (size_t)row * j.n + c;
+        const long long row = total <= 0xffffffffLL ? (unsigned)i / per : i / per;
+        const int c = (int)(i - row * per) * 8, have = min(8, j.n - c);
         float v[8], z[8];
-        lin_ld8(src + at, have, vec, v);
+        flat_ld8(src, row * j.n + c, all, have, v);
         if (zs) {
-            lin_ld8(zs + at, have, vec, z);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (k >= have) z[k] = 0.f;
+            flat_ld8(zs, row * j.n + c, all, have, z);
             act_slope_mul(v, z, j.act);
-        }
-        if (j.f32) {
-            lin_st8(j.f32 + at, have, vec, v);
-            continue;
         }
         for (int k = 0; k < j.parts; ++k) {
             float o[8];
@@ -72,6 +99,39 @@ __global__ void __launch_bounds__(256) k_lin_prep(const __grid_constant__ PrepAr
             lin_st8(static_cast<__nv_bfloat16 *>(j.dst[k]) + (size_t)row * j.ld + c, 8, true, o);
         }
     }
+    before_next();
+}
+
+// The epilogue of a split forward or dX product, from the splits' sums in their order; VEC columns a thread.
+template <typename T, int KIND, int VEC>
+__global__ void __launch_bounds__(256) k_lin_join(const float *acc, int splits, long long M, int N, const LinEpi<T> e) {
+    after_previous();
+    const long long total = M * N, i = (blockIdx.x * 256LL + threadIdx.x) * VEC;
+    if (i >= total) return;
+    float y[8] = {}, o[8] = {};
+    for (int s = 0; s < splits; ++s) {
+        lin_ld8(acc + s * total + i, VEC, VEC > 1, o);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) y[j] += o[j];
+    }
+    if constexpr (KIND == LIN_FWD) {
+        if (e.bias) {
+            lin_ld8(e.bias + i % N, VEC, VEC > 1, o);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) y[j] += o[j];
+        }
+        if (e.out2) lin_st8(e.out2 + i, VEC, VEC > 1, y);
+        act_apply(y, e.act);
+    } else if (e.zin) {
+        lin_ld8(e.zin + i, VEC, VEC > 1, o);
+        act_slope_mul(y, o, e.act);
+    }
+    if (e.add) {
+        lin_ld8(e.add + i, VEC, VEC > 1, o);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) y[j] += o[j];
+    }
+    lin_st8(e.out + i, VEC, VEC > 1, y);
 }
 
 // dW and db from the splits' sums, in their order: a warp sums every eighth split of 32 VEC values, the CTA
@@ -120,42 +180,58 @@ k_lin_reduce(const float *acc, float *dW, long long n, int splits, const float *
 static int round8(int n) { return (n + 7) / 8 * 8; }
 
 struct LinPlan {
-    bool vec, tc;
-    int ldx, ldw, ldz, zparts;
-    LinSplit split;
-    int bparts;                // of the bias gradient
-    size_t X, W, dZ[3], dZ32, acc, bacc, total;      // workspace offsets; 0: not there
+    bool vec;
+    int xparts, wparts, zparts;        // parts in the workspace; 0: the caller's tensor is read as it is
+    int ldx, ldw, ldz;
+    LinSplit fwd, dx, dw;
+    int bparts;                        // of the bias gradient
+    size_t X[3], W[3], dZ[3], acc, bacc, total;      // workspace offsets
 };
+
+// The products of parts of an fp32 or a bf16 result: A's parts times B's, without those below 2^-24.
+static int products(int aparts, int bparts, uint8_t (&seg)[6]) {
+    int n = 0;
+    for (int sum = 2; sum >= 0; --sum)               // the smallest first
+        for (int a = 0; a < aparts; ++a)
+            if (const int b = sum - a; b >= 0 && b < bparts) seg[n++] = (uint8_t)(a | b << 2);
+    return n;
+}
 
 static LinPlan lin_plan(const eaga_linear_dims &d, bool back) {
     LinPlan p = {};
     p.vec = d.rows <= LIN_VEC_ROWS;
-    p.tc = !p.vec && d.dtype == EAGA_BF16;
-    p.split = {1, 0, {}};
     size_t off = 256;                                // the status word
     auto take = [&](size_t bytes) {
         const size_t at = off;
         off = align256(off + bytes);
         return at;
     };
-    const size_t rows = (size_t)d.rows, in = d.in, out = d.out;
-    const bool dact = back && d.act != EAGA_ACT_NONE;
-    if (p.tc) {
+    if (!p.vec) {
+        const size_t rows = (size_t)d.rows, in = d.in, out = d.out;
+        const bool f32 = d.dtype == EAGA_FP32, dact = back && d.act != EAGA_ACT_NONE;
         p.ldx = round8(d.in);
         p.ldw = p.ldz = round8(d.out);
-        if (p.ldx != d.in) p.X = take(rows * p.ldx * 2);
-        if (p.ldw != d.out) p.W = take(in * p.ldw * 2);
-        p.zparts = dact ? 3 : 1;
-        if (back && (dact || p.ldz != d.out))
-            for (int k = 0; k < p.zparts; ++k) p.dZ[k] = take(rows * p.ldz * 2);
-        if (back) p.split = lin_tc_dw_split(d.rows, d.in, d.out, p.zparts);
-    } else if (!p.vec && back) {
-        if (dact) p.dZ32 = take(rows * out * 4);
-        p.split = lin_f32_dw_split(d.rows, d.in, d.out);
+        p.xparts = f32 ? 3 : p.ldx != d.in ? 1 : 0;
+        p.wparts = f32 ? 3 : p.ldw != d.out ? 1 : 0;
+        p.zparts = !back ? 0 : f32 || dact ? 3 : p.ldz != d.out ? 1 : 0;
+        for (int k = 0; k < p.xparts; ++k) p.X[k] = take(rows * p.ldx * 2);
+        for (int k = 0; k < p.wparts; ++k) p.W[k] = take(in * p.ldw * 2);
+        for (int k = 0; k < p.zparts; ++k) p.dZ[k] = take(rows * p.ldz * 2);
+        uint8_t seg[6];
+        size_t acc = 0;
+        if (!back) {
+            p.fwd = lin_tc_split(d.rows, d.out, d.in, f32 ? 6 : 1);
+            acc = p.fwd.splits > 1 ? p.fwd.splits * rows * out : 0;
+        } else {
+            const int z = std::max(1, p.zparts);
+            p.dx = lin_tc_split(d.rows, d.in, d.out, f32 ? 6 : std::min(z, 2));
+            p.dw = lin_tc_split(d.in, d.out, d.rows, products(f32 ? 3 : 1, z, seg));
+            acc = std::max(p.dx.splits > 1 ? p.dx.splits * rows * in : 0, p.dw.splits > 1 ? p.dw.splits * in * out : 0);
+            p.bparts = lin_db_parts(p.dw, d.in);
+        }
+        if (acc) p.acc = take(acc * 4);
+        if (p.bparts > 1) p.bacc = take(p.bparts * out * 4);
     }
-    if (p.split.splits > 1) p.acc = take(p.split.splits * in * out * 4);
-    if (back && !p.vec) p.bparts = lin_db_parts(p.split, d.in);
-    if (p.bparts > 1) p.bacc = take(p.bparts * out * 4);
     p.total = off;
     return p;
 }
@@ -193,6 +269,14 @@ static cudaError_t lin_reduce(long long n, int splits, const float *acc, float *
 
 static Span span(const void *q, size_t b) { return Span{q, q ? b : 0}; }
 
+template <int KIND, typename T>
+static cudaError_t lin_join(const LinSplit &s, const float *acc, long long M, int N, const LinEpi<T> &e, cudaStream_t st) {
+    const bool v = N % 8 == 0;
+    const long long blocks = (M * N + (v ? 2047 : 255)) / (v ? 2048 : 256);
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    return launch_pdl(v ? k_lin_join<T, KIND, 8> : k_lin_join<T, KIND, 1>, dim3((unsigned)blocks), dim3(256), 0, st, 1, acc, s.splits, M, N, e);
+}
+
 struct LinBack {
     const void *X, *W, *Z, *dY;
     int act_in;
@@ -202,74 +286,77 @@ struct LinBack {
     char *ws;
 };
 
-static cudaError_t backward_tc(const eaga_linear_dims &d, const LinPlan &p, const LinBack &b, cudaStream_t st) {
-    typedef __nv_bfloat16 bf;
-    PrepJob jobs[3] = {};
-    int n = 0;
+// An operand's parts: the caller's tensor, or prepared ones (then with a job).
+static void lin_operand(const __nv_bfloat16 *(&part)[3], const void *src, const void *z, int act, long long rows, int n, int ld, int parts,
+                        const size_t (&at)[3], char *ws, PrepJob *jobs, int &count) {
+    part[0] = static_cast<const __nv_bfloat16 *>(src);
+    if (!parts) return;
+    PrepJob j = {src, z, {}, rows, n, ld, act, parts};
+    for (int k = 0; k < parts; ++k) {
+        j.dst[k] = ws + at[k];
+        part[k] = reinterpret_cast<const __nv_bfloat16 *>(ws + at[k]);
+    }
+    jobs[count++] = j;
+}
+
+static LinTc lin_tc(const eaga_linear_dims &d, const LinPlan &p, char *ws) {
     LinTc q = {};
     q.rows = d.rows; q.in = d.in; q.out = d.out;
     q.ldx = p.ldx; q.ldw = p.ldw; q.ldz = p.ldz;
-    q.status = reinterpret_cast<int *>(b.ws);
+    q.status = reinterpret_cast<int *>(ws);
     q.clear = true;
-    auto at = [&](size_t off) { return reinterpret_cast<bf *>(b.ws + off); };
-    q.X[0] = static_cast<const bf *>(b.X);
-    q.W[0] = static_cast<const bf *>(b.W);
-    q.dZ[0] = static_cast<const bf *>(b.dY);
-    if (p.X && b.dW) {
-        jobs[n++] = {b.X, nullptr, {at(p.X)}, nullptr, d.rows, d.in, p.ldx, 0, 1};
-        q.X[0] = at(p.X);
-    }
-    if (p.W && b.dX) {
-        jobs[n++] = {b.W, nullptr, {at(p.W)}, nullptr, d.in, d.out, p.ldw, 0, 1};
-        q.W[0] = at(p.W);
-    }
-    const int zparts = b.dW ? p.zparts : std::min(p.zparts, 2);
-    if (p.dZ[0]) {
-        PrepJob j = {b.dY, b.Z, {}, nullptr, d.rows, d.out, p.ldz, d.act, zparts};
-        for (int k = 0; k < zparts; ++k) {
-            j.dst[k] = at(p.dZ[k]);
-            q.dZ[k] = at(p.dZ[k]);
-        }
-        jobs[n++] = j;
-    }
-    if (cudaError_t e = lin_prep<bf>(jobs, n, st); e != cudaSuccess) return e;
+    return q;
+}
+
+template <typename T>
+static cudaError_t forward_tc(const eaga_linear_dims &d, const LinPlan &p, const void *X, const void *W, const LinEpi<T> &e, char *ws,
+                              cudaStream_t st) {
+    PrepJob jobs[2];
+    int n = 0;
+    LinTc q = lin_tc(d, p, ws);
+    lin_operand(q.X, X, nullptr, 0, d.rows, d.in, p.ldx, p.xparts, p.X, ws, jobs, n);
+    lin_operand(q.W, W, nullptr, 0, d.in, d.out, p.ldw, p.wparts, p.W, ws, jobs, n);
+    if (cudaError_t err = lin_prep<T>(jobs, n, st); err != cudaSuccess) return err;
+    const bool f32 = d.dtype == EAGA_FP32;
+    q.nseg = products(f32 ? 3 : 1, f32 ? 3 : 1, q.seg);
+    if (p.fwd.splits == 1) return lin_tc_forward<T>(q, p.fwd, e, st);
+    LinEpi<float> sums = {};
+    sums.out = reinterpret_cast<float *>(ws + p.acc);
+    if (cudaError_t err = lin_tc_forward<float>(q, p.fwd, sums, st); err != cudaSuccess) return err;
+    return lin_join<LIN_FWD, T>(p.fwd, sums.out, d.rows, d.out, e, st);
+}
+
+template <typename T>
+static cudaError_t backward_tc(const eaga_linear_dims &d, const LinPlan &p, const LinBack &b, cudaStream_t st) {
+    PrepJob jobs[3];
+    int n = 0;
+    LinTc q = lin_tc(d, p, b.ws);
+    const bool f32 = d.dtype == EAGA_FP32;
+    if (b.dW) lin_operand(q.X, b.X, nullptr, 0, d.rows, d.in, p.ldx, p.xparts, p.X, b.ws, jobs, n);
+    if (b.dX) lin_operand(q.W, b.W, nullptr, 0, d.in, d.out, p.ldw, p.wparts, p.W, b.ws, jobs, n);
+    const int zparts = f32 || b.dW ? p.zparts : std::min(p.zparts, 2);
+    lin_operand(q.dZ, b.dY, b.Z, d.act, d.rows, d.out, p.ldz, zparts, p.dZ, b.ws, jobs, n);
+    if (cudaError_t e = lin_prep<T>(jobs, n, st); e != cudaSuccess) return e;
+    const int z = std::max(1, zparts);
     if (b.dX) {
-        LinTc x = q;
-        x.nseg = std::min(zparts, 2);
-        for (int k = 0; k < x.nseg; ++k) x.seg[k] = (uint8_t)(x.nseg - 1 - k);              // A = dZ, W in one part
-        const LinEpi<bf> e = {nullptr, static_cast<const bf *>(b.dR), static_cast<const bf *>(b.Zin), static_cast<bf *>(b.dX), nullptr, b.act_in};
-        if (cudaError_t err = lin_tc_dx(x, e, st); err != cudaSuccess) return err;
+        q.nseg = f32 ? products(3, 3, q.seg) : products(std::min(z, 2), 1, q.seg);
+        const LinEpi<T> e = {nullptr, static_cast<const T *>(b.dR), static_cast<const T *>(b.Zin), static_cast<T *>(b.dX), nullptr, b.act_in};
+        if (p.dx.splits == 1) {
+            if (cudaError_t err = lin_tc_dx<T>(q, p.dx, e, st); err != cudaSuccess) return err;
+        } else {
+            LinEpi<float> sums = {};
+            sums.out = reinterpret_cast<float *>(b.ws + p.acc);
+            if (cudaError_t err = lin_tc_dx<float>(q, p.dx, sums, st); err != cudaSuccess) return err;
+            if (cudaError_t err = lin_join<LIN_DX, T>(p.dx, sums.out, d.rows, d.in, e, st); err != cudaSuccess) return err;
+        }
         q.clear = false;
     }
     if (b.dW) {
-        q.nseg = zparts;
-        for (int k = 0; k < q.nseg; ++k) q.seg[k] = (uint8_t)((q.nseg - 1 - k) << 2);       // B = dZ, X in one part
-        float *acc = p.split.splits > 1 ? reinterpret_cast<float *>(b.ws + p.acc) : b.dW;
+        q.nseg = products(f32 ? 3 : 1, z, q.seg);
+        float *acc = p.dw.splits > 1 ? reinterpret_cast<float *>(b.ws + p.acc) : b.dW;
         float *bacc = !b.db ? nullptr : p.bparts > 1 ? reinterpret_cast<float *>(b.ws + p.bacc) : b.db;
-        if (cudaError_t err = lin_tc_dw(q, p.split, acc, bacc, st); err != cudaSuccess) return err;
-        return lin_reduce((long long)d.in * d.out, p.split.splits, acc, b.dW, d.out, p.bparts, bacc, b.db, st);
-    }
-    return cudaSuccess;
-}
-
-static cudaError_t backward_f32(const eaga_linear_dims &d, const LinPlan &p, const LinBack &b, cudaStream_t st) {
-    LinF32 q = {d.rows, d.in, d.out, static_cast<const float *>(b.X), static_cast<const float *>(b.W), static_cast<const float *>(b.dY),
-                reinterpret_cast<int *>(b.ws)};
-    if (p.dZ32) {
-        float *dz = reinterpret_cast<float *>(b.ws + p.dZ32);
-        const PrepJob j = {b.dY, b.Z, {}, dz, d.rows, d.out, round8(d.out), d.act, 0};
-        if (cudaError_t e = lin_prep<float>(&j, 1, st); e != cudaSuccess) return e;
-        q.dZ = dz;
-    }
-    if (b.dX) {
-        const LinEpi<float> e = {nullptr, static_cast<const float *>(b.dR), static_cast<const float *>(b.Zin), static_cast<float *>(b.dX), nullptr, b.act_in};
-        if (cudaError_t err = lin_f32_dx(q, e, st); err != cudaSuccess) return err;
-    }
-    if (b.dW) {
-        float *acc = p.split.splits > 1 ? reinterpret_cast<float *>(b.ws + p.acc) : b.dW;
-        float *bacc = !b.db ? nullptr : p.bparts > 1 ? reinterpret_cast<float *>(b.ws + p.bacc) : b.db;
-        if (cudaError_t err = lin_f32_dw(q, p.split, acc, bacc, st); err != cudaSuccess) return err;
-        return lin_reduce((long long)d.in * d.out, p.split.splits, acc, b.dW, d.out, p.bparts, bacc, b.db, st);
+        if (cudaError_t err = lin_tc_dw(q, p.dw, acc, bacc, st); err != cudaSuccess) return err;
+        return lin_reduce((long long)d.in * d.out, p.dw.splits, acc, b.dW, d.out, p.bparts, bacc, b.db, st);
     }
     return cudaSuccess;
 }
@@ -325,34 +412,14 @@ eaga_status eaga_linear_forward(const eaga_linear_dims *d, const void *X, const 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
     if (d->rows == 0) return cudaMemsetAsync(workspace, 0, 4, st) == cudaSuccess ? EAGA_OK : EAGA_ERR_CUDA;
-    if (p.vec) {
-        e = d->dtype == EAGA_BF16 ? forward_vec(*d, X, W, forward_epi<__nv_bfloat16>(*d, b, R, Y, Z), workspace, st)
-                                  : forward_vec(*d, X, W, forward_epi<float>(*d, b, R, Y, Z), workspace, st);
-    } else if (!p.tc) {
-        const LinF32 q = {d->rows, d->in, d->out, static_cast<const float *>(X), static_cast<const float *>(W), nullptr, static_cast<int *>(workspace)};
-        e = lin_f32_forward(q, forward_epi<float>(*d, b, R, Y, Z), st);
+    char *ws = static_cast<char *>(workspace);
+    typedef __nv_bfloat16 bf;
+    if (d->dtype == EAGA_BF16) {
+        const LinEpi<bf> epi = forward_epi<bf>(*d, b, R, Y, Z);
+        e = p.vec ? forward_vec(*d, X, W, epi, workspace, st) : forward_tc(*d, p, X, W, epi, ws, st);
     } else {
-        typedef __nv_bfloat16 bf;
-        char *ws = static_cast<char *>(workspace);
-        PrepJob jobs[2] = {};
-        int n = 0;
-        LinTc q = {};
-        q.rows = d->rows; q.in = d->in; q.out = d->out;
-        q.ldx = p.ldx; q.ldw = p.ldw; q.nseg = 1;
-        q.X[0] = static_cast<const bf *>(X);
-        q.W[0] = static_cast<const bf *>(W);
-        q.status = static_cast<int *>(workspace);
-        q.clear = true;
-        if (p.X) {
-            jobs[n++] = {X, nullptr, {ws + p.X}, nullptr, d->rows, d->in, p.ldx, 0, 1};
-            q.X[0] = reinterpret_cast<const bf *>(ws + p.X);
-        }
-        if (p.W) {
-            jobs[n++] = {W, nullptr, {ws + p.W}, nullptr, d->in, d->out, p.ldw, 0, 1};
-            q.W[0] = reinterpret_cast<const bf *>(ws + p.W);
-        }
-        e = lin_prep<bf>(jobs, n, st);
-        if (e == cudaSuccess) e = lin_tc_forward(q, forward_epi<bf>(*d, b, R, Y, Z), st);
+        const LinEpi<float> epi = forward_epi<float>(*d, b, R, Y, Z);
+        e = p.vec ? forward_vec(*d, X, W, epi, workspace, st) : forward_tc(*d, p, X, W, epi, ws, st);
     }
     return e == cudaSuccess ? EAGA_OK : EAGA_ERR_CUDA;
 }
@@ -388,9 +455,8 @@ eaga_status eaga_linear_backward(const eaga_linear_dims *d, const void *X, const
         return e == cudaSuccess ? EAGA_OK : EAGA_ERR_CUDA;
     }
     const LinBack b = {X, W, Z, dY, act_in, Zin, dR, dX, dW, db, static_cast<char *>(workspace)};
-    if (p.tc) e = backward_tc(*d, p, b, st);
-    else if (!p.vec) e = backward_f32(*d, p, b, st);
-    else e = d->dtype == EAGA_BF16 ? backward_vec<__nv_bfloat16>(*d, b, st) : backward_vec<float>(*d, b, st);
+    if (d->dtype == EAGA_BF16) e = p.vec ? backward_vec<__nv_bfloat16>(*d, b, st) : backward_tc<__nv_bfloat16>(*d, p, b, st);
+    else e = p.vec ? backward_vec<float>(*d, b, st) : backward_tc<float>(*d, p, b, st);
     return e == cudaSuccess ? EAGA_OK : EAGA_ERR_CUDA;
 }
 

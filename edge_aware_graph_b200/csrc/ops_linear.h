@@ -110,16 +110,16 @@ struct LinTile {
     bool pair;
     int bn;
 };
-// Split of a weight gradient's reduction over rows into parts of `chunk` rows.
+// Split of a product's reduction into parts of `chunk`, and its tiles.
 struct LinSplit {
     int splits;
     long long chunk;
-    LinTile tile;              // tensor cores only
+    LinTile tile;
 };
 
 // tcgen05 products of bf16 operands whose rows are ld elements long (a multiple of 8), zero past the true
-// size.  An operand may come in parts that are added: the segments are the products of parts to sum, as
-// pairs of part numbers, A's low (X or dZ in LIN_DX; X in LIN_DW), four bits each.
+// size.  An operand may come in parts that are added; seg: the products of parts to sum, A's part (of X, or of
+// dZ in LIN_DX) in the low two bits, B's in the next two.
 struct LinTc {
     long long rows;
     int in, out;
@@ -130,27 +130,16 @@ struct LinTc {
     int *status;
     bool clear;                // this launch clears the status word
 };
+// Of a product [M, K] x [K, N].
+LinSplit lin_tc_split(long long M, int N, long long K, int nseg);
+// With one split the finished outputs; with more e.out takes the splits' sums [splits][M][N] in fp32, and nothing else of e is there.
 template <typename T>
-cudaError_t lin_tc_forward(const LinTc &p, const LinEpi<T> &e, cudaStream_t st);
+cudaError_t lin_tc_forward(const LinTc &p, const LinSplit &s, const LinEpi<T> &e, cudaStream_t st);
 template <typename T>
-cudaError_t lin_tc_dx(const LinTc &p, const LinEpi<T> &e, cudaStream_t st);
-// dW or, with more than one split, the splits' sums [splits][in][out]; and where db is not null the column sums in
-// lin_db_parts() parts [parts][out].
-LinSplit lin_tc_dw_split(long long rows, int in, int out, int nseg);
+cudaError_t lin_tc_dx(const LinTc &p, const LinSplit &s, const LinEpi<T> &e, cudaStream_t st);
+// dW likewise; and where db is not null the column sums in lin_db_parts() parts [parts][out].
 inline int lin_db_parts(const LinSplit &s, int in) { return s.splits * (s.tile.pair ? (in + 255) / 256 : 1); }
 cudaError_t lin_tc_dw(const LinTc &p, const LinSplit &s, float *dW, float *db, cudaStream_t st);
-
-// CUDA-core products of fp32 operands of any size; partial sums as above.
-struct LinF32 {
-    long long rows;
-    int in, out;
-    const float *X, *W, *dZ;
-    int *status;               // cleared
-};
-cudaError_t lin_f32_forward(const LinF32 &p, const LinEpi<float> &e, cudaStream_t st);
-cudaError_t lin_f32_dx(const LinF32 &p, const LinEpi<float> &e, cudaStream_t st);
-LinSplit lin_f32_dw_split(long long rows, int in, int out);
-cudaError_t lin_f32_dw(const LinF32 &p, const LinSplit &s, float *dW, float *db, cudaStream_t st);
 
 // Up to LIN_VEC_ROWS rows: the weights are read once, bound by memory.
 constexpr int LIN_VEC_ROWS = 8;

@@ -29,16 +29,19 @@
 // every 512 steps of the reduction for a sum in registers, rounded to nearest.
 //
 // A weight gradient reduces over rows, of which there may be a million for a
-// 64 x 128 result: its tiles are split over rows, the splits' sums are added
-// in a fixed order by the caller's reduction.  The bias gradient, the column
+// 64 x 128 result, and a few rows' products over thousands of features: where
+// tiles are few, the reduction is split, and the splits' fp32 sums are added in a
+// fixed order by a kernel that has the epilogue then.  The bias gradient, the column
 // sums of dZ, comes from two more warps: on single tiles in those of the first
 // row, from the dZ tiles in shared memory times a matrix of ones (warp-level MMAs,
 // joined in fp32 after every 64 rows); on pairs, where the barriers are the first
 // CTA's, from dZ itself, which the tiles' loads have brought into L2, a share of
 // the rows in every row of tiles.
 //
-// An operand in fp32 comes as bf16 parts (two carry 16 bits of it, three 24):
-// the products of parts are segments of one longer reduction, the smallest first.
+// An operand in fp32 comes as bf16 parts (two carry 16 bits of it, three 24),
+// and a step of the reduction is one for each product of parts that counts: fp32
+// products take six, all but those below 2^-24, at a sixth of the bf16 rate, which is
+// 2.5 times what the CUDA cores could reach.
 #include <algorithm>
 #include <type_traits>
 #include "ops_linear.h"
@@ -104,17 +107,16 @@ struct LtMaps {
 
 template <typename TO>
 struct LtParams {
-    LinEpi<TO> e;
-    float *acc, *db;           // weight gradient: fp32 sums [split][M][N]; [split][N], on pairs [split][row of tiles][N]
+    LinEpi<TO> e;              // out: [split][M][N]
+    float *db;                 // weight gradient: [split][N], on pairs [split][row of tiles][N]
     const bf16 *dz[3];         // on pairs, for db: dZ's parts, their row length
     int ldz, rows;
     int *status;
     int M, N;                  // output
-    int kts;                   // forward, dX: 64-deep steps a segment; weight gradient: those of all rows
+    int kts, per;              // 64-deep steps of the reduction, of a split
     int nseg;
-    uint32_t seg;              // four bits a segment: A's part, B's part
+    uint32_t seg;              // products of parts, four bits each: A's part, B's part
     int tiles_m, tiles_n, units;
-    int per;                   // weight gradient: a split's steps
     int clear;
 };
 
@@ -177,13 +179,13 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
     auto unit_of = [&](int u) {
         Unit r;
         const int tiles = p.tiles_m * p.tiles_n;
-        r.split = KIND == LIN_DW ? u / tiles : 0;
-        const int t = KIND == LIN_DW ? u - r.split * tiles : u;
+        r.split = u / tiles;
+        const int t = u - r.split * tiles;
         r.tm = t / p.tiles_n;
         r.m0 = r.tm * S::BM + rank * LT_BM;                  // this CTA's rows
         r.n0 = (t - r.tm * p.tiles_n) * BN;
-        r.k0 = KIND == LIN_DW ? r.split * p.per : 0;
-        r.steps = KIND == LIN_DW ? min(p.per, p.kts - r.k0) : p.kts;
+        r.k0 = r.split * p.per;
+        r.steps = min(p.per, p.kts - r.k0);
         return r;
     };
 
@@ -197,11 +199,11 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
                 for (int u = first; ok && u < p.units; u += stride) {
                     const Unit t = unit_of(u);
                     const int nb = t.n0 + rank * S::PB;      // this CTA's columns of B
-                    for (int seg = 0; ok && seg < p.nseg; ++seg) {
-                        const uint32_t parts = p.seg >> (4 * seg);
-                        const CUtensorMap *am = &maps.a[parts & 3], *bm = &maps.b[(parts >> 2) & 3];
-                        int kk = t.k0 * LT_BK;
-                        for (int k = t.steps; k > 0; --k, kk += LT_BK) {
+                    int kk = t.k0 * LT_BK;
+                    for (int k = t.steps; ok && k > 0; --k, kk += LT_BK) {
+                        uint32_t parts = p.seg;
+                        for (int seg = p.nseg; seg > 0; --seg, parts >>= 4) {
+                            const CUtensorMap *am = &maps.a[parts & 3], *bm = &maps.b[(parts >> 2) & 3];
                             if (!lt_wait(empty(s), ph, fail, p.status)) { ok = false; break; }
                             const uint32_t st = sbase + s * S::STAGE;
                             const uint32_t bar = PAIR ? cluster_map(full(s), 0) : full(s);
@@ -308,10 +310,14 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
                     float sum[NT][2];
 #pragma unroll
                     for (int j = 0; j < NT; ++j) sum[j][0] = sum[j][1] = 0.f;
-                    for (int k = 0; k < nk; ++k, ++it) {
+                    for (int k = 0, seg = 0; k < nk; ++k, ++it, seg = seg + 1 < p.nseg ? seg + 1 : 0) {
                         const int s = it % ST;
                         ok = __all_sync(0xffffffffu, lt_wait(full(s), (it / ST) & 1, fail, p.status));
                         if (!ok) break;
+                        if ((p.seg >> (4 * seg)) & 3) {     // each part of dZ once: beside X's first
+                            if (lane == 0) mbar_arrive(empty(s));
+                            continue;
+                        }
                         const uint32_t bt = sbase + s * S::STAGE + S::A_BYTES;
 #pragma unroll
                         for (int j = 0; j < NT; j += 2) {
@@ -356,6 +362,7 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
                     for (int j = 0; j < 8; ++j) sum[j] = 0.f;
                     if (c < p.ldz) {
                         for (int seg = 0; seg < p.nseg; ++seg) {
+                            if ((p.seg >> (4 * seg)) & 3) continue;
                             const bf16 *z = p.dz[(p.seg >> (4 * seg + 2)) & 3] + c;
 #pragma unroll 8
                             for (long long r = r0 + (lane >> 3); r < r1; r += 4) {
@@ -555,7 +562,7 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        tma_store_3d(&maps.out, io, col, row0, KIND == LIN_DW ? t.split : 0);
+                        tma_store_3d(&maps.out, io, col, row0, t.split);
                         if (has_z) tma_store_3d(&maps.out2, side, col, row0, 0);
                         tma_store_commit();
                         if (S::NIO == 1 && (has_add || has_zin)) {
@@ -567,46 +574,42 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
                     __syncwarp();
                     ++k;
                 } else {
-                    // 4 lanes a row, 8 columns each; 8 rows at a time
-                    __syncwarp();                   // lanes without columns are back; the last piece's reads are done
+                    // rows that do not begin on 16 bytes: a lane a column, eight rows at a time
+                    __syncwarp();                   // the last piece's reads are done
 #pragma unroll
                     for (int x = 0; x < 8; ++x)
                         asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(slots + fast::sw128(lane, x)), "f"(v[4 * x]),
                                      "f"(v[4 * x + 1]), "f"(v[4 * x + 2]), "f"(v[4 * x + 3])
                                      : "memory");
                     __syncwarp();
-                    const int cl = lane & 3, cc = col + 8 * cl, have = min(8, p.N - cc);
-                    if (have > 0) {
-                        float bias[8];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) bias[j] = KIND == LIN_FWD && p.e.bias && j < have ? ldf(p.e.bias + cc + j) : 0.f;
+                    const int cc = col + lane;
+                    if (cc < p.N) {
+                        const float bias = KIND == LIN_FWD && p.e.bias ? ldf(p.e.bias + cc) : 0.f;
 #pragma unroll 1
-                        for (int r8 = 0; r8 < 4; ++r8) {
-                            const int rl = 8 * r8 + (lane >> 2), row = row0 + rl;
-                            if (row >= p.M) break;
-                            const float4 x0 = *reinterpret_cast<const float4 *>(slots_p + fast::sw128(rl, 2 * cl));
-                            const float4 x1 = *reinterpret_cast<const float4 *>(slots_p + fast::sw128(rl, 2 * cl + 1));
-                            float y[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w}, o[8];
-                            const size_t at = (size_t)row * p.N + cc;
-                            if constexpr (KIND == LIN_DW) {
-                                lin_st8(p.acc + (size_t)t.split * p.M * p.N + at, have, false, y);
-                            } else {
-                                if constexpr (KIND == LIN_FWD) {
+                        for (int r0 = 0; r0 < 32 && row0 + r0 < p.M; r0 += 8) {
+                            const size_t at = (size_t)(row0 + r0) * p.N + cc;
+                            float y[8], zi[8], ad[8];
 #pragma unroll
-                                    for (int j = 0; j < 8; ++j) y[j] += bias[j];
-                                    if (p.e.out2) lin_st8(p.e.out2 + at, have, false, y);
-                                    act_apply(y, p.e.act);
-                                } else if (p.e.zin) {
-                                    lin_ld8(p.e.zin + at, have, false, o);
-                                    act_slope_mul(y, o, p.e.act);
-                                }
-                                if (p.e.add) {
-                                    lin_ld8(p.e.add + at, have, false, o);
-#pragma unroll
-                                    for (int j = 0; j < 8; ++j) y[j] += o[j];
-                                }
-                                lin_st8(p.e.out + at, have, false, y);
+                            for (int j = 0; j < 8; ++j) {
+                                const bool in = row0 + r0 + j < p.M;
+                                y[j] = *reinterpret_cast<const float *>(slots_p + fast::sw128(r0 + j, lane >> 2) + 4 * (lane & 3));
+                                if (KIND == LIN_DX) zi[j] = p.e.zin && in ? ldf(p.e.zin + at + (size_t)j * p.N) : 0.f;
+                                if (KIND != LIN_DW) ad[j] = p.e.add && in ? ldf(p.e.add + at + (size_t)j * p.N) : 0.f;
                             }
+                            if constexpr (KIND == LIN_FWD) {
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) {
+                                    y[j] += bias;
+                                    if (p.e.out2 && row0 + r0 + j < p.M) stf(p.e.out2 + at + (size_t)j * p.N, y[j]);
+                                }
+                                act_apply(y, p.e.act);
+                            } else if constexpr (KIND == LIN_DX) {
+                                if (p.e.zin) act_slope_mul(y, zi, p.e.act);
+                            }
+                            TO *o = p.e.out + (size_t)t.split * p.M * p.N + at;
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                if (row0 + r0 + j < p.M) stf(o + (size_t)j * p.N, KIND != LIN_DW && p.e.add ? y[j] + ad[j] : y[j]);
                         }
                     }
                     __syncwarp();
@@ -685,107 +688,37 @@ static cudaError_t lt_run(const LinTile &t, const LtMaps &m, const LtParams<TO> 
     return lt_launch<KIND, 64, 1, TO, VEC>(m, p, st);
 }
 
-// Tiles and, for a weight gradient, splits: the least of an estimate of each form's time.  The unit is a 64-deep
-// step of a pair's tile, 0.28 us.  A step of the single tiles takes 0.75 (128 columns) and 0.45 (64) of it for a
-// half and a quarter of a CTA's work: the shared memory's traffic bounds them (measured 1.0e15 op/s, pairs 1.4e15).  A tile
-// costs six steps more for the pipeline's start and the epilogue's end, a split the write and read of its sums.
-static double lt_cost(const LinTile &t, long long M, int N, long long steps, int splits, bool dw) {
+// Tiles and splits: the least of an estimate of each form's time.  The unit is a 64-deep step of a pair's tile,
+// 0.28 us.  A step of the single tiles takes 0.75 (128 columns) and 0.45 (64) of it for a half and a quarter of
+// a CTA's work: the shared memory's traffic bounds them (measured 1.0e15 op/s, pairs 1.4e15).  A tile costs three
+// steps more for the pipeline's start and the epilogue's end; splits cost the write and read of their sums and,
+// of products that need no second kernel otherwise, its launch.
+static double lt_cost(const LinTile &t, long long M, int N, long long steps, int splits) {
     const int bm = t.pair ? 256 : 128, sms = sm_count();
     const double units = (double)((M + bm - 1) / bm) * ((N + t.bn - 1) / t.bn) * splits;
     const double step = t.pair ? 1.0 : t.bn == 128 ? 0.75 : 0.45;
     const double waves = std::ceil(units / (t.pair ? sms / 2 : sms));
     const double per = (double)((steps + splits - 1) / splits);
     double c = waves * (per * step + 3 * step) + 6;
-    if (dw && splits > 1) c += 10 + (double)splits * M * N * 8 / 6.5e6 / 0.28;       // bytes / (bytes a us) / (us a step)
+    if (splits > 1) c += 10 + (double)splits * M * N * 8 / 6.5e6 / 0.28;             // bytes / (bytes a us) / (us a step)
     return c;
 }
-static const LinTile LT_TILES[3] = {{true, 256}, {false, 128}, {false, 64}};
-static bool lt_fits(const LinTile &t, long long M, int N) {
-    if (t.pair) return M > 128 && N > 128;
-    return t.bn == 64 || N > 64;
-}
-static LinTile lt_tile(long long M, int N, long long steps) {
-    LinTile best = LT_TILES[2];
+
+LinSplit lin_tc_split(long long M, int N, long long K, int nseg) {
+    static const LinTile tiles[3] = {{true, 256}, {false, 128}, {false, 64}};
+    const long long steps = std::max(1LL, (K + LT_BK - 1) / LT_BK);
+    LinSplit best = {1, steps * LT_BK, tiles[2]};
     double least = 1e300;
-    for (const LinTile &t : LT_TILES)
-        if (lt_fits(t, M, N))
-            if (const double c = lt_cost(t, M, N, steps, 1, false); c < least) {
-                least = c;
-                best = t;
-            }
-    return best;
-}
-
-template <typename TO>
-static LtParams<TO> lt_params(const LinTc &q, const LinTile &t, long long M, int N) {
-    LtParams<TO> p = {};
-    p.status = q.status;
-    p.clear = q.clear;
-    p.M = (int)M;
-    p.N = N;
-    p.nseg = q.nseg;
-    for (int s = 0; s < q.nseg; ++s) p.seg |= (uint32_t)q.seg[s] << (4 * s);
-    const int bm = t.pair ? 2 * LT_BM : LT_BM;
-    p.tiles_m = (int)((M + bm - 1) / bm);
-    p.tiles_n = (N + t.bn - 1) / t.bn;
-    return p;
-}
-// The maps of the parts that are there.
-static bool lt_encode(CUtensorMap (&m)[3], const bf16 *const (&base)[3], long long rows, int ld, int box) {
-    for (int k = 0; k < 3 && base[k]; ++k)
-        if (!fast::encode_2d(&m[k], base[k], (int)rows, ld, box)) return false;
-    return true;
-}
-// The maps of the outputs and the epilogue's inputs, a warp's piece at a time.
-template <typename TO>
-static bool lt_encode_out(LtMaps &m, const LinTile &t, const void *out, const LinEpi<TO> &e, long long planes, long long M, int N) {
-    const int pc = std::min((t.pair ? 64 : 128) / (int)sizeof(TO), t.bn / 2);
-    auto enc = [&](CUtensorMap *x, const void *base) { return !base || fast::encode_3d(x, base, sizeof(TO) == 4, planes, M, N, pc, 32); };
-    return enc(&m.out, out) && enc(&m.out2, e.out2) && enc(&m.add, e.add) && enc(&m.zin, e.zin);
-}
-
-template <int KIND, typename T>
-static cudaError_t lt_product(const LinTc &q, const LinEpi<T> &e, long long M, int N, int K, cudaStream_t st) {
-    const int steps = (K + LT_BK - 1) / LT_BK;
-    const LinTile t = lt_tile(M, N, (long long)steps * q.nseg);
-    LtParams<T> p = lt_params<T>(q, t, M, N);
-    if ((long long)p.tiles_m * p.tiles_n > 0x7fffffffLL) return cudaErrorInvalidValue;
-    p.units = p.tiles_m * p.tiles_n;
-    p.e = e;
-    p.kts = steps;
-    LtMaps m;
-    const int bk = t.pair ? 128 : t.bn;             // B's columns a CTA loads
-    if (KIND == LIN_FWD ? !lt_encode(m.a, q.X, q.rows, q.ldx, LT_BM) || !lt_encode(m.b, q.W, q.in, q.ldw, 64)
-                        : !lt_encode(m.a, q.dZ, q.rows, q.ldz, LT_BM) || !lt_encode(m.b, q.W, q.in, q.ldw, bk))
-        return cudaErrorInvalidValue;
-    if ((long long)N * sizeof(T) % 16) return lt_run<KIND, T, false>(t, m, p, st);
-    if (!lt_encode_out<T>(m, t, e.out, e, 1, M, N)) return cudaErrorInvalidValue;
-    return lt_run<KIND, T, true>(t, m, p, st);
-}
-template <typename T>
-cudaError_t lin_tc_forward(const LinTc &q, const LinEpi<T> &e, cudaStream_t st) {
-    return lt_product<LIN_FWD, T>(q, e, q.rows, q.out, q.in, st);
-}
-template <typename T>
-cudaError_t lin_tc_dx(const LinTc &q, const LinEpi<T> &e, cudaStream_t st) {
-    return lt_product<LIN_DX, T>(q, e, q.rows, q.in, q.out, st);
-}
-template cudaError_t lin_tc_forward<bf16>(const LinTc &, const LinEpi<bf16> &, cudaStream_t);
-template cudaError_t lin_tc_dx<bf16>(const LinTc &, const LinEpi<bf16> &, cudaStream_t);
-
-LinSplit lin_tc_dw_split(long long rows, int in, int out, int nseg) {
-    const long long steps = std::max(1LL, (rows + LT_BK - 1) / LT_BK);
-    LinSplit best = {1, steps * LT_BK, LT_TILES[2]};
-    double least = 1e300;
-    for (const LinTile &t : LT_TILES) {
-        if (!lt_fits(t, in, out)) continue;
-        // splits of four steps or more, up to two for each SM
-        const int most = (int)std::max(1LL, std::min(steps / 4, 2LL * sm_count()));
+    for (const LinTile &t : tiles) {
+        if (t.pair ? M <= 128 || N <= 128 : t.bn == 128 && N <= 64) continue;
+        // splits of four steps or more, while they are not more than two units an SM
+        const int bm = t.pair ? 256 : 128;
+        const long long units = (M + bm - 1) / bm * ((N + t.bn - 1) / t.bn);
+        const int most = (int)std::max(1LL, std::min(steps * nseg / 4, std::min(steps, 2LL * sm_count() / units)));
         for (int s = 1; s <= most; ++s) {
             const long long per = (steps + s - 1) / s;
-            const int real = (int)((steps + per - 1) / per);
-            if (real != s) continue;
-            const double c = lt_cost(t, in, out, steps * nseg, s, true);
+            if ((steps + per - 1) / per != s) continue;
+            const double c = lt_cost(t, M, N, steps * nseg, s);
             if (c < least) {
                 least = c;
                 best = {s, per * LT_BK, t};
@@ -795,23 +728,70 @@ LinSplit lin_tc_dw_split(long long rows, int in, int out, int nseg) {
     return best;
 }
 
-cudaError_t lin_tc_dw(const LinTc &q, const LinSplit &s, float *dW, float *db, cudaStream_t st) {
-    LtParams<float> p = lt_params<float>(q, s.tile, q.in, q.out);
-    const long long units = (long long)p.tiles_m * p.tiles_n * s.splits;
+// The maps of the parts that are there.
+static bool lt_encode(CUtensorMap (&m)[3], const bf16 *const (&base)[3], long long rows, int ld, int box) {
+    for (int k = 0; k < 3 && base[k]; ++k)
+        if (!fast::encode_2d(&m[k], base[k], (int)rows, ld, box)) return false;
+    return true;
+}
+// The maps of the outputs and the epilogue's inputs, a warp's piece at a time.
+template <typename TO>
+static bool lt_encode_out(LtMaps &m, const LinTile &t, const LinEpi<TO> &e, long long planes, long long M, int N) {
+    const int pc = std::min((t.pair ? 64 : 128) / (int)sizeof(TO), t.bn / 2);
+    auto enc = [&](CUtensorMap *x, const void *base) { return !base || fast::encode_3d(x, base, sizeof(TO) == 4, planes, M, N, pc, 32); };
+    return enc(&m.out, e.out) && enc(&m.out2, e.out2) && enc(&m.add, e.add) && enc(&m.zin, e.zin);
+}
+
+template <int KIND, typename T>
+static cudaError_t lt_product(const LinTc &q, const LinSplit &sp, const LinEpi<T> &e, float *db, long long M, int N, long long K,
+                              cudaStream_t st) {
+    LtParams<T> p = {};
+    p.status = q.status;
+    p.clear = q.clear;
+    p.M = (int)M;
+    p.N = N;
+    p.nseg = q.nseg;
+    for (int s = 0; s < q.nseg; ++s) p.seg |= (uint32_t)q.seg[s] << (4 * s);
+    const int bm = sp.tile.pair ? 2 * LT_BM : LT_BM;
+    p.tiles_m = (int)((M + bm - 1) / bm);
+    p.tiles_n = (N + sp.tile.bn - 1) / sp.tile.bn;
+    const long long units = (long long)p.tiles_m * p.tiles_n * sp.splits;
     if (units > 0x7fffffffLL) return cudaErrorInvalidValue;
     p.units = (int)units;
-    p.acc = dW; p.db = db;
+    p.kts = (int)((K + LT_BK - 1) / LT_BK);
+    p.per = (int)(sp.chunk / LT_BK);
+    p.e = e;
+    p.db = db;
     for (int k = 0; k < 3; ++k) p.dz[k] = q.dZ[k];
     p.ldz = q.ldz;
     p.rows = (int)q.rows;
-    p.per = (int)(s.chunk / LT_BK);
-    p.kts = (int)((q.rows + LT_BK - 1) / LT_BK);
     LtMaps m;
-    if (!lt_encode(m.a, q.X, q.rows, q.ldx, 64) || !lt_encode(m.b, q.dZ, q.rows, q.ldz, 64)) return cudaErrorInvalidValue;
-    if (q.out % 4) return lt_run<LIN_DW, float, false>(s.tile, m, p, st);
-    if (!lt_encode_out<float>(m, s.tile, dW, p.e, s.splits, q.in, q.out)) return cudaErrorInvalidValue;
-    return lt_run<LIN_DW, float, true>(s.tile, m, p, st);
+    bool ok;
+    if (KIND == LIN_FWD) ok = lt_encode(m.a, q.X, q.rows, q.ldx, LT_BM) && lt_encode(m.b, q.W, q.in, q.ldw, 64);
+    else if (KIND == LIN_DX) ok = lt_encode(m.a, q.dZ, q.rows, q.ldz, LT_BM) && lt_encode(m.b, q.W, q.in, q.ldw, sp.tile.pair ? 128 : sp.tile.bn);
+    else ok = lt_encode(m.a, q.X, q.rows, q.ldx, 64) && lt_encode(m.b, q.dZ, q.rows, q.ldz, 64);
+    if (!ok) return cudaErrorInvalidValue;
+    if ((long long)N * sizeof(T) % 16) return lt_run<KIND, T, false>(sp.tile, m, p, st);
+    if (!lt_encode_out<T>(m, sp.tile, e, sp.splits, M, N)) return cudaErrorInvalidValue;
+    return lt_run<KIND, T, true>(sp.tile, m, p, st);
 }
+template <typename T>
+cudaError_t lin_tc_forward(const LinTc &q, const LinSplit &s, const LinEpi<T> &e, cudaStream_t st) {
+    return lt_product<LIN_FWD, T>(q, s, e, nullptr, q.rows, q.out, q.in, st);
+}
+template <typename T>
+cudaError_t lin_tc_dx(const LinTc &q, const LinSplit &s, const LinEpi<T> &e, cudaStream_t st) {
+    return lt_product<LIN_DX, T>(q, s, e, nullptr, q.rows, q.in, q.out, st);
+}
+cudaError_t lin_tc_dw(const LinTc &q, const LinSplit &s, float *dW, float *db, cudaStream_t st) {
+    LinEpi<float> e = {};
+    e.out = dW;
+    return lt_product<LIN_DW, float>(q, s, e, db, q.in, q.out, q.rows, st);
+}
+template cudaError_t lin_tc_forward<bf16>(const LinTc &, const LinSplit &, const LinEpi<bf16> &, cudaStream_t);
+template cudaError_t lin_tc_forward<float>(const LinTc &, const LinSplit &, const LinEpi<float> &, cudaStream_t);
+template cudaError_t lin_tc_dx<bf16>(const LinTc &, const LinSplit &, const LinEpi<bf16> &, cudaStream_t);
+template cudaError_t lin_tc_dx<float>(const LinTc &, const LinSplit &, const LinEpi<float> &, cudaStream_t);
 
 }  // namespace ops
 }  // namespace eaga

@@ -58,7 +58,7 @@ def cuda(*ts):
 SHAPES = [  # rows, in, out: tile edges, rows that are not 16 bytes, one of each, reductions over many rows
     (1, 1, 1), (1, 512, 40), (3, 7, 5), (8, 64, 64), (9, 64, 64), (16, 8, 4), (127, 65, 33), (128, 64, 128), (129, 128, 256),
     (130, 72, 264), (257, 200, 136), (5, 1040, 72), (2, 4099, 131), (700, 8, 520), (64, 640, 8), (3000, 24, 16), (20011, 64, 128),
-    (33, 300, 2056), (1000, 257, 131),
+    (33, 300, 2056), (1000, 257, 131), (11, 3800, 9), (516, 2776, 132), (40, 9, 3801), (260, 12, 2000), (9, 1, 1), (64, 65536, 3),
 ]
 
 
@@ -89,33 +89,55 @@ def test_exact_products(rows, i, o, dtype):
     assert torch.equal(dB.cpu().double(), dz.sum(0))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("rows,i,o", [(4000, 200, 2056), (3900, 136, 2051), (4000, 2056, 200), (3900, 2051, 140), (520, 4000, 2056),
                                       (777, 2200, 4099), (10_000, 1000, 1032)])
-def test_exact_products_of_large_tiles(rows, i, o):
+def test_exact_products_of_large_tiles(rows, i, o, dtype):
     """Results of many tiles, whole and ragged, and reductions of many steps."""
     g = torch.Generator().manual_seed(rows + i)
-    X, W, b, R = cuda(*(whole(g, *s, dtype="bf16") for s in ((rows, i), (i, o), (o,), (rows, o))))
-    dY, dR, Zin, zo = cuda(*(whole(g, *s, dtype="bf16") for s in ((rows, o), (rows, i), (rows, i), (rows, o))))
+    X, W, b, R = cuda(*(whole(g, *s, dtype=dtype) for s in ((rows, i), (i, o), (o,), (rows, o))))
+    dY, dR, Zin, zo = cuda(*(whole(g, *s, dtype=dtype) for s in ((rows, o), (rows, i), (rows, i), (rows, o))))
     z = X.double() @ W.double() + b.double()
     for res in (R, None):
         for save in (True, False):
-            Y, Z = forward(X, W, b, res, act="relu", save=save)
+            Y, Z = forward(X, W, b, res, act="relu", save=save, dtype=dtype)
             if save:
-                assert torch.equal(Z, z.bfloat16())
-            assert torch.equal(Y, (z.clamp(min=0) + (R.double() if res is not None else 0)).bfloat16())
-    dX, dW, dB = backward(X, W, dY)
-    assert torch.equal(dX, (dY.double() @ W.double().T).bfloat16())
+                assert torch.equal(Z, z.to(TD[dtype]))
+            assert torch.equal(Y, (z.clamp(min=0) + (R.double() if res is not None else 0)).to(TD[dtype]))
+    dX, dW, dB = backward(X, W, dY, dtype=dtype)
+    assert torch.equal(dX, (dY.double() @ W.double().T).to(TD[dtype]))
     assert torch.equal(dW.double(), X.double().T @ dY.double())
     assert torch.equal(dB.double(), dY.double().sum(0))
     dz = dY.double() * (zo.double() > 0)
     dx = (dz @ W.double().T) * (Zin.double() > 0)
     for res in (dR, None):
-        dX, dW, dB = backward(X, W, dY, Z=zo, act="relu", act_in="relu", Zin=Zin, dR=res)
-        assert torch.equal(dX.double(), (dx + (dR.double() if res is not None else 0)).bfloat16().double())
+        dX, dW, dB = backward(X, W, dY, Z=zo, act="relu", act_in="relu", Zin=Zin, dR=res, dtype=dtype)
+        assert torch.equal(dX.double(), (dx + (dR.double() if res is not None else 0)).to(TD[dtype]).double())
         assert torch.equal(dW.double(), X.double().T @ dz)
         assert torch.equal(dB.double(), dz.sum(0))
-    dX, _, _ = backward(None, W, dY, dR=dR, dw=False)
-    assert torch.equal(dX, (dY.double() @ W.double().T + dR.double()).bfloat16())
+    dX, _, _ = backward(None, W, dY, dR=dR, dw=False, dtype=dtype)
+    assert torch.equal(dX, (dY.double() @ W.double().T + dR.double()).to(TD[dtype]))
+
+
+@pytest.mark.parametrize("xbits,wbits", [(23, 1), (1, 23), (12, 12), (16, 8), (8, 16)])
+def test_all_bits_of_fp32_operands(xbits, wbits):
+    """Whole numbers of up to 24 bits, one product a sum: exact only if no part of an operand that counts is left out."""
+    g = torch.Generator().manual_seed(xbits)
+    rows, i, o = 200, 72, 40
+
+    def numbers(bits, *s):
+        return (torch.randint(1 << (bits - 1), 1 << bits, s, generator=g) * (2 * torch.randint(0, 2, s, generator=g) - 1)).float()
+
+    X = numbers(xbits, rows, 1) * torch.nn.functional.one_hot(torch.arange(rows) % i, i).float()
+    W = numbers(wbits, i, o)
+    Y, _ = forward(*cuda(X, W), dtype="fp32")
+    assert torch.equal(Y.cpu().double(), X.double() @ W.double())
+    dY = numbers(xbits, rows, 1) * torch.nn.functional.one_hot(torch.arange(rows) % o, o).float()
+    dX, _, _ = backward(None, *cuda(W, dY), dtype="fp32", dw=False)
+    assert torch.equal(dX.cpu().double(), dY.double() @ W.double().T)
+    X1, dY1 = numbers(xbits, i, i) * torch.eye(i), numbers(wbits, i, o)
+    _, dW, _ = backward(*cuda(X1, W, dY1), dtype="fp32", dx=False)
+    assert torch.equal(dW.cpu().double(), X1.double().T @ dY1.double())
 
 
 def act64(z, act):

@@ -144,7 +144,7 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
     if (tid == 0) {
         for (int s = 0; s < ST; ++s) {
             mbar_init(full(s), 1);
-            mbar_init(empty(s), SMEM_SUMS ? 3 : 1);          // the MMAs; two column-sum warps
+            mbar_init(empty(s), SMEM_SUMS && p.db ? 3 : 1);  // the MMAs; two column-sum warps
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(acc_full(b), 1);
@@ -252,7 +252,6 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
                 for (int u = first; ok && u < p.units; u += stride) {
                     const Unit t = unit_of(u);
                     const int nk = t.steps * p.nseg;
-                    const bool sums = SMEM_SUMS && p.db != nullptr && t.tm == 0;
                     for (int k0 = 0; ok && k0 < nk; ++n) {
                         const int b = n & 1, k1 = PROMO ? min(k0 + LT_PROMO, nk) : nk;
                         if (!lt_wait(acc_empty(b), ((n >> 1) & 1) ^ 1, fail, p.status)) { ok = false; break; }
@@ -270,10 +269,6 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
                             }
                             if constexpr (PAIR) mma_commit_pair(empty(s), 3);
                             else mma_commit(empty(s));
-                            if (SMEM_SUMS && !sums) {            // no column sums: their two arrivals
-                                mbar_arrive(empty(s));
-                                mbar_arrive(empty(s));
-                            }
                             if (++s == ST) {
                                 s = 0;
                                 ph ^= 1;
@@ -300,13 +295,10 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
                 const int c0 = (w - 2) * COLS;
                 int it = 0;
                 bool ok = true;
-                for (int u = first; ok && u < p.units; u += stride) {
+                // every step of every unit, the unsummed ones too: a wait by parity knows a phase from its neighbours only
+                for (int u = first; p.db != nullptr && ok && u < p.units; u += stride) {
                     const Unit t = unit_of(u);
                     const int nk = t.steps * p.nseg;
-                    if (p.db == nullptr || t.tm != 0) {
-                        it += nk;
-                        continue;
-                    }
                     float sum[NT][2];
 #pragma unroll
                     for (int j = 0; j < NT; ++j) sum[j][0] = sum[j][1] = 0.f;
@@ -314,7 +306,7 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
                         const int s = it % ST;
                         ok = __all_sync(0xffffffffu, lt_wait(full(s), (it / ST) & 1, fail, p.status));
                         if (!ok) break;
-                        if ((p.seg >> (4 * seg)) & 3) {     // each part of dZ once: beside X's first
+                        if (t.tm != 0 || ((p.seg >> (4 * seg)) & 3)) {     // each part of dZ once: beside X's first
                             if (lane == 0) mbar_arrive(empty(s));
                             continue;
                         }
@@ -337,7 +329,7 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
                         __syncwarp();
                         if (lane == 0) mbar_arrive(empty(s));
                     }
-                    if (ok && lane < 4) {               // row 0 of the product: columns 2 lane, 2 lane + 1 of each 8
+                    if (ok && t.tm == 0 && lane < 4) {  // row 0 of the product: columns 2 lane, 2 lane + 1 of each 8
 #pragma unroll
                         for (int j = 0; j < NT; ++j) {
                             const int c = t.n0 + c0 + 8 * j + 2 * lane;
@@ -574,7 +566,7 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
                     __syncwarp();
                     ++k;
                 } else {
-                    // rows that do not begin on 16 bytes: a lane a column, eight rows at a time
+                    // rows that do not begin on 16 bytes: a lane a column, 16 rows' loads in flight
                     __syncwarp();                   // the last piece's reads are done
 #pragma unroll
                     for (int x = 0; x < 8; ++x)
@@ -586,30 +578,37 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
                     if (cc < p.N) {
                         const float bias = KIND == LIN_FWD && p.e.bias ? ldf(p.e.bias + cc) : 0.f;
 #pragma unroll 1
-                        for (int r0 = 0; r0 < 32 && row0 + r0 < p.M; r0 += 8) {
+                        for (int r0 = 0; r0 < 32 && row0 + r0 < p.M; r0 += 16) {
                             const size_t at = (size_t)(row0 + r0) * p.N + cc;
-                            float y[8], zi[8], ad[8];
+                            TO zi[16], ad[16];
+                            if (KIND == LIN_DX && p.e.zin) {
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const bool in = row0 + r0 + j < p.M;
-                                y[j] = *reinterpret_cast<const float *>(slots_p + fast::sw128(r0 + j, lane >> 2) + 4 * (lane & 3));
-                                if (KIND == LIN_DX) zi[j] = p.e.zin && in ? ldf(p.e.zin + at + (size_t)j * p.N) : 0.f;
-                                if (KIND != LIN_DW) ad[j] = p.e.add && in ? ldf(p.e.add + at + (size_t)j * p.N) : 0.f;
+                                for (int j = 0; j < 16; ++j)
+                                    if (row0 + r0 + j < p.M) zi[j] = p.e.zin[at + (size_t)j * p.N];
                             }
-                            if constexpr (KIND == LIN_FWD) {
+                            if (KIND != LIN_DW && p.e.add) {
 #pragma unroll
-                                for (int j = 0; j < 8; ++j) {
-                                    y[j] += bias;
-                                    if (p.e.out2 && row0 + r0 + j < p.M) stf(p.e.out2 + at + (size_t)j * p.N, y[j]);
-                                }
-                                act_apply(y, p.e.act);
-                            } else if constexpr (KIND == LIN_DX) {
-                                if (p.e.zin) act_slope_mul(y, zi, p.e.act);
+                                for (int j = 0; j < 16; ++j)
+                                    if (row0 + r0 + j < p.M) ad[j] = p.e.add[at + (size_t)j * p.N];
                             }
                             TO *o = p.e.out + (size_t)t.split * p.M * p.N + at;
 #pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                if (row0 + r0 + j < p.M) stf(o + (size_t)j * p.N, KIND != LIN_DW && p.e.add ? y[j] + ad[j] : y[j]);
+                            for (int j = 0; j < 16; ++j) {
+                                if (row0 + r0 + j >= p.M) break;
+                                float y[1] = {*reinterpret_cast<const float *>(slots_p + fast::sw128(r0 + j, lane >> 2) + 4 * (lane & 3))};
+                                if constexpr (KIND == LIN_FWD) {
+                                    y[0] += bias;
+                                    if (p.e.out2) stf(p.e.out2 + at + (size_t)j * p.N, y[0]);
+                                    act_apply(y, p.e.act);
+                                } else if constexpr (KIND == LIN_DX) {
+                                    if (p.e.zin) {
+                                        const float z[1] = {ldf(&zi[j])};
+                                        act_slope_mul(y, z, p.e.act);
+                                    }
+                                }
+                                if (KIND != LIN_DW && p.e.add) y[0] += ldf(&ad[j]);
+                                stf(o + (size_t)j * p.N, y[0]);
+                            }
                         }
                     }
                     __syncwarp();
@@ -690,16 +689,17 @@ static cudaError_t lt_run(const LinTile &t, const LtMaps &m, const LtParams<TO> 
 
 // Tiles and splits: the least of an estimate of each form's time.  The unit is a 64-deep step of a pair's tile,
 // 0.28 us.  A step of the single tiles takes 0.75 (128 columns) and 0.45 (64) of it for a half and a quarter of
-// a CTA's work: the shared memory's traffic bounds them (measured 1.0e15 op/s, pairs 1.4e15).  A tile costs three
-// steps more for the pipeline's start and the epilogue's end; splits cost the write and read of their sums and,
-// of products that need no second kernel otherwise, its launch.
+// a CTA's work: the shared memory's traffic bounds them (measured 1.0e15 op/s, pairs 1.4e15).  A tile's epilogue runs
+// beside the next one's steps and bounds short reductions: 2 us and 1 us of a single tile, 11 us of a pair's, which
+// has one slot a warp and waits for each store (138936 x 24 -> 136 with two outputs: 98 us on pairs).  Splits cost the
+// write and read of their sums and, of products that need no second kernel otherwise, its launch.
 static double lt_cost(const LinTile &t, long long M, int N, long long steps, int splits) {
     const int bm = t.pair ? 256 : 128, sms = sm_count();
     const double units = (double)((M + bm - 1) / bm) * ((N + t.bn - 1) / t.bn) * splits;
-    const double step = t.pair ? 1.0 : t.bn == 128 ? 0.75 : 0.45;
+    const double step = t.pair ? 1.0 : t.bn == 128 ? 0.75 : 0.45, epilogue = t.pair ? 40 : t.bn == 128 ? 7 : 4;
     const double waves = std::ceil(units / (t.pair ? sms / 2 : sms));
-    const double per = (double)((steps + splits - 1) / splits);
-    double c = waves * (per * step + 3 * step) + 6;
+    const double per = (double)((steps + splits - 1) / splits) * step;
+    double c = (waves - 1) * std::max(per, epilogue) + per + epilogue + 4;
     if (splits > 1) c += 10 + (double)splits * M * N * 8 / 6.5e6 / 0.28;             // bytes / (bytes a us) / (us a step)
     return c;
 }

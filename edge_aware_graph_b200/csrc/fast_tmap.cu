@@ -71,6 +71,20 @@ bool encode_2d(CUtensorMap *m, const void *base, int rows, int cols, int box_row
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A row-major [rows, cols] bf16 matrix, cols a multiple of 64, as (64 columns, rows, blocks of 64 columns): a box of
+// 64 rows of `blocks` blocks lands block by block, each 64 swizzled rows of 128 bytes.
+bool encode_blocks(CUtensorMap *m, const void *base, int rows, int cols, int blocks) {
+    auto enc = get_encode();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)(cols / 64)};
+    const cuuint64_t strides[2] = {(cuuint64_t)cols * 2, 128};
+    const cuuint32_t box[3] = {64, 64, (cuuint32_t)blocks};
+    const cuuint32_t one[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // [planes, rows, cols] bf16 (or fp32) with a box of box_cols x box_rows in one plane, whose rows of 64 or 128
 // bytes land swizzled by as much; box_cols * element size is one of the two.
 bool encode_3d(CUtensorMap *m, const void *base, bool f32, long long planes, long long rows, long long cols, int box_cols,

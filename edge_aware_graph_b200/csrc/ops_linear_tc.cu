@@ -50,6 +50,7 @@
 namespace eaga {
 namespace fast {
 bool encode_2d(CUtensorMap *m, const void *base, int rows, int cols, int box_rows);
+bool encode_blocks(CUtensorMap *m, const void *base, int rows, int cols, int blocks);
 bool encode_3d(CUtensorMap *m, const void *base, bool f32, long long planes, long long rows, long long cols, int box_cols,
                int box_rows);
 }
@@ -118,6 +119,7 @@ struct LtParams {
     uint32_t seg;              // products of parts, four bits each: A's part, B's part
     int tiles_m, tiles_n, units;
     int clear;
+    int ablocks, bblocks;      // an MN-major operand's map has blocks of 64 columns: one load a step
 };
 
 template <int KIND, int BN, int CG, typename TO, bool VEC>
@@ -196,43 +198,60 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
                 int s = 0, issued = 0;                       // the stage; stages filled
                 uint32_t ph = 1;
                 bool ok = true;
+                const CUtensorMap *am = &maps.a[p.seg & 3], *bm = &maps.b[(p.seg >> 2) & 3];
+                const uint32_t full0 = PAIR ? cluster_map(full(0), 0) : full(0);     // the first CTA's barriers
+                // One 64-deep step of a unit.  This thread, like the MMAs', has 512 clocks for it on pairs: the fewer
+                // instructions and loads, the better (an MN-major operand is one load where its rows are blocks of 64 columns).
+                auto step = [&](const CUtensorMap *am, const CUtensorMap *bm, int kk, int m0, int nb) {
+                    if (!lt_wait(empty(s), ph, fail, p.status)) return false;
+                    const uint32_t st = sbase + s * S::STAGE, bar = full0 + 8 * s;
+                    if (rank == 0) mbar_expect_tx(full(s), S::STAGE * CG);
+                    auto load = [&](uint32_t dst, const CUtensorMap *m, int c0, int c1) {
+                        if constexpr (PAIR) tma_load_2d_pair(dst, m, bar, c0, c1);
+                        else tma_load_2d(dst, m, bar, c0, c1);
+                    };
+                    auto load_blocks = [&](uint32_t dst, const CUtensorMap *m, int row, int block) {
+                        if constexpr (PAIR) tma_load_3d_pair(dst, m, bar, 0, row, block);
+                        else tma_load_3d(dst, m, bar, 0, row, block);
+                    };
+                    if constexpr (!A_MN) {
+                        load(st, am, kk, m0);
+                    } else if (p.ablocks) {
+                        load_blocks(st, am, kk, m0 >> 6);
+                    } else {
+                        load(st, am, m0, kk);
+                        load(st + 8192, am, m0 + 64, kk);
+                    }
+                    if constexpr (!B_MN) {
+                        load(st + S::A_BYTES, bm, kk, nb);
+                    } else if (p.bblocks) {
+                        load_blocks(st + S::A_BYTES, bm, kk, nb >> 6);
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < S::PB / 64; ++h) load(st + S::A_BYTES + h * 8192, bm, nb + 64 * h, kk);
+                    }
+                    ++issued;
+                    if (++s == ST) {
+                        s = 0;
+                        ph ^= 1;
+                    }
+                    return true;
+                };
                 for (int u = first; ok && u < p.units; u += stride) {
                     const Unit t = unit_of(u);
                     const int nb = t.n0 + rank * S::PB;      // this CTA's columns of B
                     int kk = t.k0 * LT_BK;
-                    for (int k = t.steps; ok && k > 0; --k, kk += LT_BK) {
-                        uint32_t parts = p.seg;
-                        for (int seg = p.nseg; seg > 0; --seg, parts >>= 4) {
-                            const CUtensorMap *am = &maps.a[parts & 3], *bm = &maps.b[(parts >> 2) & 3];
-                            if (!lt_wait(empty(s), ph, fail, p.status)) { ok = false; break; }
-                            const uint32_t st = sbase + s * S::STAGE;
-                            const uint32_t bar = PAIR ? cluster_map(full(s), 0) : full(s);
-                            if (rank == 0) mbar_expect_tx(full(s), S::STAGE * CG);
-                            auto load = [&](uint32_t dst, const CUtensorMap *m, int c0, int c1) {
-                                if constexpr (PAIR) tma_load_2d_pair(dst, m, bar, c0, c1);
-                                else tma_load_2d(dst, m, bar, c0, c1);
-                            };
-                            if constexpr (A_MN) {
-                                load(st, am, t.m0, kk);
-                                load(st + 8192, am, t.m0 + 64, kk);
-                            } else {
-                                load(st, am, kk, t.m0);
-                            }
-                            if constexpr (B_MN) {
-#pragma unroll
-                                for (int h = 0; h < S::PB / 64; ++h) load(st + S::A_BYTES + h * 8192, bm, nb + 64 * h, kk);
-                            } else {
-                                load(st + S::A_BYTES, bm, kk, nb);
-                            }
-                            ++issued;
-                            if (++s == ST) {
-                                s = 0;
-                                ph ^= 1;
-                            }
+                    if (p.nseg == 1) {
+                        for (int k = t.steps; ok && k > 0; --k, kk += LT_BK) ok = step(am, bm, kk, t.m0, nb);
+                    } else {
+                        for (int k = t.steps; ok && k > 0; --k, kk += LT_BK) {
+                            uint32_t parts = p.seg;
+                            for (int seg = p.nseg; ok && seg > 0; --seg, parts >>= 4)
+                                ok = step(&maps.a[parts & 3], &maps.b[(parts >> 2) & 3], kk, t.m0, nb);
                         }
                     }
                 }
-            // After a wait that gave up: what was issued lands before the CTA's memory is released.  (Of a pair the first
+                // After a wait that gave up: what was issued lands before the CTA's memory is released.  (Of a pair the first
                 // CTA's barriers count both CTAs' loads, and the two leave together.)
                 if (!ok && rank == 0)
                     for (int i = max(issued - ST, 0); i < issued; ++i) mbar_wait(full(i % ST), (i / ST) & 1);
@@ -728,10 +747,11 @@ LinSplit lin_tc_split(long long M, int N, long long K, int nseg) {
     return best;
 }
 
-// The maps of the parts that are there.
-static bool lt_encode(CUtensorMap (&m)[3], const bf16 *const (&base)[3], long long rows, int ld, int box) {
+// The maps of the parts that are there: boxes of 64 columns and `box` rows, or of 64 rows and `blocks` blocks of columns.
+static bool lt_encode(CUtensorMap (&m)[3], const bf16 *const (&base)[3], long long rows, int ld, int box, int blocks = 0) {
     for (int k = 0; k < 3 && base[k]; ++k)
-        if (!fast::encode_2d(&m[k], base[k], (int)rows, ld, box)) return false;
+        if (!(blocks ? fast::encode_blocks(&m[k], base[k], (int)rows, ld, blocks) : fast::encode_2d(&m[k], base[k], (int)rows, ld, box)))
+            return false;
     return true;
 }
 // The maps of the outputs and the epilogue's inputs, a warp's piece at a time.
@@ -767,9 +787,12 @@ static cudaError_t lt_product(const LinTc &q, const LinSplit &sp, const LinEpi<T
     p.rows = (int)q.rows;
     LtMaps m;
     bool ok;
-    if (KIND == LIN_FWD) ok = lt_encode(m.a, q.X, q.rows, q.ldx, LT_BM) && lt_encode(m.b, q.W, q.in, q.ldw, 64);
+    const int nb = sp.tile.pair ? 2 : sp.tile.bn / 64;       // blocks of B a CTA loads
+    if (KIND != LIN_DX) p.bblocks = (KIND == LIN_FWD ? q.ldw : q.ldz) % 64 == 0 ? nb : 0;
+    if (KIND == LIN_DW) p.ablocks = q.ldx % 64 == 0 ? 2 : 0;
+    if (KIND == LIN_FWD) ok = lt_encode(m.a, q.X, q.rows, q.ldx, LT_BM) && lt_encode(m.b, q.W, q.in, q.ldw, 64, p.bblocks);
     else if (KIND == LIN_DX) ok = lt_encode(m.a, q.dZ, q.rows, q.ldz, LT_BM) && lt_encode(m.b, q.W, q.in, q.ldw, sp.tile.pair ? 128 : sp.tile.bn);
-    else ok = lt_encode(m.a, q.X, q.rows, q.ldx, 64) && lt_encode(m.b, q.dZ, q.rows, q.ldz, 64);
+    else ok = lt_encode(m.a, q.X, q.rows, q.ldx, 64, p.ablocks) && lt_encode(m.b, q.dZ, q.rows, q.ldz, 64, p.bblocks);
     if (!ok) return cudaErrorInvalidValue;
     if ((long long)N * sizeof(T) % 16) return lt_run<KIND, T, false>(sp.tile, m, p, st);
     if (!lt_encode_out<T>(m, sp.tile, e, sp.splits, M, N)) return cudaErrorInvalidValue;

@@ -143,6 +143,11 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
     const int rank = PAIR ? (int)cluster_rank() : 0;
     const int first = blockIdx.x / CG, stride = gridDim.x / CG;
 
+    if (tid == 32) {
+        prefetch_map(&maps.a[0]);
+        prefetch_map(&maps.b[0]);
+        if (VEC) prefetch_map(&maps.out);
+    }
     if (tid == 0) {
         for (int s = 0; s < ST; ++s) {
             mbar_init(full(s), 1);
@@ -707,19 +712,19 @@ static cudaError_t lt_run(const LinTile &t, const LtMaps &m, const LtParams<TO> 
 }
 
 // Tiles and splits: the least of an estimate of each form's time.  The unit is a 64-deep step of a pair's tile,
-// 0.28 us.  A step of the single tiles takes 0.75 (128 columns) and 0.45 (64) of it for a half and a quarter of
-// a CTA's work: the shared memory's traffic bounds them (measured 1.0e15 op/s, pairs 1.4e15).  A tile's epilogue runs
+// 0.28 us.  A step of the single tiles takes as long (128 columns) or 0.75 of it (64) for a half and a quarter of
+// a CTA's work: 32 and 24 KB from L2 bound them (measured 1.0e15 op/s, pairs 1.4e15).  A tile's epilogue runs
 // beside the next one's steps and bounds short reductions: 1.5 us and 1.3 us of a single tile, 11 us of a pair's, which
 // has one slot a warp and waits for each store (138936 x 24 -> 136 with two outputs: 98 us on pairs).  Splits cost the
 // write and read of their sums and, of products that need no second kernel otherwise, its launch.
 static double lt_cost(const LinTile &t, long long M, int N, long long steps, int splits) {
     const int bm = t.pair ? 256 : 128, sms = sm_count();
     const double units = (double)((M + bm - 1) / bm) * ((N + t.bn - 1) / t.bn) * splits;
-    const double step = t.pair ? 1.0 : t.bn == 128 ? 0.75 : 0.45, epilogue = t.pair ? 40 : t.bn == 128 ? 5.5 : 4.8;
+    const double step = t.bn == 64 ? 0.75 : 1.0, epilogue = t.pair ? 40 : t.bn == 128 ? 5.5 : 4.8;
     const double waves = std::ceil(units / (t.pair ? sms / 2 : sms));
     const double per = (double)((steps + splits - 1) / splits) * step;
     double c = (waves - 1) * std::max(per, epilogue) + per + epilogue + 4;
-    if (splits > 1) c += 10 + (double)splits * M * N * 8 / 6.5e6 / 0.28;             // bytes / (bytes a us) / (us a step)
+    if (splits > 1) c += 8 + (double)splits * M * N * 8 / 6.5e6 / 0.28;             // bytes / (bytes a us) / (us a step)
     return c;
 }
 

@@ -190,11 +190,11 @@ constexpr int RN_DEPTH = 4;        // steps of the backward in shared memory, th
 // those from L1 again, and run two CTAs an SM instead.
 template <int VEC, int E, bool WIDE>
 struct RnKeep {
-    static constexpr bool AHEAD = VEC == 8 && E == 8, KEEP = AHEAD && !WIDE;
+    static constexpr bool AHEAD = VEC == 8, KEEP = AHEAD && !WIDE;
 };
 
 template <typename T, int VEC, int E, bool WIDE, int MAXT>
-__global__ void __launch_bounds__(MAXT, E > 8 ? 1 : WIDE ? 1024 / MAXT : 3)
+__global__ void __launch_bounds__(MAXT, MAXT == 256 && (E > 8 || !WIDE) ? 3 : E > 8 ? 1 : 1024 / MAXT)
 k_rn_fwd(const RnArgs a) {
     after_previous();
     using IO = RowIo<T, VEC, E>;
@@ -701,36 +701,51 @@ __global__ void __launch_bounds__(1024) k_rn_finish(const FinishArgs f) {
 
 // ------------------------------------------------------------------ host side
 
+// Threads of a row and of a CTA.
+struct RnShape {
+    bool wide;
+    int e, team, threads;
+};
 struct RnPlan {
-    bool vec, wide;
-    int e, team, crew, threads, ctas_fwd, ctas_bwd;
+    bool vec;
+    RnShape fwd, bwd;
+    int crew, ctas_fwd, ctas_bwd;
     unsigned run, runs_per_group, runs;
     size_t parts, gparts, total;      // workspace offsets
 };
 
-// Elements a thread: 8, so that up to 256 elements stay in a warp; 16 for rows
-// beyond 4096 elements (a CTA of 512 threads then has the registers for the
-// backward).  A team is the smallest power of two that holds a row.
-static RnPlan rn_plan(const eaga_residual_norm_dims &d) {
-    RnPlan p;
-    const int es = d.dtype == EAGA_BF16 ? 2 : 4;
-    p.vec = (long long)d.w * es % 16 == 0;
-    p.e = d.w > 4096 ? 16 : 8;
-    const int slots = (d.w + p.e - 1) / p.e;
+// e elements a thread; a team is the smallest power of two that holds a row.
+static RnShape rn_shape(int w, int e) {
+    RnShape p;
+    p.e = e;
+    const int slots = (w + e - 1) / e;
     p.team = 1;
     while (p.team < slots) p.team <<= 1;
     p.wide = p.team > 32;
     p.threads = p.wide ? p.team : 256;
-    const long long per = p.wide ? 1 : p.threads / p.team;
+    return p;
+}
+
+// Elements a thread: 8, so that up to 256 elements stay in a warp; 16 for rows beyond 4096 elements (a CTA of 512
+// threads then has the registers for the backward), forward in bf16 beyond 2048 (three CTAs of 256 threads an SM hide
+// each other's sums better than two of 512: 8192 x 4096 rms).
+static RnPlan rn_plan(const eaga_residual_norm_dims &d) {
+    RnPlan p;
+    const int es = d.dtype == EAGA_BF16 ? 2 : 4;
+    p.vec = (long long)d.w * es % 16 == 0;
+    p.bwd = rn_shape(d.w, d.w > 4096 ? 16 : 8);
+    p.fwd = rn_shape(d.w, d.w > (p.vec && es == 2 ? 2048 : 4096) ? 16 : 8);
     const long long rows = d.rows, sms = sm_count();
-    // the registers: 512 threads an SM backward, 768 or 1024 forward
-    p.ctas_fwd = (int)std::max(1LL, std::min((rows + per - 1) / per, p.wide ? sms * (p.e > 8 ? 1 : 1024 / p.threads) : sms * 3));
+    const long long per_fwd = p.fwd.wide ? 1 : p.fwd.threads / p.fwd.team;
+    const long long each = p.fwd.threads == 256 && (p.fwd.e > 8 || !p.fwd.wide) ? 3 : p.fwd.e > 8 ? 1 : 1024 / p.fwd.threads;    // CTAs an SM
+    p.ctas_fwd = (int)std::max(1LL, std::min((rows + per_fwd - 1) / per_fwd, sms * each));
     // Backward.  A run costs a partial row of the gate's gradient, a CTA one of each parameter's: runs of four rows a team
     // or more (up to 64 rows, whose masks a warp holds), long inputs RN_ROUNDS or more a crew.
-    p.crew = p.wide ? p.team : d.rows_per_group >= 2 * 32 / p.team ? 32 : p.team;
-    const long long abreast = p.crew / p.team, crews = p.threads / p.crew, room = sms * (512 / p.threads);
+    const RnShape &b = p.bwd;
+    p.crew = b.wide ? b.team : d.rows_per_group >= 2 * 32 / b.team ? 32 : b.team;
+    const long long abreast = p.crew / b.team, crews = b.threads / p.crew, room = sms * (512 / b.threads);    // 512 threads an SM
     long long want = std::max(4 * abreast, (rows + room * crews - 1) / (room * crews));
-    const long long most = p.wide ? 64 : std::max(abreast, std::min(64LL, 16 * abreast) / abreast * abreast);
+    const long long most = b.wide ? 64 : std::max(abreast, std::min(64LL, 16 * abreast) / abreast * abreast);
     if (want > 4 * abreast) want = std::max(std::min(most, 4 * abreast), std::min(most, (rows + RN_ROUNDS * room * crews - 1) / (RN_ROUNDS * room * crews)));
     want = std::min(want, most);
     const long long parts = std::max(1LL, (d.rows_per_group + want - 1) / want);
@@ -744,9 +759,10 @@ static RnPlan rn_plan(const eaga_residual_norm_dims &d) {
     return p;
 }
 
-template <typename F>
+template <bool FWD, typename F>
 static cudaError_t rn_dispatch(const eaga_residual_norm_dims &d, const RnPlan &p, F &&f) {
     using bf = __nv_bfloat16;
+    const RnShape &sh = FWD ? p.fwd : p.bwd;
     auto pick = [&](auto t, auto vec) {
         using T = decltype(t);
         constexpr int V = decltype(vec)::value;
@@ -755,9 +771,14 @@ static cudaError_t rn_dispatch(const eaga_residual_norm_dims &d, const RnPlan &p
         constexpr std::integral_constant<int, 16> e16{};
         constexpr std::integral_constant<int, 256> t256{};
         constexpr std::integral_constant<int, 512> t512{};
-        if (p.e == 16) return go(e16, std::true_type{}, t512);
-        if (p.threads > 256) return go(e8, std::true_type{}, t512);
-        return p.wide ? go(e8, std::true_type{}, t256) : go(e8, std::false_type{}, t256);
+        if constexpr (FWD && V == 8) {
+            if (sh.e == 16 && sh.threads <= 256) return go(e16, std::true_type{}, t256);
+        }
+        if (sh.e == 16) return go(e16, std::true_type{}, t512);
+        if constexpr (!(FWD && V == 8)) {
+            if (sh.threads > 256) return go(e8, std::true_type{}, t512);
+        }
+        return sh.wide ? go(e8, std::true_type{}, t256) : go(e8, std::false_type{}, t256);
     };
     if (d.dtype == EAGA_BF16)
         return p.vec ? pick(bf{}, std::integral_constant<int, 8>{}) : pick(bf{}, std::integral_constant<int, 1>{});
@@ -775,12 +796,12 @@ static eaga_status rn_check(const eaga_residual_norm_dims *d) {
     return EAGA_OK;
 }
 
-static RnArgs rn_args(const eaga_residual_norm_dims &d, const RnPlan &p) {
+static RnArgs rn_args(const eaga_residual_norm_dims &d, const RnPlan &p, const RnShape &sh) {
     RnArgs a = {};
     a.alpha = d.alpha; a.eps = d.eps; a.inv_w = 1.f / (float)d.w;
     a.rows = (unsigned)d.rows; a.w = (unsigned)d.w; a.group = (unsigned)d.rows_per_group;
     a.run = p.run; a.runs_per_group = p.runs_per_group; a.runs = p.runs;
-    a.pre = d.pre; a.post = d.post; a.team = p.team; a.crew = p.crew;
+    a.pre = d.pre; a.post = d.post; a.team = sh.team; a.crew = p.crew;
     return a;
 }
 
@@ -823,14 +844,14 @@ eaga_status eaga_residual_norm_forward(const eaga_residual_norm_dims *d, const v
         if ((s = check_no_alias(outs, 2, ins, 8)) != EAGA_OK) return s;
     }
     const RnPlan p = rn_plan(*d);
-    RnArgs a = rn_args(*d, p);
+    RnArgs a = rn_args(*d, p, p.fwd);
     a.x = x; a.u = u; a.M = M; a.gate = gate;
     a.post_g = post_g; a.post_s = post_s; a.pre_g = pre_g; a.pre_s = pre_s;
     a.r = r; a.h = h;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = rn_dispatch(*d, p, [&](auto t, auto vec, auto el, auto wide, auto maxt) {
+    const cudaError_t e = rn_dispatch<true>(*d, p, [&](auto t, auto vec, auto el, auto wide, auto maxt) {
         return launch_pdl(k_rn_fwd<decltype(t), decltype(vec)::value, decltype(el)::value, decltype(wide)::value, decltype(maxt)::value>,
-                          dim3(p.ctas_fwd), dim3(p.threads), 0, st, 1, a);
+                          dim3(p.ctas_fwd), dim3(p.fwd.threads), 0, st, 1, a);
     });
     return e == cudaSuccess ? EAGA_OK : EAGA_ERR_CUDA;
 }
@@ -868,24 +889,24 @@ eaga_status eaga_residual_norm_backward(const eaga_residual_norm_dims *d, const 
     }
     if (ws_bytes < need) return EAGA_ERR_WORKSPACE;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    RnArgs a = rn_args(*d, p);
+    RnArgs a = rn_args(*d, p, p.bwd);
     a.u = u; a.M = M; a.gate = gate; a.post_g = post_g; a.post_s = post_s; a.pre_g = pre_g;
     a.rin = r; a.dr = dr; a.dh = dh; a.dx = dx; a.du = du; a.dgate = dgate;
     char *ws = static_cast<char *>(workspace);
     a.parts = reinterpret_cast<float *>(ws + p.parts);
     a.gparts = reinterpret_cast<float *>(ws + p.gparts);
-    cudaError_t e = rn_dispatch(*d, p, [&](auto t, auto vec, auto el, auto wide, auto maxt) {
+    cudaError_t e = rn_dispatch<false>(*d, p, [&](auto t, auto vec, auto el, auto wide, auto maxt) {
         constexpr int E = decltype(el)::value;
         constexpr bool AHEAD = decltype(vec)::value == 8 && E == 8;
         const size_t sums = decltype(wide)::value && E == 8 ? 0 : (size_t)4 * d->w * 4;
-        const size_t smem = std::max(sums, AHEAD ? (size_t)RN_DEPTH * 5 * 16 * p.threads : 0);
+        const size_t smem = std::max(sums, AHEAD ? (size_t)RN_DEPTH * 5 * 16 * p.bwd.threads : 0);
         auto kernel = k_rn_bwd<decltype(t), decltype(vec)::value, E, decltype(wide)::value, decltype(maxt)::value>;
         if (E > 8 || AHEAD) {
             static std::atomic<uint32_t> attr_set{0};
             const int most = E > 8 ? 4 * 8192 * 4 : RN_DEPTH * 5 * 16 * decltype(maxt)::value;
             if (cudaError_t err = ensure_smem_attr(kernel, most, attr_set); err != cudaSuccess) return err;
         }
-        return launch_pdl(kernel, dim3(p.ctas_bwd), dim3(p.threads), smem, st, 1, a);
+        return launch_pdl(kernel, dim3(p.ctas_bwd), dim3(p.bwd.threads), smem, st, 1, a);
     });
     if (e != cudaSuccess) return EAGA_ERR_CUDA;
     FinishArgs f = {};

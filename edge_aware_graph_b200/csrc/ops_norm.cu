@@ -32,6 +32,16 @@ namespace ops {
 
 enum { RN_NONE = EAGA_NORM_NONE, RN_LAYER = EAGA_NORM_LAYER, RN_RMS = EAGA_NORM_RMS };
 
+// The sums over partial rows that end a backward: the parameters' gradients (`parts`, a row a CTA and parameter), then
+// the gate's groups (`gparts`, a row a run).
+struct FinishArgs {
+    const float *parts, *gparts;
+    float *out[4];
+    void *dgate;
+    unsigned w, ctas, groups, runs_per_group;
+    int n_out, which[4], dtype;
+};
+
 struct RnArgs {
     const void *x, *u, *gate, *post_g, *post_s, *pre_g, *pre_s;
     const uint8_t *M;
@@ -42,6 +52,8 @@ struct RnArgs {
     float *parts, *gparts;     // [CTA][4][w] sums of the gains' and shifts' gradients, [run][w] of the gate's
     float alpha, eps, inv_w;
     unsigned rows, w, group, run, runs_per_group, runs;
+    FinishArgs fin;
+    int join;                  // the grid is one cluster (or CTA) and ends the backward itself
     int pre, post, team, crew; // threads that hold a row; threads that share a run (backward)
 };
 
@@ -317,6 +329,26 @@ k_rn_fwd(const RnArgs a) {
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
+
+// One output of the last sums.
+struct FinishJob {
+    bool param;
+    unsigned job, rows;
+    size_t stride;
+    const float *src;
+    __device__ __forceinline__ FinishJob(const FinishArgs &f, unsigned n) {
+        param = n < (unsigned)f.n_out;
+        job = param ? n : n - f.n_out;
+        rows = param ? f.ctas : f.runs_per_group;
+        stride = param ? (size_t)4 * f.w : f.w;
+        src = param ? f.parts + (size_t)f.which[job] * f.w : f.gparts + (size_t)job * f.runs_per_group * f.w;
+    }
+    __device__ __forceinline__ void put(const FinishArgs &f, unsigned c, float s) const {
+        if (param) f.out[job][c] = s;
+        else if (f.dtype == EAGA_FP32) static_cast<float *>(f.dgate)[(size_t)job * f.w + c] = s;
+        else static_cast<__nv_bfloat16 *>(f.dgate)[(size_t)job * f.w + c] = __float2bfloat16_rn(s);
+    }
+};
 
 // A crew takes runs of consecutive rows of one group (a run is the whole group
 // or a part of it).  A crew is a team, or a warp whose teams take a row each,
@@ -658,45 +690,41 @@ k_rn_bwd(const RnArgs a) {
         __syncthreads();
         for (unsigned c = threadIdx.x; c < 4 * w; c += blockDim.x) out[c] = acc[c];
     }
+    if (a.join) {                                    // few CTAs: no second launch
+        __syncthreads();
+        if (gridDim.x > 1) sm100::cluster_sync_all();       // what the others wrote is there
+        const FinishArgs &f = a.fin;
+        const unsigned long long n = (unsigned long long)(f.n_out + f.groups) * w;
+        for (unsigned long long i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) {
+            const unsigned job = (unsigned)(i / w), c = (unsigned)(i - (unsigned long long)job * w);
+            const FinishJob j(f, job);
+            float s = 0.f;
+#pragma unroll 8
+            for (unsigned r = 0; r < j.rows; ++r) s += j.src[r * j.stride + c];
+            j.put(f, c, s);
+        }
+    }
 }
 
-// The partial rows' sums, in a fixed order.  A CTA takes 32 columns of one
-// output: its 32 warps sum every 32nd row each, then the 32 in order.
-// Outputs: the four parameters' gradients (`parts` CTA rows each), then the gate's groups.
-struct FinishArgs {
-    const float *parts, *gparts;
-    float *out[4];
-    void *dgate;
-    unsigned w, ctas, groups, runs_per_group;
-    int n_out, which[4], dtype;
-};
+// A CTA takes 32 columns of one output: its 32 warps sum every 32nd row each, then the 32 in a tree.
 __global__ void __launch_bounds__(1024) k_rn_finish(const FinishArgs f) {
     after_previous();
     __shared__ float sum[32][33];
     const unsigned lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     for (unsigned job = blockIdx.y; job < f.n_out + f.groups; job += gridDim.y) {
-        const bool param = job < (unsigned)f.n_out;
-        const unsigned rows = param ? f.ctas : f.runs_per_group;
-        const size_t stride = param ? (size_t)4 * f.w : f.w;
-        const float *src = param ? f.parts + (size_t)f.which[job] * f.w
-                                 : f.gparts + (size_t)(job - f.n_out) * f.runs_per_group * f.w;
+        const FinishJob j(f, job);
         float s = 0.f;
         if (c < f.w) {
 #pragma unroll 8
-            for (unsigned r = warp; r < rows; r += 32) s += src[r * stride + c];
+            for (unsigned r = warp; r < j.rows; r += 32) s += j.src[r * j.stride + c];
         }
         sum[warp][lane] = s;
         __syncthreads();
-        if (warp == 0 && c < f.w) {
-            s = 0.f;
-#pragma unroll
-            for (int v = 0; v < 32; ++v) s += sum[v][lane];
-            if (param) f.out[job][c] = s;
-            else if (f.dtype == EAGA_FP32) static_cast<float *>(f.dgate)[(size_t)(job - f.n_out) * f.w + c] = s;
-            else static_cast<__nv_bfloat16 *>(f.dgate)[(size_t)(job - f.n_out) * f.w + c] = __float2bfloat16_rn(s);
-        }
+        s = warp_sum(sum[lane][warp]);               // column `warp`
+        if (lane == 0 && blockIdx.x * 32 + warp < f.w) j.put(f, blockIdx.x * 32 + warp, s);
         __syncthreads();
     }
+    before_next();
 }
 
 // ------------------------------------------------------------------ host side
@@ -707,7 +735,7 @@ struct RnShape {
     int e, team, threads;
 };
 struct RnPlan {
-    bool vec;
+    bool vec, join;
     RnShape fwd, bwd;
     int crew, ctas_fwd, ctas_bwd;
     unsigned run, runs_per_group, runs;
@@ -753,6 +781,8 @@ static RnPlan rn_plan(const eaga_residual_norm_dims &d) {
     p.runs_per_group = (unsigned)((d.rows_per_group + p.run - 1) / p.run);
     p.runs = (unsigned)(rows / d.rows_per_group * p.runs_per_group);
     p.ctas_bwd = (int)std::max(1LL, std::min((p.runs + crews - 1) / crews, room));
+    p.join = p.ctas_bwd <= 8;                        // a cluster: 1, 2, 4 or 8 CTAs
+    while (p.join && (p.ctas_bwd & (p.ctas_bwd - 1))) ++p.ctas_bwd;
     p.parts = 0;
     p.gparts = align256((size_t)p.ctas_bwd * 4 * d.w * 4);
     p.total = p.gparts + (p.runs_per_group > 1 ? align256((size_t)p.runs * d.w * 4) : 0);
@@ -895,6 +925,18 @@ eaga_status eaga_residual_norm_backward(const eaga_residual_norm_dims *d, const 
     char *ws = static_cast<char *>(workspace);
     a.parts = reinterpret_cast<float *>(ws + p.parts);
     a.gparts = reinterpret_cast<float *>(ws + p.gparts);
+    FinishArgs f = {};
+    float *const out[4] = {dpost_g, dpost_s, dpre_g, dpre_s};
+    for (int k = 0; k < 4; ++k)
+        if (out[k]) {
+            f.out[f.n_out] = out[k];
+            f.which[f.n_out++] = k;
+        }
+    f.groups = dgate && p.runs_per_group > 1 ? (unsigned)(d->rows / d->rows_per_group) : 0;
+    f.parts = a.parts; f.gparts = a.gparts; f.dgate = dgate;
+    f.w = a.w; f.ctas = p.ctas_bwd; f.runs_per_group = p.runs_per_group; f.dtype = d->dtype;
+    a.fin = f;
+    a.join = p.join && f.n_out + f.groups > 0;
     cudaError_t e = rn_dispatch<false>(*d, p, [&](auto t, auto vec, auto el, auto wide, auto maxt) {
         constexpr int E = decltype(el)::value;
         constexpr bool AHEAD = decltype(vec)::value == 8 && E == 8;
@@ -906,20 +948,10 @@ eaga_status eaga_residual_norm_backward(const eaga_residual_norm_dims *d, const 
             const int most = E > 8 ? 4 * 8192 * 4 : RN_DEPTH * 5 * 16 * decltype(maxt)::value;
             if (cudaError_t err = ensure_smem_attr(kernel, most, attr_set); err != cudaSuccess) return err;
         }
-        return launch_pdl(kernel, dim3(p.ctas_bwd), dim3(p.bwd.threads), smem, st, 1, a);
+        return launch_pdl(kernel, dim3(p.ctas_bwd), dim3(p.bwd.threads), smem, st, a.join ? p.ctas_bwd : 1, a);
     });
     if (e != cudaSuccess) return EAGA_ERR_CUDA;
-    FinishArgs f = {};
-    float *const out[4] = {dpost_g, dpost_s, dpre_g, dpre_s};
-    for (int k = 0; k < 4; ++k)
-        if (out[k]) {
-            f.out[f.n_out] = out[k];
-            f.which[f.n_out++] = k;
-        }
-    f.groups = dgate && p.runs_per_group > 1 ? (unsigned)(d->rows / d->rows_per_group) : 0;
-    if (f.n_out + f.groups == 0) return EAGA_OK;
-    f.parts = a.parts; f.gparts = a.gparts; f.dgate = dgate;
-    f.w = a.w; f.ctas = p.ctas_bwd; f.runs_per_group = p.runs_per_group; f.dtype = d->dtype;
+    if (a.join || f.n_out + f.groups == 0) return EAGA_OK;
     const dim3 grid((a.w + 31) / 32, std::min(f.n_out + f.groups, 65535u));
     return launch_pdl(k_rn_finish, grid, dim3(1024), 0, st, 1, f) == cudaSuccess ? EAGA_OK : EAGA_ERR_CUDA;
 }

@@ -36,9 +36,9 @@ enum { RN_NONE = EAGA_NORM_NONE, RN_LAYER = EAGA_NORM_LAYER, RN_RMS = EAGA_NORM_
 // the gate's groups (`gparts`, a row a run).
 struct FinishArgs {
     const float *parts, *gparts;
-    float *out[4];
+    float *out[4], *all[4];    // those that are wanted; by parameter
     void *dgate;
-    unsigned w, ctas, groups, runs_per_group;
+    unsigned w, ctas, groups, runs_per_group, flat;
     int n_out, which[4], dtype;
 };
 
@@ -350,6 +350,30 @@ struct FinishJob {
     }
 };
 
+// Outputs from number `job0` on, a thread four columns of them at a time, each the sum of its rows one after another.
+__device__ __forceinline__ void finish_flat(const FinishArgs &f, unsigned job0, unsigned long long first, unsigned long long step) {
+    const unsigned long long n = (unsigned long long)(f.n_out + f.groups) * f.w;
+    for (unsigned long long i = (unsigned long long)job0 * f.w + first; i < n; i += 4 * step) {
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const unsigned long long at = i + q * step;
+            if (at >= n) break;
+            const unsigned job = (unsigned)(at / f.w), c = (unsigned)(at - (unsigned long long)job * f.w);
+            const FinishJob j(f, job);
+#pragma unroll 4
+            for (unsigned r = 0; r < j.rows; ++r) s[q] += j.src[r * j.stride + c];
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const unsigned long long at = i + q * step;
+            if (at >= n) break;
+            const unsigned job = (unsigned)(at / f.w), c = (unsigned)(at - (unsigned long long)job * f.w);
+            FinishJob(f, job).put(f, c, s[q]);
+        }
+    }
+}
+
 // A crew takes runs of consecutive rows of one group (a run is the whole group
 // or a part of it).  A crew is a team, or a warp whose teams take a row each,
 // where groups are long enough: one sum of the gate's gradient a run then, and
@@ -385,7 +409,7 @@ k_rn_bwd(const RnArgs a) {
     // Sums of the gains' and shifts' gradients, post then pre: in registers, or, where a thread holds 16 columns
     // and they would not fit, in shared memory (each thread its own columns).
     constexpr bool IN_SMEM = E > 8;
-    extern __shared__ __align__(16) float acc[];     // [4][w]; before the end of the AHEAD form, the rows to come
+    extern __shared__ __align__(16) float acc[];     // [4][w], of teams in a warp [warp][4][w]; before the end of the AHEAD form, the rows to come
     f2 sums[4][IN_SMEM ? 1 : H];
     if constexpr (IN_SMEM) {
         for (unsigned c = threadIdx.x; c < 4 * w; c += blockDim.x) acc[c] = 0.f;
@@ -654,14 +678,18 @@ k_rn_bwd(const RnArgs a) {
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();                             // the sums take the rows' place
     }
-    // The CTA's sums: its warps' teams by shuffles (same columns), the warps one after another.
-    float *out = a.parts + (size_t)blockIdx.x * 4 * w;
+    // The CTA's sums: its warps' teams by shuffles (same columns), the warps in order.
+    // (One CTA alone writes the outputs.)
+    const bool alone = a.join && gridDim.x == 1;
+    float *const out = a.parts + (size_t)blockIdx.x * 4 * w;
+    auto target = [&](int n) { return alone ? a.fin.all[n] : out + n * w; };
     if constexpr (WIDE && !IN_SMEM) {
 #pragma unroll
         for (int q = 0; q < E; ++q)
             if (IO::col(q, k, team) < w) {
 #pragma unroll
-                for (int n = 0; n < 4; ++n) out[n * w + IO::col(q, k, team)] = q & 1 ? hi(sums[n][q / 2]) : lo(sums[n][q / 2]);
+                for (int n = 0; n < 4; ++n)
+                    if (float *o = target(n)) o[IO::col(q, k, team)] = q & 1 ? hi(sums[n][q / 2]) : lo(sums[n][q / 2]);
             }
     } else if constexpr (!IN_SMEM) {
         const unsigned warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
@@ -671,47 +699,50 @@ k_rn_bwd(const RnArgs a) {
             for (int n = 0; n < 4; ++n)
                 for (unsigned o = team; o < 32; o <<= 1)
                     sums[n][q] = sums[n][q] + pair(__shfl_xor_sync(0xffffffffu, lo(sums[n][q]), o), __shfl_xor_sync(0xffffffffu, hi(sums[n][q]), o));
-        for (unsigned v = 0; v < nw; ++v) {
-            if (warp == v && lane < team) {
+        if (lane < team) {
 #pragma unroll
-                for (int q = 0; q < E; ++q)
-                    if (IO::col(q, k, team) < w) {
+            for (int q = 0; q < E; ++q)
+                if (IO::col(q, k, team) < w) {
 #pragma unroll
-                        for (int n = 0; n < 4; ++n) {
-                            float &o = acc[n * w + IO::col(q, k, team)];
-                            o = (v ? o : 0.f) + (q & 1 ? hi(sums[n][q / 2]) : lo(sums[n][q / 2]));
-                        }
-                    }
-            }
-            __syncthreads();
+                    for (int n = 0; n < 4; ++n) acc[(warp * 4 + n) * w + IO::col(q, k, team)] = q & 1 ? hi(sums[n][q / 2]) : lo(sums[n][q / 2]);
+                }
+        }
+        __syncthreads();
+        for (unsigned c = threadIdx.x; c < 4 * w; c += blockDim.x) {
+            float s = 0.f;
+            for (unsigned v = 0; v < nw; ++v) s += acc[v * 4 * w + c];
+            const unsigned n = c / w;
+            if (float *o = target(n)) o[c - n * w] = s;
         }
     }
-    if constexpr (!WIDE || IN_SMEM) {
+    if constexpr (IN_SMEM) {
         __syncthreads();
-        for (unsigned c = threadIdx.x; c < 4 * w; c += blockDim.x) out[c] = acc[c];
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+            if (float *o = target(n))
+                for (unsigned c = threadIdx.x; c < w; c += blockDim.x) o[c] = acc[n * w + c];
     }
     if (a.join) {                                    // few CTAs: no second launch
         __syncthreads();
         if (gridDim.x > 1) sm100::cluster_sync_all();       // what the others wrote is there
-        const FinishArgs &f = a.fin;
-        const unsigned long long n = (unsigned long long)(f.n_out + f.groups) * w;
-        for (unsigned long long i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) {
-            const unsigned job = (unsigned)(i / w), c = (unsigned)(i - (unsigned long long)job * w);
-            const FinishJob j(f, job);
-            float s = 0.f;
-#pragma unroll 8
-            for (unsigned r = 0; r < j.rows; ++r) s += j.src[r * j.stride + c];
-            j.put(f, c, s);
-        }
+        finish_flat(a.fin, alone ? a.fin.n_out : 0, blockIdx.x * blockDim.x + threadIdx.x, gridDim.x * blockDim.x);
     }
 }
 
-// A CTA takes 32 columns of one output: its 32 warps sum every 32nd row each, then the 32 in a tree.
+// Many rows an output: a CTA takes 32 columns of it, its 32 warps sum every 32nd row each, then the 32 in a tree.  The
+// gate's groups of up to 64 runs: a thread a column (`flat` CTAs, behind the others).
 __global__ void __launch_bounds__(1024) k_rn_finish(const FinishArgs f) {
     after_previous();
     __shared__ float sum[32][33];
-    const unsigned lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
-    for (unsigned job = blockIdx.y; job < f.n_out + f.groups; job += gridDim.y) {
+    const unsigned tree = gridDim.x - f.flat, jobs = f.n_out + (f.flat ? 0 : f.groups), blocks = (f.w + 31) / 32;
+    if (blockIdx.x >= tree) {
+        finish_flat(f, f.n_out, (blockIdx.x - tree) * 1024ull + threadIdx.x, f.flat * 1024ull);
+        before_next();
+        return;
+    }
+    const unsigned lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (unsigned long long unit = blockIdx.x; unit < (unsigned long long)jobs * blocks; unit += tree) {
+        const unsigned job = (unsigned)(unit / blocks), c0 = (unsigned)(unit - (unsigned long long)job * blocks) * 32, c = c0 + lane;
         const FinishJob j(f, job);
         float s = 0.f;
         if (c < f.w) {
@@ -721,7 +752,7 @@ __global__ void __launch_bounds__(1024) k_rn_finish(const FinishArgs f) {
         sum[warp][lane] = s;
         __syncthreads();
         s = warp_sum(sum[lane][warp]);               // column `warp`
-        if (lane == 0 && blockIdx.x * 32 + warp < f.w) j.put(f, blockIdx.x * 32 + warp, s);
+        if (lane == 0 && c0 + warp < f.w) j.put(f, c0 + warp, s);
         __syncthreads();
     }
     before_next();
@@ -767,12 +798,12 @@ static RnPlan rn_plan(const eaga_residual_norm_dims &d) {
     const long long per_fwd = p.fwd.wide ? 1 : p.fwd.threads / p.fwd.team;
     const long long each = p.fwd.threads == 256 && (p.fwd.e > 8 || !p.fwd.wide) ? 3 : p.fwd.e > 8 ? 1 : 1024 / p.fwd.threads;    // CTAs an SM
     p.ctas_fwd = (int)std::max(1LL, std::min((rows + per_fwd - 1) / per_fwd, sms * each));
-    // Backward.  A run costs a partial row of the gate's gradient, a CTA one of each parameter's: runs of four rows a team
-    // or more (up to 64 rows, whose masks a warp holds), long inputs RN_ROUNDS or more a crew.
+    // Backward.  A run costs a partial row of the gate's gradient, a CTA one of each parameter's: runs of two rows a team
+    // (four a CTA) or more (up to 64 rows, whose masks a warp holds), long inputs RN_ROUNDS or more a crew.
     const RnShape &b = p.bwd;
     p.crew = b.wide ? b.team : d.rows_per_group >= 2 * 32 / b.team ? 32 : b.team;
     const long long abreast = p.crew / b.team, crews = b.threads / p.crew, room = sms * (512 / b.threads);    // 512 threads an SM
-    long long want = std::max(4 * abreast, (rows + room * crews - 1) / (room * crews));
+    long long want = std::max((b.wide ? 4 : 2) * abreast, (rows + room * crews - 1) / (room * crews));
     const long long most = b.wide ? 64 : std::max(abreast, std::min(64LL, 16 * abreast) / abreast * abreast);
     if (want > 4 * abreast) want = std::max(std::min(most, 4 * abreast), std::min(most, (rows + RN_ROUNDS * room * crews - 1) / (RN_ROUNDS * room * crews)));
     want = std::min(want, most);
@@ -932,6 +963,7 @@ eaga_status eaga_residual_norm_backward(const eaga_residual_norm_dims *d, const 
             f.out[f.n_out] = out[k];
             f.which[f.n_out++] = k;
         }
+    for (int k = 0; k < 4; ++k) f.all[k] = out[k];
     f.groups = dgate && p.runs_per_group > 1 ? (unsigned)(d->rows / d->rows_per_group) : 0;
     f.parts = a.parts; f.gparts = a.gparts; f.dgate = dgate;
     f.w = a.w; f.ctas = p.ctas_bwd; f.runs_per_group = p.runs_per_group; f.dtype = d->dtype;
@@ -940,7 +972,7 @@ eaga_status eaga_residual_norm_backward(const eaga_residual_norm_dims *d, const 
     cudaError_t e = rn_dispatch<false>(*d, p, [&](auto t, auto vec, auto el, auto wide, auto maxt) {
         constexpr int E = decltype(el)::value;
         constexpr bool AHEAD = decltype(vec)::value == 8 && E == 8;
-        const size_t sums = decltype(wide)::value && E == 8 ? 0 : (size_t)4 * d->w * 4;
+        const size_t sums = decltype(wide)::value ? (E == 8 ? 0 : (size_t)4 * d->w * 4) : (size_t)p.bwd.threads / 32 * 4 * d->w * 4;
         const size_t smem = std::max(sums, AHEAD ? (size_t)RN_DEPTH * 5 * 16 * p.bwd.threads : 0);
         auto kernel = k_rn_bwd<decltype(t), decltype(vec)::value, E, decltype(wide)::value, decltype(maxt)::value>;
         if (E > 8 || AHEAD) {
@@ -952,8 +984,11 @@ eaga_status eaga_residual_norm_backward(const eaga_residual_norm_dims *d, const 
     });
     if (e != cudaSuccess) return EAGA_ERR_CUDA;
     if (a.join || f.n_out + f.groups == 0) return EAGA_OK;
-    const dim3 grid((a.w + 31) / 32, std::min(f.n_out + f.groups, 65535u));
-    return launch_pdl(k_rn_finish, grid, dim3(1024), 0, st, 1, f) == cudaSuccess ? EAGA_OK : EAGA_ERR_CUDA;
+    const unsigned long long cols = (a.w + 31) / 32, most = 2ull * sm_count();
+    if (f.groups && f.runs_per_group <= 64) f.flat = (unsigned)std::min(most, ((unsigned long long)f.groups * f.w + 4095) / 4096);
+    const unsigned long long units = (f.n_out + (f.flat ? 0ull : f.groups)) * cols;
+    const unsigned grid = (unsigned)std::min(units, 1ull << 20) + f.flat;
+    return launch_pdl(k_rn_finish, dim3(grid), dim3(1024), 0, st, 1, f) == cudaSuccess ? EAGA_OK : EAGA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -985,7 +985,7 @@ eaga_status eaga_residual_norm_backward(const eaga_residual_norm_dims *d, const 
     if (e != cudaSuccess) return EAGA_ERR_CUDA;
     if (a.join || f.n_out + f.groups == 0) return EAGA_OK;
     const unsigned long long cols = (a.w + 31) / 32, most = 2ull * sm_count();
-    if (f.groups && f.runs_per_group <= 64) f.flat = (unsigned)std::min(most, ((unsigned long long)f.groups * f.w + 4095) / 4096);
+    if (f.groups && f.runs_per_group <= 64) f.flat = (unsigned)std::min(most, ((unsigned long long)f.groups * f.w + 1023) / 1024);
     const unsigned long long units = (f.n_out + (f.flat ? 0ull : f.groups)) * cols;
     const unsigned grid = (unsigned)std::min(units, 1ull << 20) + f.flat;
     return launch_pdl(k_rn_finish, dim3(grid), dim3(1024), 0, st, 1, f) == cudaSuccess ? EAGA_OK : EAGA_ERR_CUDA;

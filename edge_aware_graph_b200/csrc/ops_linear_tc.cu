@@ -7,7 +7,7 @@
 // so every operand is read as it lies in memory.  Persistent CTAs take output
 // tiles: a TMA warp fills a ring of 64-deep operand tiles (128-byte swizzled),
 // one thread of the next warp issues the MMAs into one of two fp32 accumulators
-// in TMEM, and eight warps drain the other one, so the epilogue of a tile hides
+// in TMEM, and 8 or 16 warps drain the other one, so the epilogue of a tile hides
 // behind the next tile's products.
 //
 // Large products (CG = 2) run on pairs of CTAs: a 256 x 256 tile, of which each
@@ -60,38 +60,31 @@ using namespace sm100;
 typedef __nv_bfloat16 bf16;
 
 constexpr int LT_BM = 128, LT_BK = 64;
-constexpr int LT_EPI = 8;                              // epilogue warps: two a TMEM quadrant
-constexpr int LT_THR = 32 * (4 + LT_EPI);              // TMA, MMA, two column-sum warps, epilogue
 constexpr int LT_PROMO = 8;                            // 64-deep steps an accumulator of an fp32 result takes
-
-// Registers of a pair's CTA with 128 sums a lane in the epilogue: 384 threads launched with 168 each; the four
-// other warps keep 88, the eight epilogue warps get 208 (128 x 88 + 256 x 208 = 384 x 168).
-constexpr int LT_REGS = 168, LT_REGS_LOW = 88, LT_REGS_EPI = 208;
-static_assert(128 * LT_REGS_LOW + 256 * LT_REGS_EPI <= LT_THR * LT_REGS, "register split");
 
 template <int KIND, int BN, int CG, typename TO, bool VEC>
 struct Lt {
     static constexpr int BM = LT_BM * CG, PB = BN / CG;              // the tile's rows; B columns a CTA holds
     static constexpr bool PROMO = KIND == LIN_DW || sizeof(TO) == 4;
-    static constexpr int HALF = BN / 2;                              // columns of an epilogue warp
-    // A piece's columns: rows of 128 bytes, or 64 where the tile is narrow or, on pairs, the ring needs the room.
-    static constexpr int ROW = CG == 2 ? 64 : 128;
-    static constexpr int PC = VEC ? (ROW / (int)sizeof(TO) < HALF ? ROW / (int)sizeof(TO) : HALF) : 32;
-    static constexpr int PIECES = HALF / PC;
+    // Epilogue warps: two or four a TMEM quadrant (32 rows), each with its part of the columns.  A short reduction's tile is
+    // bound by them: with 8 warps on 128 columns 34355 x 16 -> 1320 with silu and Z took 60 us.
+    static constexpr int EPI = BN == 64 ? 8 : 16, THR = 32 * (4 + EPI);      // TMA, MMA, two column-sum warps, epilogue
+    static constexpr int COLS = BN / (EPI / 4);                      // columns of an epilogue warp
+    static constexpr int PC = VEC ? 64 / (int)sizeof(TO) : 32;       // a piece's columns: rows of 64 bytes in a slot
+    static constexpr int PIECES = COLS / PC;
     static constexpr uint32_t A_BYTES = LT_BM * LT_BK * 2, B_BYTES = PB * LT_BK * 2, STAGE = A_BYTES + B_BYTES;
-    static constexpr uint32_t SLOT = VEC ? 32 * PC * sizeof(TO) : 4096;
+    static constexpr uint32_t SLOT = VEC ? 2048 : 4096;
     // Slots of a warp: the output's (in it the residual), two in turn where the epilogue is not hidden behind long
     // products anyway; one for Z or Zin.
-    static constexpr int NIO = CG == 2 && KIND != LIN_DW ? 1 : 2, SLOTS = KIND == LIN_DW ? NIO : NIO + 1;
-    static constexpr uint32_t RING = 232448 - 1024 - 512 - LT_EPI * SLOTS * SLOT;
+    static constexpr int NIO = !VEC || (CG == 2 && KIND != LIN_DW) ? 1 : 2, SLOTS = !VEC || KIND == LIN_DW ? NIO : NIO + 1;
+    static constexpr uint32_t RING = 232448 - 1024 - 1024 - EPI * SLOTS * SLOT;
     static constexpr int ST = RING / STAGE < 8 ? RING / STAGE : 8;
-    static constexpr uint32_t EPI = ST * STAGE;
-    static constexpr uint32_t BAR = EPI + LT_EPI * SLOTS * SLOT;     // full[ST], empty[ST], acc_full[2], acc_empty[2], drained, slots' [EPI][3]
-    static constexpr uint32_t TM = BAR + (2 * ST + 5 + 3 * LT_EPI) * 8;
+    static constexpr uint32_t EPI_AT = ST * STAGE;
+    static constexpr uint32_t BAR = EPI_AT + EPI * SLOTS * SLOT;     // full[ST], empty[ST], acc_full[2], acc_empty[2], drained, slots' [EPI][3]
+    static constexpr uint32_t TM = BAR + (2 * ST + 5 + 3 * EPI) * 8;
     static constexpr uint32_t FAIL = TM + 4;
-    static constexpr uint32_t SUM = FAIL + 4;
-    static constexpr uint32_t BYTES = SUM + 8 + 1024;
-    static_assert(ST >= 3 && BYTES <= 232448, "shared memory");
+    static constexpr uint32_t BYTES = FAIL + 4 + 1024;
+    static_assert(ST >= 3 && BYTES <= 232448 && COLS % 32 == 0, "shared memory");
 };
 
 // A bounded wait that looks at the CTA's failure flag only where the barrier is not there yet.
@@ -123,7 +116,7 @@ struct LtParams {
 };
 
 template <int KIND, int BN, int CG, typename TO, bool VEC>
-__global__ void __launch_bounds__(LT_THR, 1)
+__global__ void __launch_bounds__(Lt<KIND, BN, CG, TO, VEC>::THR, 1)
 k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<TO> p) {
     using S = Lt<KIND, BN, CG, TO, VEC>;
     constexpr int ST = S::ST, PC = S::PC, PIECES = S::PIECES;
@@ -155,10 +148,10 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(acc_full(b), 1);
-            mbar_init(acc_empty(b), LT_EPI * CG);
+            mbar_init(acc_empty(b), S::EPI * CG);
         }
         mbar_init(drained, 1);
-        for (int k = 0; k < 3 * LT_EPI; ++k) mbar_init(drained + 8 + 8 * k, 1);
+        for (int k = 0; k < 3 * S::EPI; ++k) mbar_init(drained + 8 + 8 * k, 1);
         fence_mbar_init();
         *fail = 0;
     }
@@ -178,7 +171,6 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
     if constexpr (PAIR) cluster_sync_all();                  // the other CTA's barriers are there
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sp + S::TM);
-    constexpr bool REGS = PAIR && PROMO;
     // unit -> output tile (columns fastest), split, its steps
     struct Unit {
         int m0, n0, split, k0, steps, tm;
@@ -197,7 +189,6 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
     };
 
     if (w < 4) {
-        if constexpr (REGS) regs_dec<LT_REGS_LOW>();
         if (w == 0) {
             if (lane == 0) {
                 int s = 0, issued = 0;                       // the stage; stages filled
@@ -404,17 +395,15 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
             }
         }
     } else {
-        if constexpr (REGS) regs_inc<LT_REGS_EPI>();
-        const int q = w & 3, half = (w - 4) >> 2, ew = w - 4;   // TMEM quadrant: rows 32 q ..; the tile's columns: half
-        const uint32_t slots = sbase + S::EPI + ew * S::SLOTS * S::SLOT;
-        const uint8_t *slots_p = sp + S::EPI + ew * S::SLOTS * S::SLOT;
+        const int q = w & 3, ew = w - 4, first_col = (ew >> 2) * S::COLS;   // TMEM quadrant: rows 32 q ..; its columns of the tile
+        const uint32_t slots = sbase + S::EPI_AT + ew * S::SLOTS * S::SLOT;
+        const uint8_t *slots_p = sp + S::EPI_AT + ew * S::SLOTS * S::SLOT;
         const uint32_t slot_bar = drained + 8 + 24 * ew;
         const bool has_add = VEC && KIND != LIN_DW && p.e.add != nullptr, has_zin = VEC && KIND == LIN_DX && p.e.zin != nullptr;
         const bool has_z = VEC && KIND == LIN_FWD && p.e.out2 != nullptr;
         const bool two = has_add && has_zin;        // Zin goes to the third slot where the residual has the output's
-        auto swz = [](uint32_t row, uint32_t ch) { return S::SLOT == 4096 ? fast::sw128(row, ch) : fast::sw64(row, ch); };
         // the pieces with something in them, in order
-        auto some = [&](const Unit &t, int c) { return t.m0 + 32 * q < p.M && t.n0 + half * S::HALF + c * PC < p.N; };
+        auto some = [&](const Unit &t, int c) { return t.m0 + 32 * q < p.M && t.n0 + first_col + c * PC < p.N; };
         struct Place {
             int u, c;
         };
@@ -431,7 +420,7 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
         auto ask = [&](Place x, int k, bool side) {
             if (x.u >= p.units) return;
             const Unit t = unit_of(x.u);
-            const int col = t.n0 + half * S::HALF + x.c * PC, row = t.m0 + 32 * q;
+            const int col = t.n0 + first_col + x.c * PC, row = t.m0 + 32 * q;
             const int s = side ? S::NIO : k % S::NIO;
             mbar_expect_tx(slot_bar + 8 * s, S::SLOT);
             tma_load_3d(slots + s * S::SLOT, side || !has_add ? &maps.zin : &maps.add, slot_bar + 8 * s, col, row, 0);
@@ -450,7 +439,7 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
         for (int u = first; ok && u < p.units; u += stride) {
             const Unit t = unit_of(u);
             const int nk = t.steps * p.nseg, chunks = PROMO ? (nk + LT_PROMO - 1) / LT_PROMO : 1;
-            float acc[PROMO ? S::HALF : 1] = {};
+            float acc[PROMO ? S::COLS : 1] = {};
             auto released = [&](int b) {            // the accumulator may be written again
                 tc_fence_before();
                 __syncwarp();
@@ -465,14 +454,14 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
                 if (!ok) break;
                 tc_fence_after();
                 if constexpr (PROMO) {
-                    const uint32_t ta = tmem + b * BN + ((uint32_t)(32 * q) << 16) + half * S::HALF;
+                    const uint32_t ta = tmem + b * BN + ((uint32_t)(32 * q) << 16) + first_col;
 #pragma unroll
-                    for (int c = 0; c < S::HALF; c += 32) {
-                        float v[32];
-                        tmem_ld32(ta + c, v);
+                    for (int c = 0; c < S::COLS; c += 16) {
+                        float v[16];
+                        tmem_ld16(ta + c, v);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) acc[c + j] += v[j];
+                        for (int j = 0; j < 16; ++j) acc[c + j] += v[j];
                     }
                     released(b);
                 }
@@ -481,7 +470,7 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
             const int b = (n - 1) & 1;
             const int row0 = t.m0 + 32 * q;
             auto piece = [&](int c, float (&v)[PC]) {
-                const int col = t.n0 + half * S::HALF + c * PC;
+                const int col = t.n0 + first_col + c * PC;
                 if (row0 >= p.M || col >= p.N) return;
                 if constexpr (VEC) {
                     const int s = k % S::NIO;
@@ -518,13 +507,13 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
                                 if constexpr (sizeof(TO) == 2) o[j] = pack_bf16(v[x * 8 + 2 * j], v[x * 8 + 2 * j + 1]);
                                 else o[j] = __float_as_uint(v[x * 4 + j]);
                             }
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(base + swz(lane, x)), "r"(o[0]), "r"(o[1]),
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(base + fast::sw64(lane, x)), "r"(o[0]), "r"(o[1]),
                                          "r"(o[2]), "r"(o[3])
                                          : "memory");
                         }
                     };
                     auto get = [&](const uint8_t *base, int x, float (&f)[PER]) {
-                        const uint4 a = *reinterpret_cast<const uint4 *>(base + swz(lane, x));
+                        const uint4 a = *reinterpret_cast<const uint4 *>(base + fast::sw64(lane, x));
                         const uint32_t y[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -651,7 +640,7 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
 #pragma unroll 1
                 for (int c = 0; c < PIECES; ++c) {
                     float v[PC];
-                    const uint32_t ta = tmem + b * BN + ((uint32_t)(32 * q) << 16) + half * S::HALF + c * PC;
+                    const uint32_t ta = tmem + b * BN + ((uint32_t)(32 * q) << 16) + first_col + c * PC;
 #pragma unroll
                     for (int j = 0; j < PC; j += 32) tmem_ld32(ta + j, *reinterpret_cast<float(*)[32]>(v + j));
                     tmem_ld_wait();
@@ -691,18 +680,7 @@ static cudaError_t lt_launch(const LtMaps &m, const LtParams<TO> &p, cudaStream_
     auto kernel = k_lin_tc<KIND, BN, CG, TO, VEC>;
     static std::atomic<uint32_t> attr_set{0};
     if (cudaError_t e = ensure_smem_attr(kernel, S::BYTES, attr_set); e != cudaSuccess) return e;
-    if constexpr (CG == 2 && S::PROMO) {
-        // the register split draws on what the launch has: never with less
-        static std::atomic<int> regs{0};
-        int r = regs.load(std::memory_order_relaxed);
-        if (!r) {
-            cudaFuncAttributes a;
-            if (cudaError_t e = cudaFuncGetAttributes(&a, kernel); e != cudaSuccess) return e;
-            regs.store(r = a.numRegs, std::memory_order_relaxed);
-        }
-        if (r < LT_REGS) return cudaErrorLaunchOutOfResources;
-    }
-    return launch_pdl(kernel, dim3((unsigned)(std::min(p.units, sm_count() / CG) * CG)), dim3(LT_THR), S::BYTES, st, CG, m, p);
+    return launch_pdl(kernel, dim3((unsigned)(std::min(p.units, sm_count() / CG) * CG)), dim3(S::THR), S::BYTES, st, CG, m, p);
 }
 template <int KIND, typename TO, bool VEC>
 static cudaError_t lt_run(const LinTile &t, const LtMaps &m, const LtParams<TO> &p, cudaStream_t st) {
@@ -714,13 +692,13 @@ static cudaError_t lt_run(const LinTile &t, const LtMaps &m, const LtParams<TO> 
 // Tiles and splits: the least of an estimate of each form's time.  The unit is a 64-deep step of a pair's tile,
 // 0.28 us.  A step of the single tiles takes as long (128 columns) or 0.75 of it (64) for a half and a quarter of
 // a CTA's work: 32 and 24 KB from L2 bound them (measured 1.0e15 op/s, pairs 1.4e15).  A tile's epilogue runs
-// beside the next one's steps and bounds short reductions: 1.5 us and 1.3 us of a single tile, 11 us of a pair's, which
-// has one slot a warp and waits for each store (138936 x 24 -> 136 with two outputs: 98 us on pairs).  Splits cost the
+// beside the next one's steps and bounds short reductions: 1.5 us and 1.3 us of a single tile, 11 us of a pair's (20 us in
+// fp32), which has one slot a warp and waits for each store (138936 x 24 -> 136 with two outputs: 98 us on pairs).  Splits cost the
 // write and read of their sums and, of products that need no second kernel otherwise, its launch.
-static double lt_cost(const LinTile &t, long long M, int N, long long steps, int splits) {
+static double lt_cost(const LinTile &t, long long M, int N, long long steps, int splits, bool f32) {
     const int bm = t.pair ? 256 : 128, sms = sm_count();
     const double units = (double)((M + bm - 1) / bm) * ((N + t.bn - 1) / t.bn) * splits;
-    const double step = t.bn == 64 ? 0.75 : 1.0, epilogue = t.pair ? 40 : t.bn == 128 ? 5.5 : 4.8;
+    const double step = t.bn == 64 ? 0.75 : 1.0, epilogue = t.pair ? (f32 ? 70 : 40) : t.bn == 128 ? 5.5 : 4.8;
     const double waves = std::ceil(units / (t.pair ? sms / 2 : sms));
     const double per = (double)((steps + splits - 1) / splits) * step;
     double c = (waves - 1) * std::max(per, epilogue) + per + epilogue + 4;
@@ -728,7 +706,7 @@ static double lt_cost(const LinTile &t, long long M, int N, long long steps, int
     return c;
 }
 
-LinSplit lin_tc_split(long long M, int N, long long K, int nseg) {
+LinSplit lin_tc_split(long long M, int N, long long K, int nseg, bool f32) {
     static const LinTile tiles[3] = {{true, 256}, {false, 128}, {false, 64}};
     const long long steps = std::max(1LL, (K + LT_BK - 1) / LT_BK);
     LinSplit best = {1, steps * LT_BK, tiles[2]};
@@ -743,7 +721,7 @@ LinSplit lin_tc_split(long long M, int N, long long K, int nseg) {
         for (int s = 1; s <= most; s += s < 8 ? 1 : s / 8) {
             const long long per = (steps + s - 1) / s;
             const int real = (int)((steps + per - 1) / per);
-            const double c = lt_cost(t, M, N, steps * nseg, real);
+            const double c = lt_cost(t, M, N, steps * nseg, real, f32);
             if (c < least) {
                 least = c;
                 best = {real, per * LT_BK, t};
@@ -763,7 +741,7 @@ static bool lt_encode(CUtensorMap (&m)[3], const bf16 *const (&base)[3], long lo
 // The maps of the outputs and the epilogue's inputs, a warp's piece at a time.
 template <typename TO>
 static bool lt_encode_out(LtMaps &m, const LinTile &t, const LinEpi<TO> &e, long long planes, long long M, int N) {
-    const int pc = std::min((t.pair ? 64 : 128) / (int)sizeof(TO), t.bn / 2);
+    const int pc = 64 / (int)sizeof(TO);
     auto enc = [&](CUtensorMap *x, const void *base) { return !base || fast::encode_3d(x, base, sizeof(TO) == 4, planes, M, N, pc, 32); };
     return enc(&m.out, e.out) && enc(&m.out2, e.out2) && enc(&m.add, e.add) && enc(&m.zin, e.zin);
 }

@@ -220,12 +220,12 @@ static LinPlan lin_plan(const eaga_linear_dims &d, bool back) {
         uint8_t seg[6];
         size_t acc = 0;
         if (!back) {
-            p.fwd = lin_tc_split(d.rows, d.out, d.in, f32 ? 6 : 1, f32);
+            p.fwd = lin_tc_split(d.rows, d.out, d.in, f32 ? 6 : 1);
             acc = p.fwd.splits > 1 ? p.fwd.splits * rows * out : 0;
         } else {
             const int z = std::max(1, p.zparts);
-            p.dx = lin_tc_split(d.rows, d.in, d.out, f32 ? 6 : std::min(z, 2), f32);
-            p.dw = lin_tc_split(d.in, d.out, d.rows, products(f32 ? 3 : 1, z, seg), false);
+            p.dx = lin_tc_split(d.rows, d.in, d.out, f32 ? 6 : std::min(z, 2));
+            p.dw = lin_tc_split(d.in, d.out, d.rows, products(f32 ? 3 : 1, z, seg));
             acc = std::max(p.dx.splits > 1 ? p.dx.splits * rows * in : 0, p.dw.splits > 1 ? p.dw.splits * in * out : 0);
             p.bparts = lin_db_parts(p.dw, d.in);
         }

@@ -168,8 +168,8 @@ struct LinTc {
     int *status;
     bool clear;                // this launch clears the status word
 };
-// Of a product [M, K] x [K, N]; f32: its epilogue reads and writes fp32 tensors.
-LinSplit lin_tc_split(long long M, int N, long long K, int nseg, bool f32);
+// Of a product [M, K] x [K, N].
+LinSplit lin_tc_split(long long M, int N, long long K, int nseg);
 // With one split the finished outputs; with more e.out takes the splits' sums [splits][M][N] in fp32, and nothing else of e is there.
 template <typename T>
 cudaError_t lin_tc_forward(const LinTc &p, const LinSplit &s, const LinEpi<T> &e, cudaStream_t st);

@@ -692,13 +692,13 @@ static cudaError_t lt_run(const LinTile &t, const LtMaps &m, const LtParams<TO> 
 // Tiles and splits: the least of an estimate of each form's time.  The unit is a 64-deep step of a pair's tile,
 // 0.28 us.  A step of the single tiles takes as long (128 columns) or 0.75 of it (64) for a half and a quarter of
 // a CTA's work: 32 and 24 KB from L2 bound them (measured 1.0e15 op/s, pairs 1.4e15).  A tile's epilogue runs
-// beside the next one's steps and bounds short reductions: 1.5 us and 1.3 us of a single tile, 11 us of a pair's (20 us in
-// fp32), which has one slot a warp and waits for each store (138936 x 24 -> 136 with two outputs: 98 us on pairs).  Splits cost the
+// beside the next one's steps and bounds short reductions: 1.5 us and 1.3 us of a single tile, 11 us of a pair's, which
+// has one slot a warp and waits for each store (138936 x 24 -> 136 with two outputs: 98 us on pairs).  Splits cost the
 // write and read of their sums and, of products that need no second kernel otherwise, its launch.
-static double lt_cost(const LinTile &t, long long M, int N, long long steps, int splits, bool f32) {
+static double lt_cost(const LinTile &t, long long M, int N, long long steps, int splits) {
     const int bm = t.pair ? 256 : 128, sms = sm_count();
     const double units = (double)((M + bm - 1) / bm) * ((N + t.bn - 1) / t.bn) * splits;
-    const double step = t.bn == 64 ? 0.75 : 1.0, epilogue = t.pair ? (f32 ? 70 : 40) : t.bn == 128 ? 5.5 : 4.8;
+    const double step = t.bn == 64 ? 0.75 : 1.0, epilogue = t.pair ? 40 : t.bn == 128 ? 5.5 : 4.8;
     const double waves = std::ceil(units / (t.pair ? sms / 2 : sms));
     const double per = (double)((steps + splits - 1) / splits) * step;
     double c = (waves - 1) * std::max(per, epilogue) + per + epilogue + 4;
@@ -706,7 +706,7 @@ static double lt_cost(const LinTile &t, long long M, int N, long long steps, int
     return c;
 }
 
-LinSplit lin_tc_split(long long M, int N, long long K, int nseg, bool f32) {
+LinSplit lin_tc_split(long long M, int N, long long K, int nseg) {
     static const LinTile tiles[3] = {{true, 256}, {false, 128}, {false, 64}};
     const long long steps = std::max(1LL, (K + LT_BK - 1) / LT_BK);
     LinSplit best = {1, steps * LT_BK, tiles[2]};
@@ -721,7 +721,7 @@ LinSplit lin_tc_split(long long M, int N, long long K, int nseg, bool f32) {
         for (int s = 1; s <= most; s += s < 8 ? 1 : s / 8) {
             const long long per = (steps + s - 1) / s;
             const int real = (int)((steps + per - 1) / per);
-            const double c = lt_cost(t, M, N, steps * nseg, real, f32);
+            const double c = lt_cost(t, M, N, steps * nseg, real);
             if (c < least) {
                 least = c;
                 best = {real, per * LT_BK, t};

@@ -50,6 +50,8 @@ struct Call {
         const void *p = b.buf;
         const Py_ssize_t len = b.len;
         PyBuffer_Release(&b);                        // the argument keeps the memory
+        // (a table of more entries than the library takes is refused there, unread)
+        if (count > (1 << 20)) count = 1;
         if (len < (Py_ssize_t)sizeof(T) * count) refuse("a structure of the library is required");
         return static_cast<const T *>(p);
     }

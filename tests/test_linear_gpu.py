@@ -332,3 +332,35 @@ def test_replayed_and_beside_another_stream():
     torch.cuda.synchronize()
     for k in keys:
         assert torch.equal(t[k], first[k]), k
+
+
+def test_refusals():
+    """What the binding and the entries refuse, before anything is launched; the outputs stay as they were."""
+    rows, i, o = 20, 24, 16
+    d = eaga.linear_dims(rows, i, o, "gelu", "bf16")
+    new = lambda *s, dtype=torch.bfloat16: torch.ones(*s, dtype=dtype, device="cuda")
+    X, W, b, R, Y, Z = new(rows, i), new(i, o), new(o), new(rows, o), new(rows, o), new(rows, o)
+    ws = torch.empty(eaga.linear_workspace_size(d, True), dtype=torch.uint8, device="cuda")
+    good = dict(X=X, W=W, b=b, R=R, Y=Y, Z=Z, ws=ws)
+
+    def call(**over):
+        a = {**good, **over}
+        eaga.linear_forward(d, a["X"], a["W"], a["b"], a["R"], a["Y"], a["Z"], a["ws"])
+
+    for k, bad in (("X", X.float()), ("W", W[:, :8]), ("W", W.T.contiguous().T), ("b", b[:8]), ("Y", Y.cpu()), ("Z", new(rows + 1, o)), ("X", None), ("Y", None),
+                   ("ws", None), ("ws", new(64, dtype=torch.float32)), ("X", [1, 2])):
+        with pytest.raises(ValueError):
+            call(**{k: bad})
+    for over, code in ((dict(Y=R), 1), (dict(Z=Y), 1), (dict(ws=ws[:64]), 4), (dict(X=new(rows * i + 8)[4:-4].view(rows, i)), 3)):
+        with pytest.raises(eaga.EagaError) as e:
+            call(**over)
+        assert e.value.code == code
+    dY, dX, dW, db = new(rows, o), new(rows, i), new(i, o, dtype=torch.float32), new(o, dtype=torch.float32)
+    with pytest.raises(eaga.EagaError):                   # gelu's backward needs Z
+        eaga.linear_backward(d, X, W, None, dY, dX, dW, db, ws)
+    with pytest.raises(ValueError):                       # weight gradients are fp32
+        eaga.linear_backward(d, X, W, Z, dY, dX, dW.bfloat16(), db, ws)
+    with pytest.raises(ValueError):
+        eaga.linear_backward(d, X, W, Z, dY, dX, dW, db, ws, act_in="tanh")
+    torch.cuda.synchronize()
+    assert (Y == 1).all() and (Z == 1).all() and (dX == 1).all() and (dW == 1).all()

@@ -168,3 +168,19 @@ def test_linear_pointers(L):
     assert linear_back(L, d, dX=OK + (6 << 28)) == 1                    # dX over dR
     with pytest.raises(ValueError):
         eaga.linear_dims(4, 8, 8, "tanh")
+
+
+def test_binding_refuses_host_tensors(L):
+    import torch
+    d, n = eaga.linear_dims(4, 8, 8), norm_dims()
+    host = torch.zeros(4, 8, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        eaga.linear_forward(d, host, None, None, None, None, None, None)
+    with pytest.raises(ValueError):
+        eaga.linear_forward(d, None, None, None, None, None, None, None)
+    with pytest.raises((ValueError, TypeError)):
+        eaga.linear_forward(None, host, None, None, None, None, None, None)
+    with pytest.raises(ValueError):
+        eaga.residual_norm_forward(n, None, host, None, None, None, None, None, None, None, None)
+    with pytest.raises(ValueError):
+        eaga.linear_forward(ctypes.c_int(4), host, None, None, None, None, None, None)      # too small for the dims

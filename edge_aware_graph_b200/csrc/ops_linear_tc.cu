@@ -62,7 +62,9 @@ typedef __nv_bfloat16 bf16;
 constexpr int LT_BM = 128, LT_BK = 64;
 constexpr int LT_PROMO = 8;                            // 64-deep steps an accumulator of an fp32 result takes
 
-template <int KIND, int BN, int CG, typename TO, bool VEC>
+// PER: CTAs an SM.  Two where reductions are short and tiles narrow and many: each waits for its loads and accumulators most of
+// the time (1M x 34 -> 48).
+template <int KIND, int BN, int CG, typename TO, bool VEC, int PER>
 struct Lt {
     static constexpr int BM = LT_BM * CG, PB = BN / CG;              // the tile's rows; B columns a CTA holds
     static constexpr bool PROMO = KIND == LIN_DW || sizeof(TO) == 4;
@@ -77,14 +79,14 @@ struct Lt {
     // Slots of a warp: the output's (in it the residual), two in turn where the epilogue is not hidden behind long
     // products anyway; one for Z or Zin.
     static constexpr int NIO = !VEC || (CG == 2 && KIND != LIN_DW) ? 1 : 2, SLOTS = !VEC || KIND == LIN_DW ? NIO : NIO + 1;
-    static constexpr uint32_t RING = 232448 - 1024 - 1024 - EPI * SLOTS * SLOT;
+    static constexpr uint32_t MOST = PER == 2 ? 115712 : 232448, RING = MOST - 1024 - 1024 - EPI * SLOTS * SLOT;
     static constexpr int ST = RING / STAGE < 8 ? RING / STAGE : 8;
     static constexpr uint32_t EPI_AT = ST * STAGE;
     static constexpr uint32_t BAR = EPI_AT + EPI * SLOTS * SLOT;     // full[ST], empty[ST], acc_full[2], acc_empty[2], drained, slots' [EPI][3]
     static constexpr uint32_t TM = BAR + (2 * ST + 5 + 3 * EPI) * 8;
     static constexpr uint32_t FAIL = TM + 4;
     static constexpr uint32_t BYTES = FAIL + 4 + 1024;
-    static_assert(ST >= 3 && BYTES <= 232448 && COLS % 32 == 0, "shared memory");
+    static_assert(ST >= (PER == 2 ? 2 : 3) && BYTES <= MOST && COLS % 32 == 0, "shared memory");
 };
 
 // A bounded wait that looks at the CTA's failure flag only where the barrier is not there yet.
@@ -115,10 +117,10 @@ struct LtParams {
     int ablocks, bblocks;      // an MN-major operand's map has blocks of 64 columns: one load a step
 };
 
-template <int KIND, int BN, int CG, typename TO, bool VEC>
-__global__ void __launch_bounds__(Lt<KIND, BN, CG, TO, VEC>::THR, 1)
+template <int KIND, int BN, int CG, typename TO, bool VEC, int PER>
+__global__ void __launch_bounds__(Lt<KIND, BN, CG, TO, VEC, PER>::THR, PER)
 k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<TO> p) {
-    using S = Lt<KIND, BN, CG, TO, VEC>;
+    using S = Lt<KIND, BN, CG, TO, VEC, PER>;
     constexpr int ST = S::ST, PC = S::PC, PIECES = S::PIECES;
     constexpr bool A_MN = KIND == LIN_DW, B_MN = KIND != LIN_DX, PAIR = CG == 2, PROMO = S::PROMO;
     constexpr bool SMEM_SUMS = KIND == LIN_DW && !PAIR;
@@ -674,18 +676,21 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
 
 // ------------------------------------------------------------------ host side
 
-template <int KIND, int BN, int CG, typename TO, bool VEC>
+template <int KIND, int BN, int CG, typename TO, bool VEC, int PER = 1>
 static cudaError_t lt_launch(const LtMaps &m, const LtParams<TO> &p, cudaStream_t st) {
-    using S = Lt<KIND, BN, CG, TO, VEC>;
-    auto kernel = k_lin_tc<KIND, BN, CG, TO, VEC>;
+    using S = Lt<KIND, BN, CG, TO, VEC, PER>;
+    auto kernel = k_lin_tc<KIND, BN, CG, TO, VEC, PER>;
     static std::atomic<uint32_t> attr_set{0};
     if (cudaError_t e = ensure_smem_attr(kernel, S::BYTES, attr_set); e != cudaSuccess) return e;
-    return launch_pdl(kernel, dim3((unsigned)(std::min(p.units, sm_count() / CG) * CG)), dim3(S::THR), S::BYTES, st, CG, m, p);
+    return launch_pdl(kernel, dim3((unsigned)(std::min(p.units, PER * sm_count() / CG) * CG)), dim3(S::THR), S::BYTES, st, CG, m, p);
 }
 template <int KIND, typename TO, bool VEC>
 static cudaError_t lt_run(const LinTile &t, const LtMaps &m, const LtParams<TO> &p, cudaStream_t st) {
     if (t.pair) return lt_launch<KIND, 256, 2, TO, VEC>(m, p, st);
     if (t.bn == 128) return lt_launch<KIND, 128, 1, TO, VEC>(m, p, st);
+    if constexpr (VEC && KIND != LIN_DW) {
+        if (p.units >= 4 * sm_count() && p.per * p.nseg <= 4) return lt_launch<KIND, 64, 1, TO, VEC, 2>(m, p, st);
+    }
     return lt_launch<KIND, 64, 1, TO, VEC>(m, p, st);
 }
 

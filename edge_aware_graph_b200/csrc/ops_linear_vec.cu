@@ -161,18 +161,17 @@ k_lin_vec_bwd(const LinVec<T> p, const LinEpi<T> e) {
     for (int c0 = 0; c0 < p.out; c0 += CC) {
         const int n = min(CC, p.out - c0);
         __syncthreads();
-        for (int q = tid; q < R * n; q += 256) {
-            const int r = q / n, c = q % n;
-            float d[1] = {0.f};
-            if (r < p.rows) {
+        for (int c = tid; c < n; c += 256) {         // a column of all rows: their loads are on their way together
+            float d[R], z[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
                 const size_t at = (size_t)r * p.out + c0 + c;
-                d[0] = ldf(p.dY + at);
-                if (p.Z) {
-                    const float z[1] = {ldf(p.Z + at)};
-                    act_slope_mul(d, z, p.act);
-                }
+                d[r] = r < p.rows ? ldf(p.dY + at) : 0.f;
+                z[r] = p.Z && r < p.rows ? ldf(p.Z + at) : 0.f;
             }
-            dz[r][c] = d[0];
+            if (p.Z) act_slope_mul(d, z, p.act);
+#pragma unroll
+            for (int r = 0; r < R; ++r) dz[r][c] = d[r];
         }
         __syncthreads();
         if (p.db && blockIdx.x == 0) {
@@ -186,7 +185,7 @@ k_lin_vec_bwd(const LinVec<T> p, const LinEpi<T> e) {
         if (on) {
             const T *w = p.W + (size_t)i * p.out + c0;
             float *o = p.dW ? p.dW + (size_t)i * p.out + c0 : nullptr;
-#pragma unroll 4
+#pragma unroll (VEC == 1 ? 8 : 4)
             for (int c = lane * VEC; c < n; c += 32 * VEC) {
                 float v[VEC], s[VEC];
                 if (p.dX) {

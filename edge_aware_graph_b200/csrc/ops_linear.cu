@@ -3,7 +3,7 @@
 //   Z = X W + b        Y = act(Z) + R
 //   dZ = act'(Z) dY    dX = act_in'(Zin) (dZ W^T) + dR    dW = X^T dZ    db = sum of dZ's rows
 //
-// Up to 8 rows run in ops_linear_vec.cu, bound by the read of W; more on the
+// A few rows run in ops_linear_vec.cu, bound by the read of W; more on the
 // tensor cores (ops_linear_tc.cu).  Those read bf16 operands by TMA, whose rows
 // begin on 16 bytes.  What is not so is prepared once in the workspace, by one
 // kernel for all operands: rows of another length are copied into padded ones;
@@ -199,7 +199,7 @@ static int products(int aparts, int bparts, uint8_t (&seg)[6]) {
 
 static LinPlan lin_plan(const eaga_linear_dims &d, bool back) {
     LinPlan p = {};
-    p.vec = d.rows <= LIN_VEC_ROWS;
+    p.vec = lin_few_rows(d, back);
     size_t off = 256;                                // the status word
     auto take = [&](size_t bytes) {
         const size_t at = off;

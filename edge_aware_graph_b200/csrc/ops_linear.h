@@ -179,8 +179,16 @@ cudaError_t lin_tc_dx(const LinTc &p, const LinSplit &s, const LinEpi<T> &e, cud
 inline int lin_db_parts(const LinSplit &s, int in) { return s.splits * (s.tile.pair ? (in + 255) / 256 : 1); }
 cudaError_t lin_tc_dw(const LinTc &p, const LinSplit &s, float *dW, float *db, cudaStream_t st);
 
-// Up to LIN_VEC_ROWS rows: the weights are read once, bound by memory.
-constexpr int LIN_VEC_ROWS = 8;
+// Few rows: the weights are read once, bound by memory (at most 8 rows in bf16, 16 in fp32).  Above four rows in bf16 the tensor
+// cores' launch is the shorter one (8 x 4096 -> 4096: 12.8 us against 22.6 forward, 30 against 75 backward; at one row 13.4
+// against 7.6 and 30 against 26), but for rows that they need copied (8 x 1000 -> 1001: 10.2 against 8.4 and 14 against 8.7) and
+// gradients of small weights (8 x 512 -> 512: 9.7 against 5.8).  fp32 products take six of the tensor cores' and three copies
+// (8 x 4096 -> 4096: 75 us against 29).
+inline bool lin_few_rows(const eaga_linear_dims &d, bool back) {
+    if (d.dtype == EAGA_FP32) return d.rows <= 16;
+    if (d.rows <= 4) return true;
+    return d.rows <= 8 && (d.in % 8 || d.out % 8 || (back && (long long)d.in * d.out <= 1 << 18));
+}
 template <typename T>
 struct LinVec {
     int rows, in, out;

@@ -1,5 +1,5 @@
-// The linear operator for up to eight rows (serving: one token, one graph's
-// global features).  Bound: the read of W, and in the backward the write of dW;
+// The linear operator for a few rows (serving: one token, one graph's global
+// features; lin_few_rows() says how many).  Bound: the read of W, and in the backward the write of dW;
 // there is nothing for the tensor cores to do, so each weight goes from memory
 // to registers once and is multiplied by all rows there.
 //
@@ -41,7 +41,7 @@ struct VecIo {
     }
 };
 
-constexpr int LV_CHUNK = 512;      // rows of W whose X is in shared memory at once
+template <int R> constexpr int lv_chunk() { return R > 8 ? 256 : 512; }      // rows of W whose X is in shared memory at once
 constexpr int LV_BATCH = 8;        // loads a thread has in flight
 
 // R: rows (the call's, rounded up).  part: rows of W a CTA takes.
@@ -50,6 +50,7 @@ __global__ void __launch_bounds__(256)
 k_lin_vec_fwd(const LinVec<T> p, const LinEpi<T> e, int part, int cluster) {
     after_previous();
     constexpr int LANES = VEC == 1 ? 32 : 8, C = LANES * VEC, KR = 256 / LANES;
+    constexpr int LV_CHUNK = lv_chunk<R>();
     __shared__ float xs[R][LV_CHUNK];
     __shared__ float red[8][R][C];
     __shared__ float sum[R][C];
@@ -259,6 +260,9 @@ static cudaError_t vec_pick(int rows, int out, F &&f) {
         if (rows <= 1) return f(vec, std::integral_constant<int, 1>{});
         if (rows <= 2) return f(vec, std::integral_constant<int, 2>{});
         if (rows <= 4) return f(vec, std::integral_constant<int, 4>{});
+        if constexpr (sizeof(T) == 4) {
+            if (rows > 8) return f(vec, std::integral_constant<int, 16>{});
+        }
         return f(vec, std::integral_constant<int, 8>{});
     };
     return out % W == 0 ? go(std::integral_constant<int, W>{}) : go(std::integral_constant<int, 1>{});

@@ -5,7 +5,8 @@
 //
 // A few rows run in ops_linear_vec.cu, bound by the read of W; more on the
 // tensor cores (ops_linear_tc.cu).  Those read bf16 operands by TMA, whose rows
-// begin on 16 bytes.  What is not so is prepared once in the workspace, by one
+// begin on 16 bytes (narrow fp32 products stay on the
+// CUDA cores, ops_linear_f32.cu).  What is not so is prepared once in the workspace, by one
 // kernel for all operands: rows of another length are copied into padded ones;
 // fp32 values (operands in fp32, and dZ where act is not none) become three bf16
 // parts that carry their 24 bits between them.  An fp32 result takes the products
@@ -22,6 +23,7 @@ namespace ops {
 struct PrepJob {
     const void *src, *z;
     void *dst[3];
+    float *f32;                // or this: fp32 [rows][n]
     long long rows;
     int n, ld, act, parts;
 };
@@ -92,6 +94,7 @@ __global__ void __launch_bounds__(256) k_lin_prep(const __grid_constant__ PrepAr
             flat_ld8(zs, row * j.n + c, all, have, z);
             act_slope_mul(v, z, j.act);
         }
+        if (j.f32) lin_st8(j.f32 + row * j.n + c, have, j.n % 4 == 0, v);
         for (int k = 0; k < j.parts; ++k) {
             float o[8];
 #pragma unroll
@@ -180,12 +183,12 @@ k_lin_reduce(const float *acc, float *dW, long long n, int splits, const float *
 static int round8(int n) { return (n + 7) / 8 * 8; }
 
 struct LinPlan {
-    bool vec;
+    bool vec, cores;                   // few rows; fp32 on the CUDA cores
     int xparts, wparts, zparts;        // parts in the workspace; 0: the caller's tensor is read as it is
     int ldx, ldw, ldz;
     LinSplit fwd, dx, dw;
     int bparts;                        // of the bias gradient
-    size_t X[3], W[3], dZ[3], acc, bacc, total;      // workspace offsets
+    size_t X[3], W[3], dZ[3], dZ32, acc, bacc, total;      // workspace offsets
 };
 
 // The products of parts of an fp32 or a bf16 result: A's parts times B's, without those below 2^-24.
@@ -197,6 +200,29 @@ static int products(int aparts, int bparts, uint8_t (&seg)[6]) {
     return n;
 }
 
+// Whether an fp32 call runs on the CUDA cores: by estimates of both, in us.  Those reach 25 TFLOP/s on tiles of 32 columns (0.6 us
+// for 16 steps of the reduction at the least); the tensor cores' operands are first copied into parts, 10 bytes an element.
+// 1033088 x 8 -> 8 took 466 us on the tensor cores.
+static double cores_us(long long M, int N, long long K) {
+    const double n = (N + 31) / 32 * 32, flops = 2.0 * M * n * K, bytes = 4.0 * ((double)M * K + 2.0 * (double)M * N + (double)K * N);
+    return std::max({flops / 25e6, bytes / 4.5e6, K / 16 * 0.6}) + 3;
+}
+static bool lin_cores(const eaga_linear_dims &d, bool back) {
+    const double x = (double)d.rows * d.in, w = (double)d.in * d.out, z = (double)d.rows * d.out;
+    double tc = 0, us = 0;
+    if (!back) {
+        lin_tc_split(d.rows, d.out, d.in, 6, true, &us);
+        return cores_us(d.rows, d.out, d.in) < us + 10 * (x + w) / 5e6 + 3;
+    }
+    lin_tc_split(d.rows, d.in, d.out, 6, true, &us);
+    tc = us;
+    lin_tc_split(d.in, d.out, d.rows, 6, false, &us);
+    tc += us + 10 * (x + w + z) / 5e6 + 3;
+    // dW: splits of the rows, none shorter than 256
+    const double dw = std::max(2.0 * d.rows * ((d.in + 31) / 32 * 32) * ((d.out + 31) / 32 * 32) / 25e6, 4 * (x + z) / 4.5e6) + 13;
+    return cores_us(d.rows, d.in, d.out) + dw < tc;
+}
+
 static LinPlan lin_plan(const eaga_linear_dims &d, bool back) {
     LinPlan p = {};
     p.vec = lin_few_rows(d, back);
@@ -206,7 +232,18 @@ static LinPlan lin_plan(const eaga_linear_dims &d, bool back) {
         off = align256(off + bytes);
         return at;
     };
-    if (!p.vec) {
+    if (!p.vec && d.dtype == EAGA_FP32 && lin_cores(d, back)) {
+        p.cores = true;
+        if (back) {
+            if (d.act != EAGA_ACT_NONE) p.dZ32 = take((size_t)d.rows * d.out * 4);
+            p.dw = lin_f32_dw_split(d.rows, d.in, d.out);
+            p.bparts = p.dw.splits;
+            if (p.dw.splits > 1) {
+                p.acc = take((size_t)p.dw.splits * d.in * d.out * 4);
+                p.bacc = take((size_t)p.dw.splits * d.out * 4);
+            }
+        }
+    } else if (!p.vec) {
         const size_t rows = (size_t)d.rows, in = d.in, out = d.out;
         const bool f32 = d.dtype == EAGA_FP32, dact = back && d.act != EAGA_ACT_NONE;
         p.ldx = round8(d.in);
@@ -220,12 +257,12 @@ static LinPlan lin_plan(const eaga_linear_dims &d, bool back) {
         uint8_t seg[6];
         size_t acc = 0;
         if (!back) {
-            p.fwd = lin_tc_split(d.rows, d.out, d.in, f32 ? 6 : 1);
+            p.fwd = lin_tc_split(d.rows, d.out, d.in, f32 ? 6 : 1, f32);
             acc = p.fwd.splits > 1 ? p.fwd.splits * rows * out : 0;
         } else {
             const int z = std::max(1, p.zparts);
-            p.dx = lin_tc_split(d.rows, d.in, d.out, f32 ? 6 : std::min(z, 2));
-            p.dw = lin_tc_split(d.in, d.out, d.rows, products(f32 ? 3 : 1, z, seg));
+            p.dx = lin_tc_split(d.rows, d.in, d.out, f32 ? 6 : std::min(z, 2), f32);
+            p.dw = lin_tc_split(d.in, d.out, d.rows, products(f32 ? 3 : 1, z, seg), false);
             acc = std::max(p.dx.splits > 1 ? p.dx.splits * rows * in : 0, p.dw.splits > 1 ? p.dw.splits * in * out : 0);
             p.bparts = lin_db_parts(p.dw, d.in);
         }
@@ -291,7 +328,7 @@ static void lin_operand(const __nv_bfloat16 *(&part)[3], const void *src, const 
                         const size_t (&at)[3], char *ws, PrepJob *jobs, int &count) {
     part[0] = static_cast<const __nv_bfloat16 *>(src);
     if (!parts) return;
-    PrepJob j = {src, z, {}, rows, n, ld, act, parts};
+    PrepJob j = {src, z, {}, nullptr, rows, n, ld, act, parts};
     for (int k = 0; k < parts; ++k) {
         j.dst[k] = ws + at[k];
         part[k] = reinterpret_cast<const __nv_bfloat16 *>(ws + at[k]);
@@ -361,6 +398,32 @@ static cudaError_t backward_tc(const eaga_linear_dims &d, const LinPlan &p, cons
     return cudaSuccess;
 }
 
+static cudaError_t forward_cores(const eaga_linear_dims &d, const void *X, const void *W, const LinEpi<float> &e, char *ws, cudaStream_t st) {
+    const LinF32 q = {d.rows, d.in, d.out, static_cast<const float *>(X), static_cast<const float *>(W), nullptr, reinterpret_cast<int *>(ws)};
+    return lin_f32_forward(q, e, st);
+}
+static cudaError_t backward_cores(const eaga_linear_dims &d, const LinPlan &p, const LinBack &b, cudaStream_t st) {
+    LinF32 q = {d.rows, d.in, d.out, static_cast<const float *>(b.X), static_cast<const float *>(b.W), static_cast<const float *>(b.dY),
+                reinterpret_cast<int *>(b.ws)};
+    if (p.dZ32) {
+        float *dz = reinterpret_cast<float *>(b.ws + p.dZ32);
+        const PrepJob j = {b.dY, b.Z, {}, dz, d.rows, d.out, round8(d.out), d.act, 0};
+        if (cudaError_t e = lin_prep<float>(&j, 1, st); e != cudaSuccess) return e;
+        q.dZ = dz;
+    }
+    if (b.dX) {
+        const LinEpi<float> e = {nullptr, static_cast<const float *>(b.dR), static_cast<const float *>(b.Zin), static_cast<float *>(b.dX), nullptr, b.act_in};
+        if (cudaError_t err = lin_f32_dx(q, e, st); err != cudaSuccess) return err;
+    }
+    if (b.dW) {
+        float *acc = p.dw.splits > 1 ? reinterpret_cast<float *>(b.ws + p.acc) : b.dW;
+        float *bacc = !b.db ? nullptr : p.bparts > 1 ? reinterpret_cast<float *>(b.ws + p.bacc) : b.db;
+        if (cudaError_t err = lin_f32_dw(q, p.dw, acc, bacc, st); err != cudaSuccess) return err;
+        return lin_reduce((long long)d.in * d.out, p.dw.splits, acc, b.dW, d.out, p.bparts, bacc, b.db, st);
+    }
+    return cudaSuccess;
+}
+
 template <typename T>
 static cudaError_t backward_vec(const eaga_linear_dims &d, const LinBack &b, cudaStream_t st) {
     const LinVec<T> q = {(int)d.rows, d.in, d.out, static_cast<const T *>(b.X), static_cast<const T *>(b.W), static_cast<const T *>(b.dY),
@@ -419,7 +482,8 @@ eaga_status eaga_linear_forward(const eaga_linear_dims *d, const void *X, const 
         e = p.vec ? forward_vec(*d, X, W, epi, workspace, st) : forward_tc(*d, p, X, W, epi, ws, st);
     } else {
         const LinEpi<float> epi = forward_epi<float>(*d, b, R, Y, Z);
-        e = p.vec ? forward_vec(*d, X, W, epi, workspace, st) : forward_tc(*d, p, X, W, epi, ws, st);
+        e = p.vec ? forward_vec(*d, X, W, epi, workspace, st)
+                  : p.cores ? forward_cores(*d, X, W, epi, ws, st) : forward_tc(*d, p, X, W, epi, ws, st);
     }
     return e == cudaSuccess ? EAGA_OK : EAGA_ERR_CUDA;
 }
@@ -456,7 +520,7 @@ eaga_status eaga_linear_backward(const eaga_linear_dims *d, const void *X, const
     }
     const LinBack b = {X, W, Z, dY, act_in, Zin, dR, dX, dW, db, static_cast<char *>(workspace)};
     if (d->dtype == EAGA_BF16) e = p.vec ? backward_vec<__nv_bfloat16>(*d, b, st) : backward_tc<__nv_bfloat16>(*d, p, b, st);
-    else e = p.vec ? backward_vec<float>(*d, b, st) : backward_tc<float>(*d, p, b, st);
+    else e = p.vec ? backward_vec<float>(*d, b, st) : p.cores ? backward_cores(*d, p, b, st) : backward_tc<float>(*d, p, b, st);
     return e == cudaSuccess ? EAGA_OK : EAGA_ERR_CUDA;
 }
 

@@ -168,8 +168,8 @@ struct LinTc {
     int *status;
     bool clear;                // this launch clears the status word
 };
-// Of a product [M, K] x [K, N].
-LinSplit lin_tc_split(long long M, int N, long long K, int nseg);
+// Of a product [M, K] x [K, N]; f32: of fp32 operands and tensors in the epilogue.  us: the estimated time, where not null.
+LinSplit lin_tc_split(long long M, int N, long long K, int nseg, bool f32, double *us = nullptr);
 // With one split the finished outputs; with more e.out takes the splits' sums [splits][M][N] in fp32, and nothing else of e is there.
 template <typename T>
 cudaError_t lin_tc_forward(const LinTc &p, const LinSplit &s, const LinEpi<T> &e, cudaStream_t st);
@@ -178,6 +178,18 @@ cudaError_t lin_tc_dx(const LinTc &p, const LinSplit &s, const LinEpi<T> &e, cud
 // dW likewise; and where db is not null the column sums in lin_db_parts() parts [parts][out].
 inline int lin_db_parts(const LinSplit &s, int in) { return s.splits * (s.tile.pair ? (in + 255) / 256 : 1); }
 cudaError_t lin_tc_dw(const LinTc &p, const LinSplit &s, float *dW, float *db, cudaStream_t st);
+
+// CUDA-core products of fp32 operands of any size; partial sums [splits][in][out] (and [splits][out]) where splits > 1.
+struct LinF32 {
+    long long rows;
+    int in, out;
+    const float *X, *W, *dZ;
+    int *status;               // cleared
+};
+cudaError_t lin_f32_forward(const LinF32 &p, const LinEpi<float> &e, cudaStream_t st);
+cudaError_t lin_f32_dx(const LinF32 &p, const LinEpi<float> &e, cudaStream_t st);
+LinSplit lin_f32_dw_split(long long rows, int in, int out);
+cudaError_t lin_f32_dw(const LinF32 &p, const LinSplit &s, float *dW, float *db, cudaStream_t st);
 
 // Few rows: the weights are read once, bound by memory (at most 8 rows in bf16, 16 in fp32).  Above four rows in bf16 the tensor
 // cores' launch is the shorter one (8 x 4096 -> 4096: 12.8 us against 22.6 forward, 30 against 75 backward; at one row 13.4

@@ -698,12 +698,14 @@ static cudaError_t lt_run(const LinTile &t, const LtMaps &m, const LtParams<TO> 
 // 0.28 us.  A step of the single tiles takes as long (128 columns) or 0.75 of it (64) for a half and a quarter of
 // a CTA's work: 32 and 24 KB from L2 bound them (measured 1.0e15 op/s, pairs 1.4e15).  A tile's epilogue runs
 // beside the next one's steps and bounds short reductions: 1.5 us and 1.3 us of a single tile, 11 us of a pair's, which
-// has one slot a warp and waits for each store (138936 x 24 -> 136 with two outputs: 98 us on pairs).  Splits cost the
+// has one slot a warp and waits for each store (138936 x 24 -> 136 with two outputs: 98 us on pairs).  fp32 tensors take 4 us of a
+// 128-wide tile, 7 us where their rows are not 16 bytes (94180 x 31 -> 520, 102998 x 431 <- 32).  Splits cost the
 // write and read of their sums and, of products that need no second kernel otherwise, its launch.
-static double lt_cost(const LinTile &t, long long M, int N, long long steps, int splits) {
+static double lt_cost(const LinTile &t, long long M, int N, long long steps, int splits, bool f32) {
     const int bm = t.pair ? 256 : 128, sms = sm_count();
     const double units = (double)((M + bm - 1) / bm) * ((N + t.bn - 1) / t.bn) * splits;
-    const double step = t.bn == 64 ? 0.75 : 1.0, epilogue = t.pair ? 40 : t.bn == 128 ? 5.5 : 4.8;
+    const double step = t.bn == 64 ? 0.75 : 1.0, wide = !f32 ? 1 : N % 4 ? 4.5 : 2.7;
+    const double epilogue = t.pair ? 40 : wide * (t.bn == 128 ? 5.5 : 4.8);
     const double waves = std::ceil(units / (t.pair ? sms / 2 : sms));
     const double per = (double)((steps + splits - 1) / splits) * step;
     double c = (waves - 1) * std::max(per, epilogue) + per + epilogue + 4;
@@ -711,7 +713,7 @@ static double lt_cost(const LinTile &t, long long M, int N, long long steps, int
     return c;
 }
 
-LinSplit lin_tc_split(long long M, int N, long long K, int nseg) {
+LinSplit lin_tc_split(long long M, int N, long long K, int nseg, bool f32, double *us) {
     static const LinTile tiles[3] = {{true, 256}, {false, 128}, {false, 64}};
     const long long steps = std::max(1LL, (K + LT_BK - 1) / LT_BK);
     LinSplit best = {1, steps * LT_BK, tiles[2]};
@@ -726,13 +728,14 @@ LinSplit lin_tc_split(long long M, int N, long long K, int nseg) {
         for (int s = 1; s <= most; s += s < 8 ? 1 : s / 8) {
             const long long per = (steps + s - 1) / s;
             const int real = (int)((steps + per - 1) / per);
-            const double c = lt_cost(t, M, N, steps * nseg, real);
+            const double c = lt_cost(t, M, N, steps * nseg, real, f32);
             if (c < least) {
                 least = c;
                 best = {real, per * LT_BK, t};
             }
         }
     }
+    if (us) *us = 0.28 * least;
     return best;
 }
 

@@ -200,12 +200,12 @@ static int products(int aparts, int bparts, uint8_t (&seg)[6]) {
     return n;
 }
 
-// Whether an fp32 call runs on the CUDA cores: by estimates of both, in us.  Those reach 25 TFLOP/s on tiles of 32 columns (0.6 us
-// for 16 steps of the reduction at the least); the tensor cores' operands are first copied into parts, 10 bytes an element.
+// Whether an fp32 call runs on the CUDA cores: by estimates of both, in us.  Those reach 22 TFLOP/s on wide
+// results, 12 on tiles of 16 or 32 columns, 15 in narrow weight gradients (0.7 us for 16 steps of the reduction at the least); the tensor cores' operands are first copied into parts, 10 bytes an element.
 // 1033088 x 8 -> 8 took 466 us on the tensor cores.
 static double cores_us(long long M, int N, long long K) {
-    const double n = (N + 31) / 32 * 32, flops = 2.0 * M * n * K, bytes = 4.0 * ((double)M * K + 2.0 * (double)M * N + (double)K * N);
-    return std::max({flops / 25e6, bytes / 4.5e6, K / 16 * 0.6}) + 3;
+    const double n = N <= 16 ? 16 : (N + 31) / 32 * 32, flops = 2.0 * M * n * K, bytes = 4.0 * ((double)M * K + 2.0 * (double)M * N + (double)K * N);
+    return std::max({flops / (N <= 32 ? 12e6 : 22e6), bytes / 4.5e6, K / 16 * 0.7}) + 4;
 }
 static bool lin_cores(const eaga_linear_dims &d, bool back) {
     const double x = (double)d.rows * d.in, w = (double)d.in * d.out, z = (double)d.rows * d.out;
@@ -217,9 +217,10 @@ static bool lin_cores(const eaga_linear_dims &d, bool back) {
     lin_tc_split(d.rows, d.in, d.out, 6, true, &us);
     tc = us;
     lin_tc_split(d.in, d.out, d.rows, 6, false, &us);
+    if (d.out <= 32) us *= 2.5;                      // rows of dZ of a few bytes load as slowly as long ones (300000 x 100 <- 8)
     tc += us + 10 * (x + w + z) / 5e6 + 3;
     // dW: splits of the rows, none shorter than 256
-    const double dw = std::max(2.0 * d.rows * ((d.in + 31) / 32 * 32) * ((d.out + 31) / 32 * 32) / 25e6, 4 * (x + z) / 4.5e6) + 13;
+    const double dw = std::max(2.0 * d.rows * ((d.in + 31) / 32 * 32) * ((d.out + 31) / 32 * 32) / (d.in <= 32 || d.out <= 32 ? 15e6 : 22e6), 4 * (x + z) / 4.5e6) + 13;
     return cores_us(d.rows, d.in, d.out) + dw < tc;
 }
 

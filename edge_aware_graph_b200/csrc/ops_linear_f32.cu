@@ -3,9 +3,8 @@
 //
 //   forward   Y  = f(X W)      dX  dX = f(dZ W^T)      dW  dW = X^T dZ
 //
-// A CTA of 256 threads takes a BT x BT tile (BT = 64, or 32 where that leaves
-// SMs without one), 16 steps of the reduction at a time through two shared
-// buffers, a thread (BT/16)^2 sums.  Bound: fp32 multiply-adds, at the sizes
+// A CTA of 256 threads takes a BM x BN tile, 16 steps of the reduction at a time
+// through two shared buffers, a thread BM/16 x BN/16 sums.  Bound: fp32 multiply-adds, at the sizes
 // it is used for their latency.  The bias gradient is summed from the dZ tiles
 // of the first row of dW's tiles.
 #include <algorithm>
@@ -208,7 +207,7 @@ __global__ void __launch_bounds__(256) k_lin_thin_dw(const LtThin p) {
 }
 static bool lf_thin(int in, int out) { return in <= 32 && out <= 32 && ((in + 7) / 8) * ((out + 7) / 8) <= 8; }
 
-// Tiles of 64 x 64; narrow results of many rows 128 x 32; 32 x 32 where others leave SMs without one.
+// Tiles of 64 x 64; narrow results of many rows 128 x 16 or 128 x 32; 32 x 32 where others leave SMs without one.
 template <int KIND>
 static cudaError_t lf_launch(const LfParams &p, int splits, cudaStream_t st) {
     auto tiles = [&](int bm, int bn) { return ((long long)p.M + bm - 1) / bm * ((p.N + bn - 1) / bn); };
@@ -218,6 +217,7 @@ static cudaError_t lf_launch(const LfParams &p, int splits, cudaStream_t st) {
         return launch_pdl(kernel, dim3((unsigned)n, splits), dim3(256), 0, st, 1, p);
     };
     if constexpr (KIND != LIN_DW) {
+        if (p.N <= 16 && tiles(128, 16) >= 2 * sm_count()) return go(k_lin_f32<KIND, 128, 16>, 128, 16);
         if (p.N <= 32 && tiles(128, 32) >= 2 * sm_count()) return go(k_lin_f32<KIND, 128, 32>, 128, 32);
     }
     if (p.N > 32 && p.M > 32 && tiles(64, 64) * splits >= sm_count()) return go(k_lin_f32<KIND, 64, 64>, 64, 64);

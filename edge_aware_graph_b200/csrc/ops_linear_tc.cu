@@ -720,11 +720,11 @@ LinSplit lin_tc_split(long long M, int N, long long K, int nseg, bool f32, doubl
     double least = 1e300;
     for (const LinTile &t : tiles) {
         if (t.pair ? M <= 128 || N <= 128 : t.bn == 128 && N <= 64) continue;
-        // splits of four steps or more, while they are not more than two units an SM; of the many, every eighth or so
+        // splits of four steps or more, while they are not more than four units an SM; of the many, every eighth or so
         // (this runs on the host in every call)
         const int bm = t.pair ? 256 : 128;
         const long long units = (M + bm - 1) / bm * ((N + t.bn - 1) / t.bn);
-        const int most = (int)std::max(1LL, std::min(steps * nseg / 4, std::min(steps, 2LL * sm_count() / units)));
+        const int most = (int)std::max(1LL, std::min(steps * nseg / 4, std::min(steps, 4LL * sm_count() / units)));
         for (int s = 1; s <= most; s += s < 8 ? 1 : s / 8) {
             const long long per = (steps + s - 1) / s;
             const int real = (int)((steps + per - 1) / per);

@@ -388,7 +388,7 @@ EAGA_API eaga_status eaga_block_backward(const eaga_dims *dims,
  * act_in is none), dR, one of dX and dW, db (given only with dW).  Outputs are
  * overwritten.  All sums run in an order that the dims fix.
  *
- * In fp32 the products run on the tensor cores over three bf16 parts of each
+ * In fp32 all but narrow products run on the tensor cores over three bf16 parts of each
  * operand (24 bits, down to 2^-133), the error that of fp32 sums.  An infinite
  * operand there, or one whose product with a part overflows, gives NaN where an
  * fp32 product might give an infinity; finite rows are not touched by it.

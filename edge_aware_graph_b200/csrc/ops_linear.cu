@@ -201,17 +201,20 @@ static int products(int aparts, int bparts, uint8_t (&seg)[6]) {
 }
 
 // Whether an fp32 call runs on the CUDA cores: by estimates of both, in us.  Those reach 22 TFLOP/s on wide
-// results, 12 on tiles of 16 or 32 columns, 15 in narrow weight gradients (0.7 us for 16 steps of the reduction at the least); the tensor cores' operands are first copied into parts, 10 bytes an element.
+// results, 13 and 17 on tiles of 16 and 32 columns, 15 in narrow weight gradients (0.7 us for 16 steps of the reduction at the least); the tensor cores' operands are first copied into parts, 10 bytes an element.
 // 1033088 x 8 -> 8 took 466 us on the tensor cores.
 static double cores_us(long long M, int N, long long K) {
+    if (lin_narrow(M, N, K))                         // by warps: 8 us for 2500 steps at the least
+        return std::max(2.0 * M * ((N + 7) / 8 * 8) * (K + 80) / 17e6, K * 0.0035) + 4;
     const double n = N <= 16 ? 16 : (N + 31) / 32 * 32, flops = 2.0 * M * n * K, bytes = 4.0 * ((double)M * K + 2.0 * (double)M * N + (double)K * N);
-    return std::max({flops / (N <= 32 ? 12e6 : 22e6), bytes / 4.5e6, K / 16 * 0.7}) + 4;
+    return std::max({flops / lin_tile_rate(N), bytes / 4.5e6, K / 16 * 0.7}) + 4;
 }
 static bool lin_cores(const eaga_linear_dims &d, bool back) {
     const double x = (double)d.rows * d.in, w = (double)d.in * d.out, z = (double)d.rows * d.out;
     double tc = 0, us = 0;
     if (!back) {
         lin_tc_split(d.rows, d.out, d.in, 6, true, &us);
+        if (d.out <= 32) us *= 2;                    // lines of Y of 128 bytes or less: 200000 x 64 -> 24 91 us without the copies, 84 by warps
         return cores_us(d.rows, d.out, d.in) < us + 10 * (x + w) / 5e6 + 3;
     }
     lin_tc_split(d.rows, d.in, d.out, 6, true, &us);

@@ -186,6 +186,14 @@ struct LinF32 {
     const float *X, *W, *dZ;
     int *status;               // cleared
 };
+// Whether an fp32 product of M x N over K runs by warps, which take columns in eights at 17 TFLOP/s and whose join is as long as
+// 80 steps, or in tiles of 16 columns at 13 or of 32 at 17, which want four CTAs of 128 rows an SM (300000 x 100 -> 8 67 us
+// against 82, 1000000 x 70 -> 9 343 against 196, 20000 x 128 -> 16 8.7 against 14.8).
+inline double lin_tile_rate(int N) { return N <= 16 ? 13e6 : N <= 32 ? 17e6 : 22e6; }        // multiply-adds as two, a us
+inline bool lin_narrow(long long M, int N, long long K) {
+    if (N > 32 || K < 64) return false;
+    return M < 512LL * sm_count() || (N + 7) / 8 * 8 * (K + 80) / 17e6 < (N <= 16 ? 16 : 32) * K / lin_tile_rate(N);
+}
 cudaError_t lin_f32_forward(const LinF32 &p, const LinEpi<float> &e, cudaStream_t st);
 cudaError_t lin_f32_dx(const LinF32 &p, const LinEpi<float> &e, cudaStream_t st);
 LinSplit lin_f32_dw_split(long long rows, int in, int out);

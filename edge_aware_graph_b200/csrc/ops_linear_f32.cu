@@ -141,6 +141,98 @@ k_lin_f32(const LfParams p) {
 
 // ------------------------------------------------------------------ host side
 
+// Narrow results (up to 32 columns) of long reductions: a warp takes four rows and eight columns, a lane every 32nd step of the
+// reduction, so A is read in whole lines and a weight from shared memory serves four rows; the lanes' 32 sums are joined at
+// the end, halving them with every exchange until a lane has one element.  (Tiles of 128 x 16 leave most threads' columns
+// empty and take the reduction in one place.)  Weights of up to 1024 steps stay while a CTA goes through its rows.
+// 60000 x 512 -> 8 33 us (3.7 TB/s; tensor cores, their copies included, 89), 6580 x 2576 -> 17 49 (86), 40000 x 1500 -> 10 125 (192):
+// multiply-adds are at a fifth of their rate and DRAM at half, so the loads' latency bounds it, at 24 or 32 warps an SM.
+constexpr int LN_K = 1024;     // steps whose weights are in shared memory at once
+constexpr int LN_R = 4;        // rows of a warp
+// U: steps whose loads are in flight.  Four leave registers for three CTAs an SM, two for four, which short reductions, of a
+// few steps and the join, want: 300000 x 100 -> 8 67 us against 81, 60000 x 512 -> 8 37 against 33.5.
+template <int KIND, int U>
+__global__ void __launch_bounds__(256, U == 2 ? 4 : 3)
+k_lin_narrow(const LfParams p) {
+    after_previous();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
+    __shared__ __align__(16) float ws[LN_K][12];     // eight lanes' rows, read as two float4, lie in different banks
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const unsigned blocks = (p.N + 7) / 8;           // of columns, fastest
+    const int n0 = blockIdx.x % blocks * 8, step = gridDim.x / blocks * 8 * LN_R;
+    auto weights = [&](long long k0, int n) {
+        if (KIND == LIN_DX) {
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c)              // a row of W at a time, as it lies in memory
+                for (int k = threadIdx.x; k < n; k += 256)
+                    ws[k][c] = n0 + c < p.N ? p.B[(size_t)(n0 + c) * p.ldb + k0 + k] : 0.f;
+        } else {
+#pragma unroll 4
+            for (int q = threadIdx.x; q < n * 8; q += 256)
+                ws[q / 8][q % 8] = n0 + q % 8 < p.N ? p.B[(size_t)(k0 + q / 8) * p.ldb + n0 + q % 8] : 0.f;
+        }
+    };
+    const bool once = p.K <= LN_K;                   // the weights stay for all of the CTA's rows
+    if (once) {
+        weights(0, (int)p.K);
+        __syncthreads();
+    }
+    for (long long row = (long long)(blockIdx.x / blocks) * (8 * LN_R); row < p.M; row += step) {
+        const long long row0 = row + warp * LN_R;
+        const float *A[LN_R];
+#pragma unroll
+        for (int r = 0; r < LN_R; ++r) A[r] = p.A + (size_t)(row0 + r < p.M ? row0 + r : 0) * p.lda;     // past the end row 0, not stored
+        float a[8 * LN_R];
+#pragma unroll
+        for (int i = 0; i < 8 * LN_R; ++i) a[i] = 0.f;
+        for (long long k0 = 0; k0 < p.K; k0 += LN_K) {
+            const int n = (int)min((long long)LN_K, p.K - k0);
+            if (!once) {
+                __syncthreads();
+                weights(k0, n);
+                __syncthreads();
+            }
+            if (row0 >= p.M) continue;
+#pragma unroll U
+            for (int k = lane; k < n; k += 32) {
+                float x[LN_R];
+#pragma unroll
+                for (int r = 0; r < LN_R; ++r) x[r] = A[r][k0 + k];
+                const float4 u = *reinterpret_cast<const float4 *>(ws[k]), v = *reinterpret_cast<const float4 *>(ws[k] + 4);
+                const float w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+#pragma unroll
+                    for (int r = 0; r < LN_R; ++r) a[8 * r + c] += x[r] * w[c];
+            }
+        }
+        int at = 0;                                  // the element that this lane is left with
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            const bool up = lane & o;
+            at += up ? o : 0;
+#pragma unroll
+            for (int i = 0; i < o; ++i) {
+                const float send = up ? a[i] : a[i + o], kept = up ? a[i + o] : a[i];
+                a[i] = kept + __shfl_xor_sync(0xffffffffu, send, o);
+            }
+        }
+        const long long m = row0 + at / 8;
+        const int n = n0 + at % 8;
+        if (m >= p.M || n >= p.N) continue;
+        const size_t to = (size_t)m * p.N + n;
+        float y[2] = {a[0], 0.f}, z[2] = {0.f, 0.f};
+        if (KIND == LIN_FWD && p.e.bias) y[0] += p.e.bias[n];
+        if (KIND == LIN_DX && p.e.zin) z[0] = p.e.zin[to];
+        if (KIND == LIN_FWD && p.e.out2) p.e.out2[to] = y[0];
+        if (KIND == LIN_FWD) act_apply(y, p.e.act);
+        else if (p.e.zin) act_slope_mul(y, z, p.e.act);
+        p.e.out[to] = p.e.add ? y[0] + p.e.add[to] : y[0];
+    }
+    before_next();
+}
+static_assert(8 * LN_R == 32, "a sum for each lane");
+
 // Weight gradients of narrow operands (in, out <= 32): a thread takes a row at a time and adds the outer product of 8 of its
 // X and 8 of its dZ, read once, to sums in registers; the threads' sums are joined at the end.  (16 rows a step through
 // shared memory, as above, took 283 us for a million rows of 8 -> 8.)
@@ -207,7 +299,7 @@ __global__ void __launch_bounds__(256) k_lin_thin_dw(const LtThin p) {
 }
 static bool lf_thin(int in, int out) { return in <= 32 && out <= 32 && ((in + 7) / 8) * ((out + 7) / 8) <= 8; }
 
-// Tiles of 64 x 64; narrow results of many rows 128 x 16 or 128 x 32; 32 x 32 where others leave SMs without one.
+// Narrow results by warps where lin_narrow() says so, else tiles: 64 x 64; narrow results of many rows 128 x 16 or 128 x 32; 32 x 32 where others leave SMs without one.
 template <int KIND>
 static cudaError_t lf_launch(const LfParams &p, int splits, cudaStream_t st) {
     auto tiles = [&](int bm, int bn) { return ((long long)p.M + bm - 1) / bm * ((p.N + bn - 1) / bn); };
@@ -217,6 +309,12 @@ static cudaError_t lf_launch(const LfParams &p, int splits, cudaStream_t st) {
         return launch_pdl(kernel, dim3((unsigned)n, splits), dim3(256), 0, st, 1, p);
     };
     if constexpr (KIND != LIN_DW) {
+        if (lin_narrow(p.M, p.N, p.K)) {
+            const bool brief = p.K < 256;
+            const long long blocks = (p.N + 7) / 8, rows = ((long long)p.M + 8 * LN_R - 1) / (8 * LN_R);
+            const dim3 grid((unsigned)(std::min(rows, std::max(1LL, (brief ? 4LL : 3LL) * sm_count() / blocks)) * blocks));
+            return brief ? launch_pdl(k_lin_narrow<KIND, 2>, grid, dim3(256), 0, st, 1, p) : launch_pdl(k_lin_narrow<KIND, 4>, grid, dim3(256), 0, st, 1, p);
+        }
         if (p.N <= 16 && tiles(128, 16) >= 2 * sm_count()) return go(k_lin_f32<KIND, 128, 16>, 128, 16);
         if (p.N <= 32 && tiles(128, 32) >= 2 * sm_count()) return go(k_lin_f32<KIND, 128, 32>, 128, 32);
     }

@@ -61,6 +61,7 @@ SHAPES = [  # rows, in, out: tile edges, rows that are not 16 bytes, one of each
     (33, 300, 2056), (1000, 257, 131), (11, 3800, 9), (516, 2776, 132), (40, 9, 3801), (260, 12, 2000), (9, 1, 1), (64, 65536, 3),
     (40_000, 300, 60), (1174, 680, 520), (5000, 1300, 120), (4, 300, 200), (6, 1000, 1001), (7, 520, 1032), (12, 70, 300), (16, 1030, 45),
     (17, 64, 96), (50_000, 8, 8), (40_001, 7, 13), (30_000, 32, 12), (20_000, 33, 20), (25_000, 64, 64),
+    (6580, 2576, 17), (3001, 70, 32), (100, 513, 7), (4000, 8, 1030), (2003, 31, 600), (20_000, 80, 20), (30_001, 257, 9),
 ]
 
 

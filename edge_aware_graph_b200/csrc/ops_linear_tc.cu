@@ -25,8 +25,12 @@
 //
 // The tensor cores add with truncation: a chain of n products of 16 is off by up
 // to n steps of fp32, all in one direction (measured 1e-6 relative after 1024
-// rows, 1.9e-5 after 16384).  fp32 results (PROMO) therefore leave the accumulator
-// every 512 steps of the reduction for a sum in registers, rounded to nearest.
+// rows, 1.9e-5 after 16384, 1.6e-4 after 65536).  The sums therefore leave the accumulator
+// (PROMO) for sums in registers, rounded to nearest: of fp32 results every 512 steps of
+// the reduction, of bf16 ones every 1024, a drift of 2^-17 at the most and 1e-6 as measured, 2000 times below
+// the result's own rounding.  Bf16 results of 8192 x 4096 -> 4096 with gelu, R and Z take 256 us with it, 251 without
+// (265 every 512 steps: a pair's epilogue is then longer than the two accumulators' next products).
+// Reductions of one such stretch go to the epilogue as they are.
 //
 // A weight gradient reduces over rows, of which there may be a million for a
 // 64 x 128 result, and a few rows' products over thousands of features: where
@@ -60,14 +64,14 @@ using namespace sm100;
 typedef __nv_bfloat16 bf16;
 
 constexpr int LT_BM = 128, LT_BK = 64;
-constexpr int LT_PROMO = 8;                            // 64-deep steps an accumulator of an fp32 result takes
+// 64-deep steps an accumulator takes before its sums move on to registers, of an fp32 and of a bf16 result.
+template <typename TO> constexpr int lt_promo() { return sizeof(TO) == 4 ? 8 : 16; }
 
 // PER: CTAs an SM.  Two where reductions are short and tiles narrow and many: each waits for its loads and accumulators most of
 // the time (1M x 34 -> 48).
 template <int KIND, int BN, int CG, typename TO, bool VEC, int PER>
 struct Lt {
     static constexpr int BM = LT_BM * CG, PB = BN / CG;              // the tile's rows; B columns a CTA holds
-    static constexpr bool PROMO = KIND == LIN_DW || sizeof(TO) == 4;
     // Epilogue warps: two or four a TMEM quadrant (32 rows), each with its part of the columns.  A short reduction's tile is
     // bound by them: with 8 warps on 128 columns 34355 x 16 -> 1320 with silu and Z took 60 us.
     static constexpr int EPI = BN == 64 ? 8 : 16, THR = 32 * (4 + EPI);      // TMA, MMA, two column-sum warps, epilogue
@@ -117,12 +121,12 @@ struct LtParams {
     int ablocks, bblocks;      // an MN-major operand's map has blocks of 64 columns: one load a step
 };
 
-template <int KIND, int BN, int CG, typename TO, bool VEC, int PER>
+template <int KIND, int BN, int CG, typename TO, bool VEC, int PER, bool PROMO>
 __global__ void __launch_bounds__(Lt<KIND, BN, CG, TO, VEC, PER>::THR, PER)
 k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<TO> p) {
     using S = Lt<KIND, BN, CG, TO, VEC, PER>;
     constexpr int ST = S::ST, PC = S::PC, PIECES = S::PIECES;
-    constexpr bool A_MN = KIND == LIN_DW, B_MN = KIND != LIN_DX, PAIR = CG == 2, PROMO = S::PROMO;
+    constexpr bool A_MN = KIND == LIN_DW, B_MN = KIND != LIN_DX, PAIR = CG == 2;
     constexpr bool SMEM_SUMS = KIND == LIN_DW && !PAIR;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -270,7 +274,7 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
                     const Unit t = unit_of(u);
                     const int nk = t.steps * p.nseg;
                     for (int k0 = 0; ok && k0 < nk; ++n) {
-                        const int b = n & 1, k1 = PROMO ? min(k0 + LT_PROMO, nk) : nk;
+                        const int b = n & 1, k1 = PROMO ? min(k0 + lt_promo<TO>(), nk) : nk;
                         if (!lt_wait(acc_empty(b), ((n >> 1) & 1) ^ 1, fail, p.status)) { ok = false; break; }
                         tc_fence_after();
                         const uint32_t d = tmem + b * BN;
@@ -440,7 +444,7 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
         bool ok = true;
         for (int u = first; ok && u < p.units; u += stride) {
             const Unit t = unit_of(u);
-            const int nk = t.steps * p.nseg, chunks = PROMO ? (nk + LT_PROMO - 1) / LT_PROMO : 1;
+            const int nk = t.steps * p.nseg, chunks = PROMO ? (nk + lt_promo<TO>() - 1) / lt_promo<TO>() : 1;
             float acc[PROMO ? S::COLS : 1] = {};
             auto released = [&](int b) {            // the accumulator may be written again
                 tc_fence_before();
@@ -676,22 +680,29 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
 
 // ------------------------------------------------------------------ host side
 
-template <int KIND, int BN, int CG, typename TO, bool VEC, int PER = 1>
+template <int KIND, int BN, int CG, typename TO, bool VEC, int PER, bool PROMO>
 static cudaError_t lt_launch(const LtMaps &m, const LtParams<TO> &p, cudaStream_t st) {
     using S = Lt<KIND, BN, CG, TO, VEC, PER>;
-    auto kernel = k_lin_tc<KIND, BN, CG, TO, VEC, PER>;
+    auto kernel = k_lin_tc<KIND, BN, CG, TO, VEC, PER, PROMO>;
     static std::atomic<uint32_t> attr_set{0};
     if (cudaError_t e = ensure_smem_attr(kernel, S::BYTES, attr_set); e != cudaSuccess) return e;
     return launch_pdl(kernel, dim3((unsigned)(std::min(p.units, PER * sm_count() / CG) * CG)), dim3(S::THR), S::BYTES, st, CG, m, p);
 }
+template <int KIND, int BN, int CG, typename TO, bool VEC>
+static cudaError_t lt_sums(const LtMaps &m, const LtParams<TO> &p, cudaStream_t st) {
+    if constexpr (KIND != LIN_DW && sizeof(TO) == 2) {
+        if (std::min(p.per, p.kts) * p.nseg <= lt_promo<TO>()) return lt_launch<KIND, BN, CG, TO, VEC, 1, false>(m, p, st);
+    }
+    return lt_launch<KIND, BN, CG, TO, VEC, 1, true>(m, p, st);
+}
 template <int KIND, typename TO, bool VEC>
 static cudaError_t lt_run(const LinTile &t, const LtMaps &m, const LtParams<TO> &p, cudaStream_t st) {
-    if (t.pair) return lt_launch<KIND, 256, 2, TO, VEC>(m, p, st);
-    if (t.bn == 128) return lt_launch<KIND, 128, 1, TO, VEC>(m, p, st);
+    if (t.pair) return lt_sums<KIND, 256, 2, TO, VEC>(m, p, st);
+    if (t.bn == 128) return lt_sums<KIND, 128, 1, TO, VEC>(m, p, st);
     if constexpr (VEC && KIND != LIN_DW) {
-        if (p.units >= 4 * sm_count() && p.per * p.nseg <= 4) return lt_launch<KIND, 64, 1, TO, VEC, 2>(m, p, st);
+        if (p.units >= 4 * sm_count() && p.per * p.nseg <= 4) return lt_launch<KIND, 64, 1, TO, VEC, 2, sizeof(TO) == 4>(m, p, st);
     }
-    return lt_launch<KIND, 64, 1, TO, VEC>(m, p, st);
+    return lt_sums<KIND, 64, 1, TO, VEC>(m, p, st);
 }
 
 // Tiles and splits: the least of an estimate of each form's time.  The unit is a 64-deep step of a pair's tile,

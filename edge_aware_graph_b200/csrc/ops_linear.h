@@ -42,12 +42,18 @@ __device__ __forceinline__ void normal_cdf(float z0, float z1, float (&phi)[2], 
     e[0] = lo(ex);
     e[1] = hi(ex);
 }
+// max(y, 0); a NaN stays one (fmaxf gives 0, which would hide it from the loss).
+__device__ __forceinline__ float relu(float y) {
+    float r;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(y));
+    return r;
+}
 // y = act(y), and y *= act'(z), the kind chosen once for N values.
 template <int N>
 __device__ __forceinline__ void act_apply(float (&y)[N], int act) {
     if (act == EAGA_ACT_RELU) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) y[j] = fmaxf(y[j], 0.f);
+        for (int j = 0; j < N; ++j) y[j] = relu(y[j]);
     } else if (act == EAGA_ACT_GELU) {
 #pragma unroll
         for (int j = 0; j < N; j += 2) {
@@ -65,7 +71,7 @@ template <int N>
 __device__ __forceinline__ void act_slope_mul(float (&y)[N], const float (&z)[N], int act) {
     if (act == EAGA_ACT_RELU) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) y[j] = z[j] > 0.f ? y[j] : y[j] * 0.f;
+        for (int j = 0; j < N; ++j) y[j] = z[j] > 0.f ? y[j] : y[j] * (z[j] <= 0.f ? 0.f : z[j]);     // NaN where z is
     } else if (act == EAGA_ACT_GELU) {
 #pragma unroll
         for (int j = 0; j < N; j += 2) {

@@ -382,7 +382,8 @@ EAGA_API eaga_status eaga_block_backward(const eaga_dims *dims,
  * to fp32 sums (off by 2^-16 of their terms' magnitudes at the most, 1e-6 as
  * measured, at any length); every output is rounded once.  act_in is the activation that
  * made X (X = act_in(Zin)) where its gradient is wanted in the same pass; dR
- * the gradient that reaches X by another way.  With act none, dY is dZ.
+ * the gradient that reaches X by another way.  With act none, dY is dZ.  A NaN
+ * stays one through every activation and its slope, relu's too.
  *
  * Nullable: b, R and, in the forward, Z (needed by the backward unless act is
  * none); in the backward Z (exactly where act is none), Zin (exactly where

@@ -545,7 +545,9 @@ eaga_status eaga_adamw_step(const eaga_adamw_config *c, const eaga_adamw_tensor 
         if (dt != EAGA_FP32 && dt != EAGA_BF16) return EAGA_ERR_INVALID_ARG;
     for (double x : {c->lr, c->beta1, c->beta2, c->eps, c->grad_scale})
         if (!std::isfinite(x)) return EAGA_ERR_INVALID_ARG;
-    if (c->beta1 < 0 || c->beta1 >= 1 || c->beta2 < 0 || c->beta2 >= 1 || c->eps <= 0 || c->lr < 0)
+    if (c->beta1 < 0 || c->beta1 >= 1 || c->beta2 < 0 || c->beta2 >= 1 || c->lr < 0) return EAGA_ERR_INVALID_ARG;
+    // as the kernels use them: an eps that is 0 in fp32 would make 0 / 0 of an element without a gradient
+    if (!((float)c->eps > 0.f) || !std::isfinite((float)c->eps) || !std::isfinite((float)c->grad_scale) || !std::isfinite((float)c->lr))
         return EAGA_ERR_INVALID_ARG;
     // a master copy for every tensor or for none, and for bf16 weights only
     bool master = false, first = true;

@@ -16,6 +16,7 @@
 #include <torch/csrc/DynamicTypes.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <climits>
 #include <stdexcept>
 #include <string>
 #include "eaga.h"
@@ -78,10 +79,12 @@ struct Call {
     }
     void *stored(const char *name, long long numel, bool optional = false) { return tensor(name, storage, numel, optional); }
     float *f32(const char *name, long long numel) { return static_cast<float *>(tensor(name, at::kFloat, numel, true)); }
-    long long number() {
+    // A whole number that the library takes as an int.
+    int number(const char *name) {
         const long long v = PyLong_AsLongLong(next());
         if (v == -1 && PyErr_Occurred()) throw Raised{};
-        return v;
+        if (v < INT_MIN || v > INT_MAX) refuse(std::string(name) + ": " + std::to_string(v) + " is out of range");
+        return (int)v;
     }
     void *stream() {
         PyObject *o = next();
@@ -132,7 +135,7 @@ PyObject *linear_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
         const long long ni = d->rows * (long long)d->in, no = d->rows * (long long)d->out, nw = (long long)d->in * d->out;
         size_t bytes;
         const void *X = c.stored("X", ni, true), *W = c.stored("W", nw, true), *Z = c.stored("Z", no, true), *dY = c.stored("dY", no);
-        const int act_in = (int)c.number();
+        const int act_in = c.number("act_in");
         const void *Zin = c.stored("Zin", ni, true), *dR = c.stored("dR", ni, true);
         void *dX = c.stored("dX", ni, true);
         float *dW = c.f32("dW", nw), *db = c.f32("db", d->out);
@@ -178,12 +181,12 @@ PyObject *adamw_step(PyObject *, PyObject *const *args, Py_ssize_t n) {
     return guarded(args, n, [&](Call &c) {
         const auto *config = c.structure<eaga_adamw_config>();
         Call peek{args, n, 2};
-        const long long count = peek.number();
+        const int count = peek.number("count");
         const auto *table = c.structure<eaga_adamw_tensor>(count);
-        c.number();
+        c.number("count");
         void *state = c.tensor("state", at::kLong, 2);
         const float *lr = c.f32("lr", 1);
-        return eaga_adamw_step(config, table, (int)count, state, lr, c.stream());
+        return eaga_adamw_step(config, table, count, state, lr, c.stream());
     });
 }
 
@@ -191,10 +194,10 @@ PyObject *adamw_step(PyObject *, PyObject *const *args, Py_ssize_t n) {
 PyObject *adamw_unpack(PyObject *, PyObject *const *args, Py_ssize_t n) {
     return guarded(args, n, [&](Call &c) {
         Call peek{args, n, 1};
-        const long long count = peek.number();
+        const int count = peek.number("count");
         const auto *table = c.structure<eaga_adamw_tensor>(count);
-        c.number();
-        return eaga_adamw_unpack(table, (int)count, c.stream());
+        c.number("count");
+        return eaga_adamw_unpack(table, count, c.stream());
     });
 }
 

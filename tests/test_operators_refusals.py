@@ -11,3 +11,18 @@ from test_operators_abi import L, adam, norm_dims, tensor  # noqa: F401  (L: the
 def test_adamw_scalars_are_checked_as_the_kernel_uses_them(L, cfg):  # noqa: F811
     """Finite in 64 bits, but 0 or infinite in the 32 that the step computes in."""
     assert adam(L, [tensor()], **cfg) == 1
+
+
+def test_adamw_counts_beyond_an_int(L):  # noqa: F811
+    """Not taken modulo 2^32, past the end of the table that was checked."""
+    table = (eaga.AdamwTensor * 1)(tensor())
+    for count in ((1 << 32) + 1, -(1 << 32) + 1, 1 << 31):
+        with pytest.raises(ValueError, match="count"):
+            eaga.adamw_unpack(table, count, 0)
+        with pytest.raises(ValueError, match="count"):
+            eaga.adamw_step(eaga.AdamwConfig(), table, count, None, None, 0)
+    with pytest.raises(eaga.EagaError) as e:
+        eaga.adamw_unpack(table, (1 << 20) + 1, 0)
+    assert e.value.code == 2
+    with pytest.raises(ValueError):
+        eaga.adamw_unpack(table, 2, 0)

@@ -5,7 +5,8 @@
 // run on the GPU; here a call costs its launch.  Each function takes the dims
 // (a ctypes structure), the call's tensors in the C entry's order and the stream
 // (None: the current one, a torch stream, or its handle as a number), and
-// returns the C entry's status.  What a tensor has to be is read from the dims:
+// returns the C entry's status.  The structures have to be eaga.py's classes of
+// them; what a tensor has to be is read from the dims:
 // a contiguous CUDA tensor on the current device, of the dtype and the number of
 // elements that the kernels will go by.
 #define PY_SSIZE_T_CLEAN
@@ -32,6 +33,28 @@ struct Raised {};
 }
 std::string dtype_name(at::ScalarType t) { return std::string("torch.") + torch::getTHPDtype(t)->name; }
 
+// The ctypes classes of the library's structures (eaga.py's, given once by bind()).
+template <typename T>
+struct Structure {
+    static PyObject *type;
+    static const char *const name;
+};
+template <typename T> PyObject *Structure<T>::type = nullptr;
+template <> const char *const Structure<eaga_linear_dims>::name = "LinearDims";
+template <> const char *const Structure<eaga_residual_norm_dims>::name = "ResidualNormDims";
+template <> const char *const Structure<eaga_adamw_config>::name = "AdamwConfig";
+template <> const char *const Structure<eaga_adamw_tensor>::name = "AdamwTensor";
+
+// Whether `o` is one of `type` or a ctypes array of them.
+bool is_structure(PyObject *o, PyObject *type) {
+    if (!type) return false;
+    if (PyObject_TypeCheck(o, reinterpret_cast<PyTypeObject *>(type))) return true;
+    PyObject *of = PyObject_GetAttrString(reinterpret_cast<PyObject *>(Py_TYPE(o)), "_type_");
+    PyErr_Clear();
+    Py_XDECREF(of);
+    return of == type;
+}
+
 struct Call {
     PyObject *const *args;
     Py_ssize_t n;
@@ -43,17 +66,19 @@ struct Call {
         if (at >= n) throw std::runtime_error("too few arguments");
         return args[at++];
     }
-    // The ctypes structure `T` (or an array of at least `count` of them).
+    // The ctypes structure `T`, or an array of at least `count` of them.
     template <typename T>
     const T *structure(Py_ssize_t count = 1) {
+        PyObject *o = next();
+        if (!is_structure(o, Structure<T>::type)) refuse(std::string("a ") + Structure<T>::name + " is required (got " + Py_TYPE(o)->tp_name + ")");
         Py_buffer b;
-        if (PyObject_GetBuffer(next(), &b, PyBUF_SIMPLE) != 0) throw Raised{};
+        if (PyObject_GetBuffer(o, &b, PyBUF_SIMPLE) != 0) throw Raised{};
         const void *p = b.buf;
         const Py_ssize_t len = b.len;
         PyBuffer_Release(&b);                        // the argument keeps the memory
         // (a table of more entries than the library takes is refused there, unread)
         if (count > (1 << 20)) count = 1;
-        if (len < (Py_ssize_t)sizeof(T) * count) refuse("a structure of the library is required");
+        if (len < (Py_ssize_t)sizeof(T) * count) refuse(std::string("a table of ") + std::to_string(count) + " " + Structure<T>::name + " is required");
         return static_cast<const T *>(p);
     }
     // The address of a tensor of `numel` elements (-1: any number); null for None where `optional`.
@@ -201,9 +226,23 @@ PyObject *adamw_unpack(PyObject *, PyObject *const *args, Py_ssize_t n) {
     });
 }
 
+// LinearDims, ResidualNormDims, AdamwConfig, AdamwTensor
+PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    PyObject **const to[4] = {&Structure<eaga_linear_dims>::type, &Structure<eaga_residual_norm_dims>::type, &Structure<eaga_adamw_config>::type,
+                              &Structure<eaga_adamw_tensor>::type};
+    for (Py_ssize_t k = 0; k < 4; ++k) {
+        if (n != 4 || !PyType_Check(args[k])) {
+            PyErr_SetString(PyExc_TypeError, "four ctypes classes are required");
+            return nullptr;
+        }
+    }
+    for (int k = 0; k < 4; ++k) Py_XSETREF(*to[k], Py_NewRef(args[k]));
+    Py_RETURN_NONE;
+}
+
 #define ENTRY(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ENTRY(linear_forward), ENTRY(linear_backward), ENTRY(residual_norm_forward), ENTRY(residual_norm_backward),
-                         ENTRY(adamw_step), ENTRY(adamw_unpack), {nullptr, nullptr, 0, nullptr}};
+                         ENTRY(adamw_step), ENTRY(adamw_unpack), ENTRY(bind), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -385,6 +385,7 @@ def _native():
         lib()
         import torch  # noqa: F401  (its libraries)
         from . import _native as m
+        m.bind(LinearDims, ResidualNormDims, AdamwConfig, AdamwTensor)
         _native_module = m
     return _native_module
 

@@ -26,3 +26,26 @@ def test_adamw_counts_beyond_an_int(L):  # noqa: F811
     assert e.value.code == 2
     with pytest.raises(ValueError):
         eaga.adamw_unpack(table, 2, 0)
+
+
+def test_structures_of_another_kind(L):  # noqa: F811
+    """Long enough is not enough: each call takes its own structure."""
+    import torch
+    host = torch.zeros(64, 128, dtype=torch.bfloat16)
+    wrong = norm_dims(), eaga.AdamwConfig(), bytearray(4096), (eaga.AdamwTensor * 9)(), None, 3
+    for d in wrong:
+        with pytest.raises(ValueError, match="LinearDims"):
+            eaga.linear_forward(d, host, None, None, None, None, None, None)
+        with pytest.raises(ValueError, match="LinearDims"):
+            eaga.linear_backward(d, host, None, None, None, None, None, None, None)
+        with pytest.raises(ValueError, match="AdamwTensor" if d is not wrong[3] else "state"):
+            eaga.adamw_step(eaga.AdamwConfig(), d, 1, None)
+    for d in (eaga.linear_dims(64, 128, 8), (eaga.ResidualNormDims * 2)()._type_, (ctypes.c_double * 64)()):
+        with pytest.raises(ValueError, match="ResidualNormDims"):
+            eaga.residual_norm_forward(d, None, host, None, None, None, None, None, None, None, None)
+        with pytest.raises(ValueError, match="ResidualNormDims"):
+            eaga.residual_norm_backward(d, *[None] * 17)
+        with pytest.raises(ValueError, match="AdamwConfig"):
+            eaga.adamw_step(d, (eaga.AdamwTensor * 1)(), 1, None)
+    with pytest.raises(ValueError, match="u: a CUDA tensor"):
+        eaga.residual_norm_forward(norm_dims(), None, host, None, None, None, None, None, None, None, None)

@@ -853,7 +853,7 @@ static eaga_status rn_check(const eaga_residual_norm_dims *d) {
         if (k != RN_NONE && k != RN_LAYER && k != RN_RMS) return EAGA_ERR_INVALID_ARG;
     if (!(d->eps > 0.f) || !std::isfinite(d->eps) || !std::isfinite(d->alpha)) return EAGA_ERR_INVALID_ARG;
     if (d->rows % d->rows_per_group) return EAGA_ERR_INVALID_ARG;
-    if (d->w > 8192 || d->rows > 0x7fff0000LL) return EAGA_ERR_UNSUPPORTED;
+    if (d->w > 8192 || d->rows > 0x7fff0000LL || d->rows_per_group > 0x7fff0000LL) return EAGA_ERR_UNSUPPORTED;
     return EAGA_OK;
 }
 

@@ -440,7 +440,7 @@ EAGA_API eaga_status eaga_linear_backward(const eaga_linear_dims *dims, const vo
  * Masked rows' dx and du are 0.  All sums in a fixed order.
  *
  * Limits: w <= 8192 (any w; multiples of 16 bytes are the fast ones), rows
- * <= 2147418112 and a multiple of rows_per_group; eps > 0.  rows = 0 is a
+ * and rows_per_group <= 2147418112, rows a multiple of rows_per_group; eps > 0.  rows = 0 is a
  * call that writes no row (and zero parameter gradients). */
 typedef enum { EAGA_NORM_NONE = 0, EAGA_NORM_LAYER = 1, EAGA_NORM_RMS = 2 } eaga_norm;
 typedef struct {

@@ -49,3 +49,11 @@ def test_structures_of_another_kind(L):  # noqa: F811
             eaga.adamw_step(d, (eaga.AdamwTensor * 1)(), 1, None)
     with pytest.raises(ValueError, match="u: a CUDA tensor"):
         eaga.residual_norm_forward(norm_dims(), None, host, None, None, None, None, None, None, None, None)
+
+
+@pytest.mark.parametrize("w", [8, 64, 128, 333, 4096])
+@pytest.mark.parametrize("group", [2 ** 63 - 1, 2 ** 63 - 40, 2 ** 40, 2 ** 31])
+def test_norm_groups_beyond_the_limit(L, w, group):  # noqa: F811
+    """Of a call without rows too, whose plan divides by the length of the groups' runs."""
+    assert eaga.residual_norm_workspace_size(norm_dims(rows=0, w=w, rows_per_group=group)) == 0
+    assert eaga.residual_norm_workspace_size(norm_dims(rows=0, w=w, rows_per_group=0x7fff0000)) >= 256

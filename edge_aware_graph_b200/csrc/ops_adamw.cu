@@ -444,7 +444,8 @@ struct Range {
 // EAGA_ERR_INVALID_ARG if a written range overlaps another one.  Lists whose
 // buffers each lie in ascending order in a region of their own (parameters,
 // gradients and states in flat buffers) are cleared in one pass; others are sorted.
-static eaga_status check_ranges(Range *r, int n, int kinds) {
+// `more`: two buffers beside the lists, for which `r` has room behind its n.
+static eaga_status check_ranges(Range *r, int n, int kinds, const Range (&more)[2]) {
     bool plain = true;
     uintptr_t lo[8], hi[8];
     for (int k = 0; k < kinds && plain; ++k) {
@@ -457,8 +458,12 @@ static eaga_status check_ranges(Range *r, int n, int kinds) {
         }
         for (int j = 0; j < k; ++j)
             if (hi[k] && hi[j] && lo[k] < hi[j] && lo[j] < hi[k]) plain = false;
+        for (const Range &m : more)
+            if (hi[k] && lo[k] < m.hi && m.lo < hi[k]) plain = false;
     }
+    if (more[0].lo < more[1].hi && more[1].lo < more[0].hi) return EAGA_ERR_INVALID_ARG;
     if (plain) return EAGA_OK;
+    for (const Range &m : more) r[n++] = m;
     std::sort(r, r + n, [](const Range &a, const Range &b) { return a.lo < b.lo; });
     uintptr_t end = 0, end_out = 0;
     for (int i = 0; i < n; ++i) {
@@ -470,11 +475,15 @@ static eaga_status check_ranges(Range *r, int n, int kinds) {
     return EAGA_OK;
 }
 
-
+static Range range_of(const void *p, long long bytes, bool out) {
+    const uintptr_t b = reinterpret_cast<uintptr_t>(p);
+    return Range{b, p ? b + (uintptr_t)bytes : b, out};
+}
 
 // Checks the tensors and lays out their entries (the empty ones left out) in `e`; `count` becomes their number.
-static eaga_status gather(const eaga_adamw_tensor *t, int &count, int bits, int pbytes, int gbytes, AdEntry *e,
-                          Range *ranges) {
+// state, lr: a step's, else null.
+static eaga_status gather(const eaga_adamw_tensor *t, int &count, int bits, int pbytes, int gbytes, const void *state, const void *lr,
+                          AdEntry *e, Range *ranges) {
     int kept = 0;
     long long tiles = 0;
     for (int i = 0; i < count; ++i) {
@@ -491,25 +500,21 @@ static eaga_status gather(const eaga_adamw_tensor *t, int &count, int bits, int 
             return EAGA_ERR_MISALIGNED;
         const long long blocks = bits == 8 ? (a.n + AD_BLOCK - 1) / AD_BLOCK * 4 : 0;
         const long long sb = bits == 8 ? a.n : 4 * a.n;
-        auto range = [](const void *p, long long bytes, bool out) {
-            const uintptr_t b = reinterpret_cast<uintptr_t>(p);
-            return Range{b, p ? b + (uintptr_t)bytes : b, out};
-        };
         Range *r = ranges + 7 * kept;
         const bool step = pbytes != 0;           // unpack writes its two fp32 outputs and reads the states
-        r[0] = range(a.p, a.n * (step ? pbytes : 4), true);
-        r[1] = range(a.master, a.n * 4, true);
-        r[2] = range(a.g, a.n * gbytes, false);
-        r[3] = range(a.m, sb, step);
-        r[4] = range(a.v, sb, step);
-        r[5] = range(bits == 8 ? a.m_scale : nullptr, blocks, step);
-        r[6] = range(bits == 8 ? a.v_scale : nullptr, blocks, step);
+        r[0] = range_of(a.p, a.n * (step ? pbytes : 4), true);
+        r[1] = range_of(a.master, a.n * 4, true);
+        r[2] = range_of(a.g, a.n * gbytes, false);
+        r[3] = range_of(a.m, sb, step);
+        r[4] = range_of(a.v, sb, step);
+        r[5] = range_of(bits == 8 ? a.m_scale : nullptr, blocks, step);
+        r[6] = range_of(bits == 8 ? a.v_scale : nullptr, blocks, step);
         e[kept++] = {a.p, a.master, a.g, a.m, a.v, a.m_scale, a.v_scale, a.n, a.counter, a.weight_decay, 0};
         tiles += (a.n + AD_TILE - 1) / AD_TILE;
         if (tiles > 0x7fffffffLL) return EAGA_ERR_UNSUPPORTED;
     }
     count = kept;
-    return check_ranges(ranges, 7 * kept, 7);
+    return check_ranges(ranges, 7 * kept, 7, {range_of(state, 16, true), range_of(lr, 4, false)});
 }
 
 // Host memory of one call's table; freed on every way out.
@@ -561,7 +566,7 @@ eaga_status eaga_adamw_step(const eaga_adamw_config *c, const eaga_adamw_tensor 
     HostTable h(count);
     if (!h.e || !h.r) return EAGA_ERR_UNSUPPORTED;
     const int pb = c->param_dtype == EAGA_FP32 ? 4 : 2, gb = c->grad_dtype == EAGA_FP32 ? 4 : 2;
-    if (eaga_status s = gather(t, count, c->state_bits, pb, gb, h.e, h.r); s != EAGA_OK) return s;
+    if (eaga_status s = gather(t, count, c->state_bits, pb, gb, state, lr, h.e, h.r); s != EAGA_OK) return s;
     AdScalars a = {};
     a.lr = c->lr; a.beta1 = c->beta1; a.beta2 = c->beta2;
     a.b1 = (float)c->beta1; a.omb1 = (float)(1.0 - c->beta1);
@@ -584,7 +589,7 @@ eaga_status eaga_adamw_unpack(const eaga_adamw_tensor *t, int count, void *strea
     if (count > (1 << 20)) return EAGA_ERR_UNSUPPORTED;
     HostTable h(count);
     if (!h.e || !h.r) return EAGA_ERR_UNSUPPORTED;
-    if (eaga_status s = gather(t, count, 8, 0, 0, h.e, h.r); s != EAGA_OK) return s;
+    if (eaga_status s = gather(t, count, 8, 0, 0, nullptr, nullptr, h.e, h.r); s != EAGA_OK) return s;
     if (!count) return EAGA_OK;
     AdScalars a = {};
     const cudaError_t err = launch_all<UnpackLaunch>(a, h.e, count, static_cast<cudaStream_t>(stream));

@@ -488,8 +488,8 @@ EAGA_API eaga_status eaga_residual_norm_backward(const eaga_residual_norm_dims *
  * number of steps taken, as int64, then zero): the step counts there, so that a
  * captured call counts its replays.  `lr` (nullable) is a device float that
  * replaces config.lr, for schedules under replay.  Weights, masters and states
- * are updated in place; no two written buffers may overlap, nor one with a
- * gradient.  Calls on the same state or tensors must be ordered by the caller.
+ * are updated in place; no two written buffers (`state` is one) may overlap, nor
+ * one with a gradient or `lr`.  Calls on the same state or tensors must be ordered by the caller.
  * lr >= 0, eps > 0 and grad_scale are finite, and eps above 0, as fp32 too. */
 typedef struct {
     double lr, beta1, beta2, eps, grad_scale;

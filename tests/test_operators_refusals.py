@@ -57,3 +57,21 @@ def test_norm_groups_beyond_the_limit(L, w, group):  # noqa: F811
     """Of a call without rows too, whose plan divides by the length of the groups' runs."""
     assert eaga.residual_norm_workspace_size(norm_dims(rows=0, w=w, rows_per_group=group)) == 0
     assert eaga.residual_norm_workspace_size(norm_dims(rows=0, w=w, rows_per_group=0x7fff0000)) >= 256
+
+
+def test_adamw_step_count_and_rate_apart_from_the_tensors(L):  # noqa: F811
+    """The step writes its count: not into a tensor's buffers, nor over the rate; and no buffer over the rate."""
+    def call(tensors, state=0x10, lr=None):
+        c = eaga.AdamwConfig(1e-3, 0.9, 0.999, 1e-8, 1.0, 1, 0, 8, 0)
+        return L.eaga_adamw_step(ctypes.byref(c), (eaga.AdamwTensor * len(tensors))(*tensors), len(tensors), state, lr, None)
+
+    two = [tensor(0), tensor(1)]
+    for k in ("p", "master", "g", "m", "v", "m_scale", "v_scale"):
+        assert call(two, state=getattr(two[1], k)) == 1, k
+        assert call(two[::-1], state=getattr(two[1], k)) == 1, k
+        if k != "g":
+            assert call(two, lr=getattr(two[0], k)) == 1, k
+    assert call(two, state=tensor().p + 192) == 1         # the last 8 of a weight's 200 bytes
+    assert call(two, state=0x40, lr=0x48) == 1
+    apart = call(two, lr=0x30)                            # what a call without overlaps answers without a GPU
+    assert apart != 1 and call(two, lr=two[0].g + 16) == apart and call(two[::-1], state=tensor().p + 208) == apart

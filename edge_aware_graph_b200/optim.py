@@ -75,7 +75,7 @@ class AdamW:
         elif master is None:
             self.master = _flat(sizes, torch.float32, self.device)
             for a, p in zip(self.master, params):
-                a.copy_(p.reshape(-1))
+                a.copy_(p.detach().reshape(-1))
         else:
             self.master = take(master, "master", torch.float32)
         sd = torch.float32 if bits == 32 else torch.uint8
@@ -154,7 +154,7 @@ class AdamW:
 
     def state_dict(self) -> dict:
         """What a checkpoint needs: the states as they are held, the masters, the step."""
-        clone = lambda ts: None if ts is None else [t.clone() for t in ts]
+        clone = lambda ts: None if ts is None else [t.detach().clone() for t in ts]
         return {"bits": int(self.config.state_bits), "step": self.steps,
                 **{k: clone(getattr(self, k)) for k in ("master", "m", "v", "m_scale", "v_scale")}}
 
@@ -166,5 +166,5 @@ class AdamW:
             if (mine is None) != (theirs is None) or (mine is not None and [t.numel() for t in mine] != [t.numel() for t in theirs]):
                 raise ValueError(f"{k}: not the states of these tensors")
             for a, b in zip(mine or (), theirs or ()):
-                a.copy_(b)
+                a.detach().copy_(b)
         self.state.copy_(torch.tensor([s["step"], 0], dtype=torch.int64))

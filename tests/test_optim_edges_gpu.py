@@ -1,0 +1,30 @@
+"""AdamW over weights that a program also differentiates, and what its Python side refuses."""
+import pytest
+import torch
+
+from edge_aware_graph_b200.optim import AdamW
+
+pytestmark = pytest.mark.gpu
+
+
+def make(bits=8, n=(300, 17), **kw):
+    g = torch.Generator().manual_seed(1)
+    p = [torch.randn(k, generator=g).to("cuda", torch.bfloat16) for k in n]
+    d = [torch.randn(k, generator=g).cuda() for k in n]
+    return p, d, AdamW(p, d, bits=bits, **kw)
+
+
+def test_weights_of_a_program_that_differentiates():
+    """Masters and states are plain tensors: no graph is kept through them, and none grows with the checkpoints."""
+    p, d, plain = make()
+    leaves = [torch.nn.Parameter(t.clone()) for t in p]
+    opt = AdamW(leaves, d, bits=8)
+    for t in opt.master + opt.m + opt.v:
+        assert not t.requires_grad and t.grad_fn is None
+    opt.step()
+    plain.step()
+    s = opt.state_dict()
+    assert not any(t.requires_grad for k in ("master", "m", "v", "m_scale", "v_scale") for t in s[k])
+    opt.load_state_dict(s)
+    for a, b in zip(opt.params + opt.master + opt.m + opt.v, plain.params + plain.master + plain.m + plain.v):
+        assert torch.equal(a.detach(), b)

@@ -149,6 +149,8 @@ class AdamW:
         held = (list(m_out), list(v_out), self)
 
         def run(stream=None, held=held):
+            if torch.cuda.current_device() != self.device.index:     # the call has no tensor of its own to tell by
+                raise ValueError(f"unpack: on {self.device}, but the current device is cuda:{torch.cuda.current_device()}")
             eaga.adamw_unpack(table, k, stream)
         return run
 

@@ -28,3 +28,23 @@ def test_weights_of_a_program_that_differentiates():
     opt.load_state_dict(s)
     for a, b in zip(opt.params + opt.master + opt.m + opt.v, plain.params + plain.master + plain.m + plain.v):
         assert torch.equal(a.detach(), b)
+
+
+def test_unpacking_on_another_device_is_refused(monkeypatch):
+    p, d, opt = make()
+    opt.step()
+    m, v = opt.unpack()
+    run = opt.unpacker(m, v)
+    before = [t.clone() for t in m + v]
+    opt.step()
+    torch.cuda.synchronize()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError, match="current device"):
+        run()
+    with pytest.raises(ValueError, match="current device"):
+        opt.unpack(m, v)
+    monkeypatch.undo()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(before, m + v))
+    run()
+    assert not torch.equal(before[0], m[0])

@@ -163,10 +163,12 @@ class AdamW:
     def load_state_dict(self, s: dict):
         if s["bits"] != self.config.state_bits:
             raise ValueError(f"states in {s['bits']} bits, expected {self.config.state_bits}")
-        for k in ("master", "m", "v", "m_scale", "v_scale"):
-            mine, theirs = getattr(self, k), s[k]
-            if (mine is None) != (theirs is None) or (mine is not None and [t.numel() for t in mine] != [t.numel() for t in theirs]):
+        names = ("master", "m", "v", "m_scale", "v_scale")
+        like = lambda ts: None if ts is None else [(t.numel(), t.dtype) for t in ts]
+        for k in names:                                 # all before any is loaded
+            if like(getattr(self, k)) != like(s[k]):
                 raise ValueError(f"{k}: not the states of these tensors")
-            for a, b in zip(mine or (), theirs or ()):
-                a.detach().copy_(b)
+        for k in names:
+            for a, b in zip(getattr(self, k) or (), s[k] or ()):
+                a.detach().copy_(b.reshape(a.shape))
         self.state.copy_(torch.tensor([s["step"], 0], dtype=torch.int64))

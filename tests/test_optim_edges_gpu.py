@@ -48,3 +48,26 @@ def test_unpacking_on_another_device_is_refused(monkeypatch):
     assert all(torch.equal(a, b) for a, b in zip(before, m + v))
     run()
     assert not torch.equal(before[0], m[0])
+
+
+def test_states_of_other_tensors_leave_the_optimiser_as_it_was():
+    """A checkpoint that does not fit is refused whole: no part of it is loaded before the misfit is found."""
+    p, d, opt = make()
+    opt.step()
+    good = opt.state_dict()
+    opt.step()
+    now = opt.state_dict()
+    for k in ("master", "m", "v", "m_scale", "v_scale"):
+        bad = {**good, k: good[k][:-1] + [torch.zeros(5, dtype=good[k][-1].dtype, device="cuda")]}
+        with pytest.raises(ValueError, match=k):
+            opt.load_state_dict(bad)
+        with pytest.raises(ValueError, match=k):
+            opt.load_state_dict({**good, k: None})
+        with pytest.raises(ValueError, match=k):          # codes read as numbers, or numbers as codes
+            opt.load_state_dict({**good, k: [t.to(torch.int16) for t in good[k]]})
+        after = opt.state_dict()
+        assert after["step"] == now["step"]
+        for name in ("master", "m", "v", "m_scale", "v_scale"):
+            assert all(torch.equal(a, b) for a, b in zip(after[name], now[name])), (k, name)
+    opt.load_state_dict(good)
+    assert opt.steps == 1 and all(torch.equal(a, b) for a, b in zip(opt.m, good["m"]))

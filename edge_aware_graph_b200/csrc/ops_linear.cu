@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(256) k_lin_prep(const __grid_constant__ PrepAr
         flat_ld8(src, row * j.n + c, all, have, v);
         if (zs) {
             flat_ld8(zs, row * j.n + c, all, have, z);
-            act_slope_mul(v, z, j.act);
+            act_slope_mul<T>(v, z, j.act);
         }
         if (j.f32) lin_st8(j.f32 + row * j.n + c, have, j.n % 4 == 0, v);
         for (int k = 0; k < j.parts; ++k) {
@@ -124,10 +124,10 @@ __global__ void __launch_bounds__(256) k_lin_join(const float *acc, int splits, 
             for (int j = 0; j < VEC; ++j) y[j] += o[j];
         }
         if (e.out2) lin_st8(e.out2 + i, VEC, VEC > 1, y);
-        act_apply(y, e.act);
+        act_apply<T>(y, e.act);
     } else if (e.zin) {
         lin_ld8(e.zin + i, VEC, VEC > 1, o);
-        act_slope_mul(y, o, e.act);
+        act_slope_mul<T>(y, o, e.act);
     }
     if (e.add) {
         lin_ld8(e.add + i, VEC, VEC > 1, o);

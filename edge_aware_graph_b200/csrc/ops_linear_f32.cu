@@ -127,9 +127,9 @@ k_lin_f32(const LfParams p) {
                     for (int j = 0; j < TN; ++j)
                         if (n + j < p.N) p.e.out2[at + j] = y[j];
                 }
-                act_apply(y, p.e.act);
+                act_apply<float>(y, p.e.act);
             } else if (p.e.zin) {
-                act_slope_mul(y, z, p.e.act);
+                act_slope_mul<float>(y, z, p.e.act);
             }
 #pragma unroll
             for (int j = 0; j < TN; ++j)
@@ -225,8 +225,8 @@ k_lin_narrow(const LfParams p) {
         if (KIND == LIN_FWD && p.e.bias) y[0] += p.e.bias[n];
         if (KIND == LIN_DX && p.e.zin) z[0] = p.e.zin[to];
         if (KIND == LIN_FWD && p.e.out2) p.e.out2[to] = y[0];
-        if (KIND == LIN_FWD) act_apply(y, p.e.act);
-        else if (p.e.zin) act_slope_mul(y, z, p.e.act);
+        if (KIND == LIN_FWD) act_apply<float>(y, p.e.act);
+        else if (p.e.zin) act_slope_mul<float>(y, z, p.e.act);
         p.e.out[to] = p.e.add ? y[0] + p.e.add[to] : y[0];
     }
     before_next();

@@ -545,7 +545,7 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
                             }
                         }
                         if (has_z) put(side);
-                        act_apply(v, p.e.act);
+                        act_apply<TO>(v, p.e.act);
                     } else if constexpr (KIND == LIN_DX) {
                         if (has_zin) {
 #pragma unroll
@@ -554,7 +554,7 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
                                 get(sidep, x, f);
 #pragma unroll
                                 for (int j = 0; j < PER; ++j) y[j] = v[x * PER + j];
-                                act_slope_mul(y, f, p.e.act);
+                                act_slope_mul<TO>(y, f, p.e.act);
 #pragma unroll
                                 for (int j = 0; j < PER; ++j) v[x * PER + j] = y[j];
                             }
@@ -618,11 +618,11 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
                                 if constexpr (KIND == LIN_FWD) {
                                     y[0] += bias;
                                     if (p.e.out2) stf(p.e.out2 + at + (size_t)j * p.N, y[0]);
-                                    act_apply(y, p.e.act);
+                                    act_apply<TO>(y, p.e.act);
                                 } else if constexpr (KIND == LIN_DX) {
                                     if (p.e.zin) {
                                         const float z[1] = {ldf(&zi[j])};
-                                        act_slope_mul(y, z, p.e.act);
+                                        act_slope_mul<TO>(y, z, p.e.act);
                                     }
                                 }
                                 if (KIND != LIN_DW && p.e.add) y[0] += ldf(&ad[j]);

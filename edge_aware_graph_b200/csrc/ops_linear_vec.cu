@@ -134,7 +134,7 @@ k_lin_vec_fwd(const LinVec<T> p, const LinEpi<T> e, int part, int cluster) {
             const size_t at = (size_t)r * p.out + c;
             if (e.out2) stf(e.out2 + at, z);
             float y[1] = {z};
-            act_apply(y, e.act);
+            act_apply<T>(y, e.act);
             if (e.add) y[0] += ldf(e.add + at);
             stf(e.out + at, y[0]);
         }
@@ -170,7 +170,7 @@ k_lin_vec_bwd(const LinVec<T> p, const LinEpi<T> e) {
                 d[r] = r < p.rows ? ldf(p.dY + at) : 0.f;
                 z[r] = p.Z && r < p.rows ? ldf(p.Z + at) : 0.f;
             }
-            if (p.Z) act_slope_mul(d, z, p.act);
+            if (p.Z) act_slope_mul<T>(d, z, p.act);
 #pragma unroll
             for (int r = 0; r < R; ++r) dz[r][c] = d[r];
         }
@@ -228,7 +228,7 @@ k_lin_vec_bwd(const LinVec<T> p, const LinEpi<T> e) {
                 float y[1] = {acc[r]};
                 if (e.zin) {
                     const float z[1] = {ldf(e.zin + at)};
-                    act_slope_mul(y, z, e.act);
+                    act_slope_mul<T>(y, z, e.act);
                 }
                 if (e.add) y[0] += ldf(e.add + at);
                 stf(p.dX + at, y[0]);

@@ -59,3 +59,47 @@ def test_a_nan_is_seen_behind_every_activation(dtype, rows, i, o, act):
     want[3, 2] = act != "none"
     col = torch.arange(o, device="cuda") == 5
     assert torch.equal(nan(dX), want) and torch.equal(nan(dW), col.expand(i, o)) and torch.equal(nan(dB), col)
+
+
+GELU_SHAPES = [(4, 8, 512), (13, 70, 128), (300, 200, 136), (2001, 257, 131), (20_001, 64, 128), (3001, 70, 32), (3001, 32, 70), (20_000, 33, 20), (700, 900, 260)]
+
+
+@pytest.mark.parametrize("rows,i,o", GELU_SHAPES)
+def test_gelu_in_fp32_is_right_in_its_relative_error(rows, i, o):
+    """Every z exactly (one product a sum, by 1 or -1), from -9 to 9, tails and the slope's zero among them.  With s = 2^-23:
+
+    Phi(-x) = t Q(t) e^(-x^2/2): t is off by 1.5 s (its divisor's rounding, the reciprocal), twice that in the result (d ln Phi / d ln t
+    is 2 at the most), Q by 2.75 s (its steps' roundings, its argument's, its fit), e by 2.5 s (the power of two's 2 s, its correction's rounding),
+    two products by half a step each: 9.25 s.  y = z Phi(z) rounds twice more: 10.25 s |y|.
+    slope = Phi + z phi, phi = e^(-z^2/2) / sqrt(2 pi): 2.5 s and three roundings: 9.25 s Phi + 4 s |z phi| and a step of the sum."""
+    g = torch.Generator().manual_seed(rows + o)
+    s = 2.0 ** -23
+    z = (torch.rand(rows, generator=g) * 18 - 9).float()
+    z[:3] = torch.tensor([-3.0, 0.0, -0.7517916])
+    X = torch.zeros(rows, i)
+    X[torch.arange(rows), torch.arange(rows) % i] = z
+    sign = (1 - 2 * (torch.arange(o) % 2)).float()
+    W = sign.expand(i, o).contiguous()
+    Z64 = z.double()[:, None] * sign.double()
+    phi = torch.special.erfc(-Z64 / 2 ** 0.5) / 2        # (ndtr is 1 + erf: nothing of a tail)
+    y = Z64 * phi
+    Y, Z = forward(X.cuda(), W.cuda(), act="gelu", dtype="fp32")
+    assert torch.equal(Z.cpu().double(), Z64)
+    off = (Y.cpu().double() - y).abs()
+    assert (off <= 10.25 * s * y.abs()).all(), float((off / (s * y.abs()).clamp(min=1e-300)).max())
+    # the slope of Z, read off a product by 1: dX has one dZ in each row
+    pdf = torch.exp(-Z64 * Z64 / 2) / (2 * torch.pi) ** 0.5
+    slope = phi + Z64 * pdf
+    tol = s * (9.25 * phi + 4 * (Z64 * pdf).abs() + slope.abs())
+    dY = torch.zeros(rows, o)
+    c = torch.arange(rows) % o
+    dY[torch.arange(rows), c] = 1
+    dX, _, _ = backward(None, W.cuda(), dY.cuda(), Z=Z, act="gelu", dw=False, dtype="fp32")
+    want = (slope[torch.arange(rows), c] * sign.double()[c])[:, None]
+    off = (dX.cpu().double() - want).abs()
+    assert (off <= tol[torch.arange(rows), c][:, None]).all(), float((off / tol[torch.arange(rows), c][:, None]).max())
+    # and of Zin, in the epilogue
+    Zin = Z64[:, :1].float().expand(rows, i).contiguous()
+    dX, _, _ = backward(None, torch.ones(i, o, device="cuda"), dY.cuda(), act_in="gelu", Zin=Zin.cuda(), dw=False, dtype="fp32")
+    off = (dX.cpu().double() - slope[:, :1]).abs()
+    assert (off <= tol[:, :1]).all(), float((off / tol[:, :1]).max())

@@ -699,8 +699,8 @@ template <int KIND, typename TO, bool VEC>
 static cudaError_t lt_run(const LinTile &t, const LtMaps &m, const LtParams<TO> &p, cudaStream_t st) {
     if (t.pair) return lt_sums<KIND, 256, 2, TO, VEC>(m, p, st);
     if (t.bn == 128) return lt_sums<KIND, 128, 1, TO, VEC>(m, p, st);
-    if constexpr (VEC && KIND != LIN_DW) {
-        if (p.units >= 4 * sm_count() && p.per * p.nseg <= 4) return lt_launch<KIND, 64, 1, TO, VEC, 2, sizeof(TO) == 4>(m, p, st);
+    if constexpr (VEC && KIND != LIN_DW && sizeof(TO) == 2) {          // (an fp32 result has six products a step, or splits of more steps)
+        if (p.units >= 4 * sm_count() && p.per * p.nseg <= 4) return lt_launch<KIND, 64, 1, TO, VEC, 2, false>(m, p, st);
     }
     return lt_sums<KIND, 64, 1, TO, VEC>(m, p, st);
 }

@@ -85,21 +85,19 @@ bool encode_blocks(CUtensorMap *m, const void *base, int rows, int cols, int blo
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// [planes, rows, cols] bf16 (or fp32) with a box of box_cols x box_rows in one plane, whose rows of 64 or 128
-// bytes land swizzled by as much; box_cols * element size is one of the two.
-bool encode_3d(CUtensorMap *m, const void *base, bool f32, long long planes, long long rows, long long cols, int box_cols,
-               int box_rows) {
+// [planes, rows, cols] bf16 (or fp32) with a box of box_rows rows of 64 bytes in one plane, which land
+// swizzled by as much.
+bool encode_3d(CUtensorMap *m, const void *base, bool f32, long long planes, long long rows, long long cols, int box_rows) {
     auto enc = get_encode();
     if (!enc) return false;
     const int es = f32 ? 4 : 2;
     const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
     const cuuint64_t strides[2] = {(cuuint64_t)cols * es, (cuuint64_t)cols * es * rows};
-    const cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
+    const cuuint32_t box[3] = {(cuuint32_t)(64 / es), (cuuint32_t)box_rows, 1};
     const cuuint32_t one[3] = {1, 1, 1};
     return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims,
-               strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               box_cols * es == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+               strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // A [B, n, n, 64] bf16 pair tensor as 4-D (c, j, i, b) with a box of 4 rows i

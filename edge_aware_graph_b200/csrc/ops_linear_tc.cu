@@ -19,7 +19,7 @@
 //
 // Epilogue: a lane holds a row; bias, activation, slope and residual work on
 // registers; residual and Zin come, and the outputs go, by TMA through one small
-// swizzled tile a warp and tensor, so global memory sees whole rows of 64 or 128
+// swizzled tile a warp and tensor, so global memory sees whole rows of 64
 // bytes.  Every output is rounded once.  Outputs whose rows do not begin on 16
 // bytes (VEC = false) take a plain path.
 //
@@ -55,8 +55,7 @@ namespace eaga {
 namespace fast {
 bool encode_2d(CUtensorMap *m, const void *base, int rows, int cols, int box_rows);
 bool encode_blocks(CUtensorMap *m, const void *base, int rows, int cols, int blocks);
-bool encode_3d(CUtensorMap *m, const void *base, bool f32, long long planes, long long rows, long long cols, int box_cols,
-               int box_rows);
+bool encode_3d(CUtensorMap *m, const void *base, bool f32, long long planes, long long rows, long long cols, int box_rows);
 }
 namespace ops {
 
@@ -759,9 +758,8 @@ static bool lt_encode(CUtensorMap (&m)[3], const bf16 *const (&base)[3], long lo
 }
 // The maps of the outputs and the epilogue's inputs, a warp's piece at a time.
 template <typename TO>
-static bool lt_encode_out(LtMaps &m, const LinTile &t, const LinEpi<TO> &e, long long planes, long long M, int N) {
-    const int pc = 64 / (int)sizeof(TO);
-    auto enc = [&](CUtensorMap *x, const void *base) { return !base || fast::encode_3d(x, base, sizeof(TO) == 4, planes, M, N, pc, 32); };
+static bool lt_encode_out(LtMaps &m, const LinEpi<TO> &e, long long planes, long long M, int N) {
+    auto enc = [&](CUtensorMap *x, const void *base) { return !base || fast::encode_3d(x, base, sizeof(TO) == 4, planes, M, N, 32); };
     return enc(&m.out, e.out) && enc(&m.out2, e.out2) && enc(&m.add, e.add) && enc(&m.zin, e.zin);
 }
 
@@ -798,7 +796,7 @@ static cudaError_t lt_product(const LinTc &q, const LinSplit &sp, const LinEpi<T
     else ok = lt_encode(m.a, q.X, q.rows, q.ldx, 64, p.ablocks) && lt_encode(m.b, q.dZ, q.rows, q.ldz, 64, p.bblocks);
     if (!ok) return cudaErrorInvalidValue;
     if ((long long)N * sizeof(T) % 16) return lt_run<KIND, T, false>(sp.tile, m, p, st);
-    if (!lt_encode_out<T>(m, sp.tile, e, sp.splits, M, N)) return cudaErrorInvalidValue;
+    if (!lt_encode_out<T>(m, e, sp.splits, M, N)) return cudaErrorInvalidValue;
     return lt_run<KIND, T, true>(sp.tile, m, p, st);
 }
 template <typename T>

@@ -13,6 +13,7 @@
 // of all parts that count (six of nine), dX in bf16 the upper two parts of dZ (16
 // bits: the rest is 2^-8 of the result's own rounding).
 #include <algorithm>
+#include <cstdio>
 #include "ops_linear.h"
 
 namespace eaga {
@@ -449,6 +450,26 @@ static cudaError_t forward_vec(const eaga_linear_dims &d, const void *X, const v
     return lin_vec_forward<T>(q, e, st);
 }
 
+// The forward's, dX's or dW's kernel by name.
+static int lin_form(const eaga_linear_dims &d, int kind, char *to, size_t bytes) {
+    const LinPlan p = lin_plan(d, kind != LIN_FWD);
+    const bool f32 = d.dtype == EAGA_FP32;
+    if (p.vec) return snprintf(to, bytes, "rows %d%s", lin_vec_rows((int)d.rows), lin_vec_wide(d.out, d.dtype) ? " wide" : "");
+    const long long M = kind == LIN_DW ? d.in : d.rows, K = kind == LIN_FWD ? d.in : kind == LIN_DX ? d.out : d.rows;
+    const int N = kind == LIN_DX ? d.in : d.out;
+    if (p.cores) {
+        static const char *const names[] = {"warps 4", "warps 2", "128x16", "128x32", "64x64", "32x32", "thin"};
+        const int splits = kind == LIN_DW ? p.dw.splits : 1;
+        return snprintf(to, bytes, "cores %s%s", names[lin_f32_form(kind, M, N, K, splits)], splits > 1 ? " split" : "");
+    }
+    const LinSplit &s = kind == LIN_FWD ? p.fwd : kind == LIN_DX ? p.dx : p.dw;
+    uint8_t seg[6];
+    const int z = std::max(1, p.zparts), nseg = f32 ? 6 : kind == LIN_FWD ? 1 : kind == LIN_DX ? std::min(z, 2) : products(1, z, seg);
+    const LtForm t = lin_tc_form(kind, s, f32 || kind == LIN_DW || s.splits > 1, M, N, K, nseg);
+    const char *tile = t.tile.pair ? "pair" : t.tile.bn == 128 ? "128" : t.two ? "64 two" : "64";
+    return snprintf(to, bytes, "tc %s%s%s%s", tile, t.tma ? " tma" : "", t.promo ? " promoted" : "", s.splits > 1 ? " split" : "");
+}
+
 }  // namespace ops
 }  // namespace eaga
 
@@ -460,6 +481,14 @@ extern "C" {
 size_t eaga_linear_workspace_size(const eaga_linear_dims *d, int for_backward) {
     if (lin_check(d) != EAGA_OK) return 0;
     return lin_plan(*d, for_backward != 0).total;
+}
+
+eaga_status eaga_linear_form(const eaga_linear_dims *d, int product, char *form, size_t bytes) {
+    const eaga_status s = lin_check(d);
+    if (s != EAGA_OK) return s;
+    if (product < LIN_FWD || product > LIN_DW || !form) return EAGA_ERR_INVALID_ARG;
+    const int n = d->rows ? lin_form(*d, product, form, bytes) : snprintf(form, bytes, "none");
+    return n >= 0 && (size_t)n < bytes ? EAGA_OK : EAGA_ERR_WORKSPACE;
 }
 
 eaga_status eaga_linear_forward(const eaga_linear_dims *d, const void *X, const void *W, const void *b, const void *R,

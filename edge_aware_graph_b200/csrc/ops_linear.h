@@ -211,6 +211,14 @@ struct LinTc {
 };
 // Of a product [M, K] x [K, N]; f32: of fp32 operands and tensors in the epilogue.  us: the estimated time, where not null.
 LinSplit lin_tc_split(long long M, int N, long long K, int nseg, bool f32, double *us = nullptr);
+// The kernel of such a product: its tile, whether outputs go by TMA (rows of whole 16 bytes), two CTAs an SM, sums that leave the
+// accumulator on the way; and its units, tiles times splits.  kind: LinKind; f32: of an fp32 result (a split one is).
+struct LtForm {
+    LinTile tile;
+    bool tma, two, promo;
+    long long units;
+};
+LtForm lin_tc_form(int kind, const LinSplit &s, bool f32, long long M, int N, long long K, int nseg);
 // With one split the finished outputs; with more e.out takes the splits' sums [splits][M][N] in fp32, and nothing else of e is there.
 template <typename T>
 cudaError_t lin_tc_forward(const LinTc &p, const LinSplit &s, const LinEpi<T> &e, cudaStream_t st);
@@ -235,6 +243,9 @@ inline bool lin_narrow(long long M, int N, long long K) {
     if (N > 32 || K < 64) return false;
     return M < 512LL * sm_count() || (N + 7) / 8 * 8 * (K + 80) / 17e6 < (N <= 16 ? 16 : 32) * K / lin_tile_rate(N);
 }
+// The kernel of a product on the CUDA cores: by warps with four or two steps in flight, tiles, or rows in registers (narrow dW).
+enum LfForm { LF_WARPS4, LF_WARPS2, LF_128x16, LF_128x32, LF_64x64, LF_32x32, LF_THIN };
+LfForm lin_f32_form(int kind, long long M, int N, long long K, int splits);
 cudaError_t lin_f32_forward(const LinF32 &p, const LinEpi<float> &e, cudaStream_t st);
 cudaError_t lin_f32_dx(const LinF32 &p, const LinEpi<float> &e, cudaStream_t st);
 LinSplit lin_f32_dw_split(long long rows, int in, int out);
@@ -259,6 +270,9 @@ struct LinVec {
     float *dW, *db;
     int *status;               // cleared
 };
+// Rows such a kernel is made for, and whether it reads W 16 bytes at a time.
+inline int lin_vec_rows(int rows) { return rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : rows <= 8 ? 8 : 16; }
+inline bool lin_vec_wide(int out, int dtype) { return out % (dtype == EAGA_BF16 ? 8 : 4) == 0; }
 template <typename T>
 cudaError_t lin_vec_forward(const LinVec<T> &p, const LinEpi<T> &e, cudaStream_t st);
 template <typename T>

@@ -300,26 +300,35 @@ __global__ void __launch_bounds__(256) k_lin_thin_dw(const LtThin p) {
 static bool lf_thin(int in, int out) { return in <= 32 && out <= 32 && ((in + 7) / 8) * ((out + 7) / 8) <= 8; }
 
 // Narrow results by warps where lin_narrow() says so, else tiles: 64 x 64; narrow results of many rows 128 x 16 or 128 x 32; 32 x 32 where others leave SMs without one.
+static long long lf_tiles(long long M, int N, int bm, int bn) { return (M + bm - 1) / bm * ((N + bn - 1) / bn); }
+LfForm lin_f32_form(int kind, long long M, int N, long long K, int splits) {
+    if (kind == LIN_DW && lf_thin((int)M, N)) return LF_THIN;
+    if (kind != LIN_DW) {
+        if (lin_narrow(M, N, K)) return K < 256 ? LF_WARPS2 : LF_WARPS4;
+        if (N <= 16 && lf_tiles(M, N, 128, 16) >= 2 * sm_count()) return LF_128x16;
+        if (N <= 32 && lf_tiles(M, N, 128, 32) >= 2 * sm_count()) return LF_128x32;
+    }
+    return N > 32 && M > 32 && lf_tiles(M, N, 64, 64) * splits >= sm_count() ? LF_64x64 : LF_32x32;
+}
 template <int KIND>
 static cudaError_t lf_launch(const LfParams &p, int splits, cudaStream_t st) {
-    auto tiles = [&](int bm, int bn) { return ((long long)p.M + bm - 1) / bm * ((p.N + bn - 1) / bn); };
     auto go = [&](auto kernel, int bm, int bn) {
-        const long long n = tiles(bm, bn);
+        const long long n = lf_tiles(p.M, p.N, bm, bn);
         if (n > 0x7fffffffLL) return cudaErrorInvalidValue;
         return launch_pdl(kernel, dim3((unsigned)n, splits), dim3(256), 0, st, 1, p);
     };
+    const LfForm form = lin_f32_form(KIND, p.M, p.N, p.K, splits);
     if constexpr (KIND != LIN_DW) {
-        if (lin_narrow(p.M, p.N, p.K)) {
-            const bool brief = p.K < 256;
+        if (form == LF_WARPS2 || form == LF_WARPS4) {
+            const bool brief = form == LF_WARPS2;
             const long long blocks = (p.N + 7) / 8, rows = ((long long)p.M + 8 * LN_R - 1) / (8 * LN_R);
             const dim3 grid((unsigned)(std::min(rows, std::max(1LL, (brief ? 4LL : 3LL) * sm_count() / blocks)) * blocks));
             return brief ? launch_pdl(k_lin_narrow<KIND, 2>, grid, dim3(256), 0, st, 1, p) : launch_pdl(k_lin_narrow<KIND, 4>, grid, dim3(256), 0, st, 1, p);
         }
-        if (p.N <= 16 && tiles(128, 16) >= 2 * sm_count()) return go(k_lin_f32<KIND, 128, 16>, 128, 16);
-        if (p.N <= 32 && tiles(128, 32) >= 2 * sm_count()) return go(k_lin_f32<KIND, 128, 32>, 128, 32);
+        if (form == LF_128x16) return go(k_lin_f32<KIND, 128, 16>, 128, 16);
+        if (form == LF_128x32) return go(k_lin_f32<KIND, 128, 32>, 128, 32);
     }
-    if (p.N > 32 && p.M > 32 && tiles(64, 64) * splits >= sm_count()) return go(k_lin_f32<KIND, 64, 64>, 64, 64);
-    return go(k_lin_f32<KIND, 32, 32>, 32, 32);
+    return form == LF_64x64 ? go(k_lin_f32<KIND, 64, 64>, 64, 64) : go(k_lin_f32<KIND, 32, 32>, 32, 32);
 }
 
 cudaError_t lin_f32_forward(const LinF32 &q, const LinEpi<float> &e, cudaStream_t st) {

@@ -687,21 +687,31 @@ static cudaError_t lt_launch(const LtMaps &m, const LtParams<TO> &p, cudaStream_
     if (cudaError_t e = ensure_smem_attr(kernel, S::BYTES, attr_set); e != cudaSuccess) return e;
     return launch_pdl(kernel, dim3((unsigned)(std::min(p.units, PER * sm_count() / CG) * CG)), dim3(S::THR), S::BYTES, st, CG, m, p);
 }
-template <int KIND, int BN, int CG, typename TO, bool VEC>
-static cudaError_t lt_sums(const LtMaps &m, const LtParams<TO> &p, cudaStream_t st) {
-    if constexpr (KIND != LIN_DW && sizeof(TO) == 2) {
-        if (std::min(p.per, p.kts) * p.nseg <= lt_promo<TO>()) return lt_launch<KIND, BN, CG, TO, VEC, 1, false>(m, p, st);
-    }
-    return lt_launch<KIND, BN, CG, TO, VEC, 1, true>(m, p, st);
+template <int KIND, typename TO, bool VEC, bool PROMO>
+static cudaError_t lt_tiles(const LinTile &t, const LtMaps &m, const LtParams<TO> &p, cudaStream_t st) {
+    if (t.pair) return lt_launch<KIND, 256, 2, TO, VEC, 1, PROMO>(m, p, st);
+    return t.bn == 128 ? lt_launch<KIND, 128, 1, TO, VEC, 1, PROMO>(m, p, st) : lt_launch<KIND, 64, 1, TO, VEC, 1, PROMO>(m, p, st);
 }
 template <int KIND, typename TO, bool VEC>
-static cudaError_t lt_run(const LinTile &t, const LtMaps &m, const LtParams<TO> &p, cudaStream_t st) {
-    if (t.pair) return lt_sums<KIND, 256, 2, TO, VEC>(m, p, st);
-    if (t.bn == 128) return lt_sums<KIND, 128, 1, TO, VEC>(m, p, st);
-    if constexpr (VEC && KIND != LIN_DW && sizeof(TO) == 2) {          // (an fp32 result has six products a step, or splits of more steps)
-        if (p.units >= 4 * sm_count() && p.per * p.nseg <= 4) return lt_launch<KIND, 64, 1, TO, VEC, 2, false>(m, p, st);
+static cudaError_t lt_run(const LtForm &f, const LtMaps &m, const LtParams<TO> &p, cudaStream_t st) {
+    if constexpr (KIND != LIN_DW && sizeof(TO) == 2) {
+        if constexpr (VEC) {
+            if (f.two) return lt_launch<KIND, 64, 1, TO, VEC, 2, false>(m, p, st);
+        }
+        if (!f.promo) return lt_tiles<KIND, TO, VEC, false>(f.tile, m, p, st);
     }
-    return lt_sums<KIND, 64, 1, TO, VEC>(m, p, st);
+    return lt_tiles<KIND, TO, VEC, true>(f.tile, m, p, st);
+}
+// (An fp32 result has six products a step, or splits of more steps than `two` is for.)
+LtForm lin_tc_form(int kind, const LinSplit &s, bool f32, long long M, int N, long long K, int nseg) {
+    const int bm = s.tile.pair ? 2 * LT_BM : LT_BM;
+    LtForm f = {s.tile, (long long)N * (f32 ? 4 : 2) % 16 == 0, false, true, (M + bm - 1) / bm * ((N + s.tile.bn - 1) / s.tile.bn) * s.splits};
+    const long long steps = std::min(s.chunk / LT_BK, (K + LT_BK - 1) / LT_BK) * nseg;     // of a unit, the longest
+    if (kind != LIN_DW && !f32) {
+        f.two = f.tma && !s.tile.pair && s.tile.bn == 64 && f.units >= 4 * sm_count() && steps <= 4;
+        f.promo = steps > lt_promo<bf16>();
+    }
+    return f;
 }
 
 // Tiles and splits: the least of an estimate of each form's time.  The unit is a 64-deep step of a pair's tile,
@@ -776,9 +786,9 @@ static cudaError_t lt_product(const LinTc &q, const LinSplit &sp, const LinEpi<T
     const int bm = sp.tile.pair ? 2 * LT_BM : LT_BM;
     p.tiles_m = (int)((M + bm - 1) / bm);
     p.tiles_n = (N + sp.tile.bn - 1) / sp.tile.bn;
-    const long long units = (long long)p.tiles_m * p.tiles_n * sp.splits;
-    if (units > 0x7fffffffLL) return cudaErrorInvalidValue;
-    p.units = (int)units;
+    const LtForm form = lin_tc_form(KIND, sp, sizeof(T) == 4, M, N, K, q.nseg);
+    if (form.units > 0x7fffffffLL) return cudaErrorInvalidValue;
+    p.units = (int)form.units;
     p.kts = (int)((K + LT_BK - 1) / LT_BK);
     p.per = (int)(sp.chunk / LT_BK);
     p.e = e;
@@ -795,9 +805,9 @@ static cudaError_t lt_product(const LinTc &q, const LinSplit &sp, const LinEpi<T
     else if (KIND == LIN_DX) ok = lt_encode(m.a, q.dZ, q.rows, q.ldz, LT_BM) && lt_encode(m.b, q.W, q.in, q.ldw, sp.tile.pair ? 128 : sp.tile.bn);
     else ok = lt_encode(m.a, q.X, q.rows, q.ldx, 64, p.ablocks) && lt_encode(m.b, q.dZ, q.rows, q.ldz, 64, p.bblocks);
     if (!ok) return cudaErrorInvalidValue;
-    if ((long long)N * sizeof(T) % 16) return lt_run<KIND, T, false>(sp.tile, m, p, st);
+    if (!form.tma) return lt_run<KIND, T, false>(form, m, p, st);
     if (!lt_encode_out<T>(m, e, sp.splits, M, N)) return cudaErrorInvalidValue;
-    return lt_run<KIND, T, true>(sp.tile, m, p, st);
+    return lt_run<KIND, T, true>(form, m, p, st);
 }
 template <typename T>
 cudaError_t lin_tc_forward(const LinTc &q, const LinSplit &s, const LinEpi<T> &e, cudaStream_t st) {

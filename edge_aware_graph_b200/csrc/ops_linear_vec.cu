@@ -255,17 +255,18 @@ static cudaError_t vec_bwd(const LinVec<T> &p, const LinEpi<T> &e, cudaStream_t 
 
 template <typename T, typename F>
 static cudaError_t vec_pick(int rows, int out, F &&f) {
-    constexpr int W = 16 / sizeof(T);
     auto go = [&](auto vec) {
-        if (rows <= 1) return f(vec, std::integral_constant<int, 1>{});
-        if (rows <= 2) return f(vec, std::integral_constant<int, 2>{});
-        if (rows <= 4) return f(vec, std::integral_constant<int, 4>{});
-        if constexpr (sizeof(T) == 4) {
-            if (rows > 8) return f(vec, std::integral_constant<int, 16>{});
+        switch (lin_vec_rows(rows)) {
+            case 1: return f(vec, std::integral_constant<int, 1>{});
+            case 2: return f(vec, std::integral_constant<int, 2>{});
+            case 4: return f(vec, std::integral_constant<int, 4>{});
+            case 8: return f(vec, std::integral_constant<int, 8>{});
         }
-        return f(vec, std::integral_constant<int, 8>{});
+        if constexpr (sizeof(T) == 4) return f(vec, std::integral_constant<int, 16>{});
+        return cudaErrorInvalidValue;
     };
-    return out % W == 0 ? go(std::integral_constant<int, W>{}) : go(std::integral_constant<int, 1>{});
+    return lin_vec_wide(out, sizeof(T) == 4 ? EAGA_FP32 : EAGA_BF16) ? go(std::integral_constant<int, 16 / sizeof(T)>{})
+                                                                     : go(std::integral_constant<int, 1>{});
 }
 
 template <typename T>

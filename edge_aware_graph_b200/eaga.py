@@ -25,7 +25,7 @@ EXPORTED = ("eaga_workspace_size", "eaga_saved_size", "eaga_forward", "eaga_back
             "eaga_forward_variant", "eaga_backward_variant", "eaga_forward_rows", "eaga_backward_rows",
             "eaga_block_saved_size", "eaga_block_workspace_size", "eaga_block_kernel_launches",
             "eaga_block_forward", "eaga_block_backward",
-            "eaga_linear_workspace_size", "eaga_linear_forward", "eaga_linear_backward",
+            "eaga_linear_workspace_size", "eaga_linear_form", "eaga_linear_forward", "eaga_linear_backward",
             "eaga_residual_norm_workspace_size", "eaga_residual_norm_forward", "eaga_residual_norm_backward",
             "eaga_adamw_step", "eaga_adamw_unpack")
 # parameters of the graph-transformer block (eaga_block_weights field order)
@@ -140,6 +140,8 @@ def lib():
         LD_ = ctypes.POINTER(LinearDims)
         L.eaga_linear_workspace_size.argtypes = [LD_, i32]
         L.eaga_linear_workspace_size.restype = sz
+        L.eaga_linear_form.argtypes = [LD_, i32, ctypes.c_char_p, sz]
+        L.eaga_linear_form.restype = i32
         L.eaga_linear_forward.argtypes = [LD_] + [vp] * 7 + [sz, vp]
         L.eaga_linear_forward.restype = i32
         L.eaga_linear_backward.argtypes = [LD_] + [vp] * 4 + [i32] + [vp] * 6 + [sz, vp]
@@ -403,6 +405,15 @@ def linear_dims(rows, in_, out, act="none", dtype="bf16") -> LinearDims:
 
 def linear_workspace_size(d: LinearDims, for_backward: bool) -> int:
     return int(lib().eaga_linear_workspace_size(ctypes.byref(d), int(bool(for_backward))))
+
+
+def linear_form(d: LinearDims, product: str) -> str:
+    """The kernel that a call's product ("Y", "dX" or "dW") runs in, by name (eaga_linear_form)."""
+    form = ctypes.create_string_buffer(64)
+    rc = lib().eaga_linear_form(ctypes.byref(d), _code(product, {"Y": 0, "dX": 1, "dW": 2}, "product"), form, len(form))
+    if rc:
+        raise EagaError(rc, "eaga_linear_form")
+    return form.value.decode()
 
 
 def linear_forward(d: LinearDims, X, W, b, R, Y, Z, workspace, stream=None):

@@ -411,6 +411,11 @@ typedef struct {
  * 0 for invalid or unsupported dims.  Starts with the status word that
  * eaga_get_device_status reads. */
 EAGA_API size_t eaga_linear_workspace_size(const eaga_linear_dims *dims, int for_backward);
+/* The name of the kernel that a product (0: Y, 1: dX, 2: dW) of such a call runs in on the
+ * current device, for tests and profiles: "rows ..." a few rows, "cores ..." fp32 on the CUDA
+ * cores, "tc ..." tcgen05 ("pair", "128" or "64" columns a tile; "tma" outputs; "two" CTAs
+ * an SM; "promoted" sums), "split" its reduction, "none" without rows. */
+EAGA_API eaga_status eaga_linear_form(const eaga_linear_dims *dims, int product, char *form, size_t bytes);
 EAGA_API eaga_status eaga_linear_forward(const eaga_linear_dims *dims, const void *X, const void *W, const void *b,
                                 const void *R, void *Y, void *Z, void *workspace, size_t ws_bytes, void *stream);
 EAGA_API eaga_status eaga_linear_backward(const eaga_linear_dims *dims, const void *X, const void *W, const void *Z,

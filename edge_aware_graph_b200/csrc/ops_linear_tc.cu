@@ -689,7 +689,7 @@ static cudaError_t lt_launch(const LtMaps &m, const LtParams<TO> &p, cudaStream_
 }
 template <int KIND, typename TO, bool VEC, bool PROMO>
 static cudaError_t lt_tiles(const LinTile &t, const LtMaps &m, const LtParams<TO> &p, cudaStream_t st) {
-    if (t.pair) return lt_launch<KIND, 256, 2, TO, VEC, 1, PROMO>(m, p, st);
+    if (t.pair) return lt_launch<KIND, 256, 2, TO, VEC, 1, true>(m, p, st);
     return t.bn == 128 ? lt_launch<KIND, 128, 1, TO, VEC, 1, PROMO>(m, p, st) : lt_launch<KIND, 64, 1, TO, VEC, 1, PROMO>(m, p, st);
 }
 template <int KIND, typename TO, bool VEC>
@@ -702,14 +702,15 @@ static cudaError_t lt_run(const LtForm &f, const LtMaps &m, const LtParams<TO> &
     }
     return lt_tiles<KIND, TO, VEC, true>(f.tile, m, p, st);
 }
-// (An fp32 result has six products a step, or splits of more steps than `two` is for.)
+// (An fp32 result has six products a step, or splits of more steps than `two` is for; pairs are chosen for longer reductions
+// than one stretch: their epilogue is as long as 40 steps.)
 LtForm lin_tc_form(int kind, const LinSplit &s, bool f32, long long M, int N, long long K, int nseg) {
     const int bm = s.tile.pair ? 2 * LT_BM : LT_BM;
     LtForm f = {s.tile, (long long)N * (f32 ? 4 : 2) % 16 == 0, false, true, (M + bm - 1) / bm * ((N + s.tile.bn - 1) / s.tile.bn) * s.splits};
     const long long steps = std::min(s.chunk / LT_BK, (K + LT_BK - 1) / LT_BK) * nseg;     // of a unit, the longest
     if (kind != LIN_DW && !f32) {
         f.two = f.tma && !s.tile.pair && s.tile.bn == 64 && f.units >= 4 * sm_count() && steps <= 4;
-        f.promo = steps > lt_promo<bf16>();
+        f.promo = s.tile.pair || steps > lt_promo<bf16>();
     }
     return f;
 }

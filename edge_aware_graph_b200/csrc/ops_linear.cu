@@ -32,12 +32,20 @@ struct PrepArgs {
     PrepJob job[3];
 };
 
-// A value's bf16 part and what it leaves.  Of an infinity or a NaN nothing is left: the first part says it all.  A finite
-// value above bf16's largest gives that.
-__device__ __forceinline__ float take_part(float &v) {
+// A value's bf16 part number k (0, 1, 2, in turn), and what it leaves in v.  Of an infinity or a NaN nothing is left: the first part says
+// it all.  A finite value above bf16's largest gives that, and where the first part is that one, the second is cut off, not rounded: no sum
+// of parts is larger than the value, so the type's lowest value, with which masks are filled, times one stays finite.  (The third is exact.)
+__device__ __forceinline__ float take_part(float &v, int k, float &first) {
     float hi = __bfloat162float(__float2bfloat16_rn(v));
-    if (isinf(hi)) hi = __uint_as_float(__float_as_uint(v) & 0xffff0000u);
-    v = isfinite(hi) ? v - hi : 0.f;
+    const float cut = __uint_as_float(__float_as_uint(v) & 0xffff0000u);
+    if (k == 0) {
+        if (isinf(hi)) hi = cut;
+        v = isfinite(hi) ? v - hi : 0.f;
+        first = fabsf(hi);
+    } else {
+        if (k == 1 && first == __uint_as_float(0x7f7f0000u)) hi = cut;
+        v -= hi;
+    }
     return hi;
 }
 
@@ -96,10 +104,13 @@ __global__ void __launch_bounds__(256) k_lin_prep(const __grid_constant__ PrepAr
             act_slope_mul<T>(v, z, j.act);
         }
         if (j.f32) lin_st8(j.f32 + row * j.n + c, have, j.n % 4 == 0, v);
-        for (int k = 0; k < j.parts; ++k) {
+        float first[8];
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            if (k >= j.parts) break;
             float o[8];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) o[u] = take_part(v[u]);
+            for (int u = 0; u < 8; ++u) o[u] = take_part(v[u], k, first[u]);
             lin_st8(static_cast<__nv_bfloat16 *>(j.dst[k]) + (size_t)row * j.ld + c, 8, true, o);
         }
     }

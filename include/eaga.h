@@ -393,8 +393,10 @@ EAGA_API eaga_status eaga_block_backward(const eaga_dims *dims,
  *
  * In fp32 all but narrow products run on the tensor cores over three bf16 parts of each
  * operand (24 bits, down to 2^-133), the error that of fp32 sums.  An infinite
- * operand there, or one whose product with a part overflows, gives NaN where an
- * fp32 product might give an infinity; finite rows are not touched by it.
+ * operand there gives NaN where an fp32 product gives an infinity, and a product within 2^-7 of
+ * the type's largest value may overflow (times a power of two it does not); the sums that
+ * neither enters are not touched by it.  With act given, a bf16 backward takes dZ (fp32, not
+ * rounded to bf16) as two such parts for dX, 16 bits of it, and as three for dW and db.
  *
  * Limits: in, out <= 65536, rows <= 2147418112.  rows = 0 is a call that
  * writes no row (and zero dW, db).  Any size; rows of X, W and dZ that are not

@@ -103,3 +103,46 @@ def test_gelu_in_fp32_is_right_in_its_relative_error(rows, i, o):
     dX, _, _ = backward(None, torch.ones(i, o, device="cuda"), dY.cuda(), act_in="gelu", Zin=Zin.cuda(), dw=False, dtype="fp32")
     off = (dX.cpu().double() - slope[:, :1]).abs()
     assert (off <= tol[:, :1]).all(), float((off / tol[:, :1]).max())
+
+
+FP32_SHAPES = [(rows, i, o) for dtype, rows, i, o in NAN_SHAPES if dtype == "fp32"] + [(200, 2048, 264), (777, 2200, 1030)]
+
+
+@pytest.mark.parametrize("rows,i,o", FP32_SHAPES)
+def test_infinities_in_fp32_stay_in_their_rows(rows, i, o):
+    """In every form: the sums that an infinity, or a product beyond the type, enters are infinite or NaN, the others the same bits as without it."""
+    g = torch.Generator(device="cuda").manual_seed(rows + o)
+    new = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    X, W, b, dY, R = new(rows, i), new(i, o), new(o), new(rows, o), new(rows, o)
+    W[W == 0] = 1
+    W[3] = W[3].sign() * (2 + W[3].abs())
+    Y0, Z0 = forward(X, W, b, R, dtype="fp32")
+    d0 = backward(X, W, dY, dtype="fp32")
+    for v in (float("inf"), float("-inf"), 3e38):
+        Xv, dYv = X.clone(), dY.clone()
+        Xv[1, 3] = v
+        row = torch.arange(rows, device="cuda") == 1
+        for got, clean in zip(forward(Xv, W, b, R, dtype="fp32"), (Y0, Z0)):
+            assert torch.equal(got[~row], clean[~row]) and not torch.isfinite(got[row]).any()
+        dYv[2, 5] = v
+        if abs(v) != float("inf"):
+            continue                                      # (its products with weights and inputs below 1 are finite)
+        dX, dW, dB = backward(X, W, dYv, dtype="fp32")
+        row, col = torch.arange(rows, device="cuda") == 2, torch.arange(o, device="cuda") == 5
+        assert torch.equal(dX[~row], d0[0][~row]) and not torch.isfinite(dX[row]).any()
+        assert torch.equal(dW[:, ~col], d0[1][:, ~col]) and not torch.isfinite(dW[:, col]).any()
+        assert torch.equal(dB[~col], d0[2][~col]) and not torch.isfinite(dB[col]).any()
+
+
+@pytest.mark.parametrize("rows,i,o", FP32_SHAPES)
+def test_the_largest_and_smallest_numbers_in_fp32(rows, i, o):
+    """The type's lowest and largest values, as masks hold them, and tiny ones: one product a sum, by a power of two, is exact
+    (the third part of a value of 2^-100 still has 9 bits above 2^-133)."""
+    top = torch.finfo(torch.float32).max
+    values = torch.tensor([top, -top, top * (1 - 2.0 ** -10), 2.0 ** -100 * (1 + 2.0 ** -23), -(2.0 ** -90) * (2 - 2.0 ** -23), 1 + 2.0 ** -23, -0.0])
+    z = values[torch.arange(rows) % len(values)]
+    X = torch.zeros(rows, i)
+    X[torch.arange(rows), torch.arange(rows) % i] = z
+    W = torch.tensor([0.5, -1.0, 0.125])[torch.arange(o) % 3].expand(i, o).contiguous()
+    Y, _ = forward(X.cuda(), W.cuda(), dtype="fp32")
+    assert torch.equal(Y.cpu().double(), z.double()[:, None] * W[:1].double())

@@ -610,22 +610,30 @@ k_lin_tc(const __grid_constant__ LtMaps maps, const __grid_constant__ LtParams<T
                                     if (row0 + r0 + j < p.M) ad[j] = p.e.add[at + (size_t)j * p.N];
                             }
                             TO *o = p.e.out + (size_t)t.split * p.M * p.N + at;
+                            float y[16];            // the rows of one column: the activation's code once for all
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                y[j] = *reinterpret_cast<const float *>(slots_p + fast::sw128(r0 + j, lane >> 2) + 4 * (lane & 3)) + bias;
+                            if constexpr (KIND == LIN_FWD) {
+                                if (p.e.out2) {
+#pragma unroll
+                                    for (int j = 0; j < 16; ++j)
+                                        if (row0 + r0 + j < p.M) stf(p.e.out2 + at + (size_t)j * p.N, y[j]);
+                                }
+                                act_apply<TO>(y, p.e.act);
+                            } else if constexpr (KIND == LIN_DX) {
+                                if (p.e.zin) {
+                                    float z[16];
+#pragma unroll
+                                    for (int j = 0; j < 16; ++j) z[j] = row0 + r0 + j < p.M ? ldf(&zi[j]) : 0.f;
+                                    act_slope_mul<TO>(y, z, p.e.act);
+                                }
+                            }
 #pragma unroll
                             for (int j = 0; j < 16; ++j) {
                                 if (row0 + r0 + j >= p.M) break;
-                                float y[1] = {*reinterpret_cast<const float *>(slots_p + fast::sw128(r0 + j, lane >> 2) + 4 * (lane & 3))};
-                                if constexpr (KIND == LIN_FWD) {
-                                    y[0] += bias;
-                                    if (p.e.out2) stf(p.e.out2 + at + (size_t)j * p.N, y[0]);
-                                    act_apply<TO>(y, p.e.act);
-                                } else if constexpr (KIND == LIN_DX) {
-                                    if (p.e.zin) {
-                                        const float z[1] = {ldf(&zi[j])};
-                                        act_slope_mul<TO>(y, z, p.e.act);
-                                    }
-                                }
-                                if (KIND != LIN_DW && p.e.add) y[0] += ldf(&ad[j]);
-                                stf(o + (size_t)j * p.N, y[0]);
+                                if (KIND != LIN_DW && p.e.add) y[j] += ldf(&ad[j]);
+                                stf(o + (size_t)j * p.N, y[j]);
                             }
                         }
                     }

@@ -94,9 +94,11 @@ k_lin_f32(const LfParams p) {
 #pragma unroll
                 for (int j = 0; j < TN; ++j) acc[i][j] += x[i] * y[j];
         }
-        if (sums && tid < BN) {
+        if (sums && tid < BN) {                      // 16 rows by themselves: a shorter chain of additions to a large sum
+            float part = 0.f;
 #pragma unroll
-            for (int kk = 0; kk < LF_BK; ++kk) col += sb[b][kk][tid];
+            for (int kk = 0; kk < LF_BK; ++kk) part += sb[b][kk][tid];
+            col += part;
         }
         if (more) keep(b ^ 1);
         __syncthreads();

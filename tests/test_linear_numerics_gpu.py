@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+from edge_aware_graph_b200 import eaga
 from test_linear_gpu import backward, forward
 
 pytestmark = pytest.mark.gpu
@@ -146,3 +147,16 @@ def test_the_largest_and_smallest_numbers_in_fp32(rows, i, o):
     W = torch.tensor([0.5, -1.0, 0.125])[torch.arange(o) % 3].expand(i, o).contiguous()
     Y, _ = forward(X.cuda(), W.cuda(), dtype="fp32")
     assert torch.equal(Y.cpu().double(), z.double()[:, None] * W[:1].double())
+
+
+@pytest.mark.parametrize("rows,i,o", [(23_661, 2376, 8), (40_000, 1500, 10), (26_000, 2376, 5)])
+def test_bias_gradients_in_fp32_are_summed_in_short_chains(rows, i, o):
+    """Equal positive values, whose roundings to a sum beyond 1024 all go one way.  A sum takes 16 rows by themselves (16 additions), then at most 2048 / 16
+    such sums of its part of the rows, then at most 128 parts in eights (16 + 8): each off by half a step (2^-24) of the whole."""
+    parts = eaga.linear_form(eaga.linear_dims(rows, i, o, "none", "fp32"), "dW")
+    assert parts == "cores 32x32 split" or parts == "cores 64x64 split"
+    dY = torch.full((rows, o), 1 + 0.49 * 2.0 ** -13, device="cuda")
+    X, W = torch.zeros(rows, i, device="cuda"), torch.zeros(i, o, device="cuda")
+    _, _, dB = backward(X, W, dY, dtype="fp32")
+    exact = rows * dY[0, 0].double()
+    assert ((dB.double() - exact).abs() <= (16 + 2048 / 16 + 24) * 2.0 ** -24 * exact).all(), float((dB.double() / exact - 1).abs().max() * 2 ** 24)

@@ -71,3 +71,25 @@ def test_states_of_other_tensors_leave_the_optimiser_as_it_was():
             assert all(torch.equal(a, b) for a, b in zip(after[name], now[name])), (k, name)
     opt.load_state_dict(good)
     assert opt.steps == 1 and all(torch.equal(a, b) for a, b in zip(opt.m, good["m"]))
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_offsets_beyond_2_31_elements(bits):
+    """One tensor of 2^31 + 4099 elements: its far end takes the same step as a tensor of that end alone, its random bits among it."""
+    n, far = (1 << 31) + 4099, (1 << 31) - 256
+    p, g = torch.zeros(n, dtype=torch.bfloat16, device="cuda"), torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    rng = torch.Generator(device="cuda").manual_seed(2)
+    end = slice(far, n)
+    p[end] = torch.randn(n - far, generator=rng, device="cuda").bfloat16()
+    g[end] = torch.randn(n - far, generator=rng, device="cuda").bfloat16()
+    kw = dict(bits=bits, master=False, weight_decay=0.0, lr=1e-2, seed=3)
+    small_p, small_g = p[end].clone(), g[end].clone()
+    big, small = AdamW([p], [g], counters=[5], **kw), AdamW([small_p], [small_g], counters=[5 + far], **kw)
+    for _ in range(2):
+        big.step()
+        small.step()
+    assert torch.equal(p[end], small_p) and torch.equal(big.m[0][end], small.m[0]) and torch.equal(big.v[0][end], small.v[0])
+    if bits == 8:
+        assert torch.equal(big.m_scale[0][far // 256:], small.m_scale[0]) and torch.equal(big.v_scale[0][far // 256:], small.v_scale[0])
+    for t in (p[:far], big.m[0][:far], big.v[0][:far]):
+        assert int(torch.count_nonzero(t)) == 0

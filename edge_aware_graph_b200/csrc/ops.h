@@ -13,7 +13,8 @@ using fast::launch_pdl;
 // First in the operators' kernels (all are launched with launch_pdl): nothing is read or written before the previous launch is
 // done.  The next launch may become resident before this one is done, so that small kernels follow one another 1 to 2 us sooner:
 // at once behind a few CTAs; behind more only when they are nearly done (before_next), since CTAs that are placed while these
-// compute land unevenly on the SMs (an fp32 product of 160 CTAs took 43 us behind another instead of 16).
+// compute land unevenly on the SMs (an fp32 product of 160 CTAs took 43 us behind another instead of 16).  The first thread of a CTA
+// that gets there signals for the CTA: in k_lin_tc without column sums that is a warp without work, at the start.
 __device__ __forceinline__ void after_previous() {
     if (gridDim.x * gridDim.y <= 32) sm100::griddep_launch_dependents();
     sm100::griddep_wait();

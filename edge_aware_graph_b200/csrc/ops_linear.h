@@ -252,7 +252,7 @@ LinSplit lin_f32_dw_split(long long rows, int in, int out);
 cudaError_t lin_f32_dw(const LinF32 &p, const LinSplit &s, float *dW, float *db, cudaStream_t st);
 
 // Few rows: the weights are read once, bound by memory (at most 8 rows in bf16, 16 in fp32).  Above four rows in bf16 the tensor
-// cores' launch is the shorter one (8 x 4096 -> 4096: 12.8 us against 22.6 forward, 30 against 75 backward; at one row 13.4
+// cores' launch is the shorter one (8 x 4096 -> 4096: 12.6 us against 22.6 forward, 29 against 72 backward; at one row 13.4
 // against 7.6 and 30 against 26), but for rows that they need copied (8 x 1000 -> 1001: 10.2 against 8.4 and 14 against 8.7) and
 // gradients of small weights (8 x 512 -> 512: 9.7 against 5.8).  fp32 products take six of the tensor cores' and three copies
 // (8 x 4096 -> 4096: 75 us against 29).

@@ -25,9 +25,9 @@
 //
 // The tensor cores add with truncation: a chain of n products of 16 is off by up
 // to n steps of fp32, all in one direction (measured 1e-6 relative after 1024
-// rows, 1.9e-5 after 16384, 1.6e-4 after 65536).  The sums therefore leave the accumulator
+// rows, 1.9e-5 after 16384, 3.4e-4 after 65536).  The sums therefore leave the accumulator
 // (PROMO) for sums in registers, rounded to nearest: of fp32 results every 512 steps of
-// the reduction, of bf16 ones every 1024, a drift of 2^-17 at the most and 1e-6 as measured, 2000 times below
+// the reduction, of bf16 ones every 1024, a drift of 2^-17 at the most and 8e-7 as measured, 2000 times below
 // the result's own rounding.  Bf16 results of 8192 x 4096 -> 4096 with gelu, R and Z take 256 us with it, 251 without
 // (265 every 512 steps: a pair's epilogue is then longer than the two accumulators' next products).
 // Reductions of one such stretch go to the epilogue as they are.
